@@ -422,6 +422,192 @@ ck_status ck_hbm_stream(const void* src, int64_t chunks, void* dst, int blocks, 
  */
 ck_status ck_mfma_ceiling(int64_t iters, int mode, int32_t* out, uint32_t seed, hipStream_t stream);
 
+/*
+ * Decode-step operators: what a model served with the int8 layers runs
+ * between its projections.  Together they are one attention block's decode
+ * step: the query/key/value projection (above), ck_qk_norm_rope into a paged
+ * cache, ck_paged_attention over it, and an output projection
+ * (ck_int8_layer, or ck_int4_linear with 4-bit weights).
+ */
+
+/* Element type of activations (16-bit) and of a paged cache. */
+typedef enum {
+    CK_DT_BF16 = 0,
+    CK_DT_FP16 = 1,
+    CK_DT_INT8 = 2     /* caches only: int8 codes with an fp32 scale per row */
+} ck_dtype;
+
+/*
+ * A paged key/value cache of one layer.  Page p, key head h, token t of the
+ * page: `head_dim` consecutive elements at
+ *   k + p * page_stride + h * head_stride + t * token_stride   (elements),
+ * and the same for v, which has the same strides.  In an int8 cache such a
+ * row is codes (-127 .. 127) times the row's scale,
+ *   k_scale[p * scale_page_stride + h * scale_head_stride + t * scale_token_stride]
+ * (v_scale alike), the codes and scale of ck_quantize_int8_rowwise.
+ *
+ * dtype       ck_dtype of the rows; a 16-bit cache has the activations' type.
+ * page_size   tokens per page, a power of two from 1 to 32768.
+ * head_dim    a multiple of 8 from 8 to 512 (attention: 64, 96, 128, 192, 256).
+ * Rows start 16 bytes apart (int8: 8 bytes apart, and 16 for attention):
+ * k, v and the strides times the element size are multiples of that.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;    /* int8 caches only, else NULL */
+    float* v_scale;
+    int64_t pages, page_size, heads, head_dim;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+    int32_t dtype;
+    int32_t reserved;  /* 0 */
+} ck_kv_cache;
+
+/*
+ * Norm and rotation of query and key heads, and the write of keys and values
+ * into a paged cache, in one pass.  For each token t and head (x = its
+ * head_dim values, all arithmetic in fp32, one rounding at the end):
+ *   y = x * w / sqrt(mean(x^2) + eps)    (w = q_weight or k_weight; a NULL
+ *                                         weight skips the norm)
+ *   (y[a], y[b]) -> (y[a] c - y[b] s, y[b] c + y[a] s)  for pair i < rot / 2,
+ *     c = cos_sin[p, i], s = cos_sin[p, rot / 2 + i], p = positions[t],
+ *     a, b = i, i + rot / 2 (interleaved == 0) or 2 i, 2 i + 1 (otherwise);
+ *     elements from rot on are not rotated.
+ * Queries go to q_out; keys to k_out (unless NULL) and to row
+ * (slots[t] / page_size, head, slots[t] % page_size) of the cache (unless
+ * NULL), values unchanged to the same row of v.  An int8 cache quantises the
+ * fp32 values (not their 16-bit rounding).
+ *
+ * q, k, v      [in]  16-bit, element (t, h, i) at q[t * q_token_stride +
+ *                    h * q_head_stride + i] and so on: views of one fused
+ *                    projection's rows are fine.  v NULL only without a cache.
+ *                    hk == 0 (queries alone) takes no k, v and no cache.
+ * positions    [in]  int64 [tokens].  A position outside [0, table_rows) is
+ *                    an error of the token: its q_out and k_out rows become
+ *                    NaN, and the cache is not written.
+ * cos_sin      [in]  fp32 [table_rows, rot], contiguous, 16-B aligned.
+ * q_out, k_out [out] as q and k; may be q and k themselves (same strides).
+ * slots        [in]  int64 [tokens]; a slot outside [0, pages * page_size)
+ *                    (-1, say, for padding) writes nothing to the cache.  Two
+ *                    tokens of a call must not share a slot.
+ * head_dim     a multiple of 8 up to 512; rot a multiple of 16 up to
+ *              head_dim, or 0 (no rotation; positions and cos_sin unused).
+ * Every row must start 16 bytes apart (CK_ERR_UNSUPPORTED otherwise).
+ * Inputs must be finite.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    const int64_t* positions;
+    const float* cos_sin;
+    const float* q_weight;
+    const float* k_weight;
+    void* q_out;
+    void* k_out;
+    const int64_t* slots;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+    int64_t tokens, hq, hk, head_dim, rot, table_rows;
+    float eps;
+    int32_t dtype;          /* CK_DT_BF16 or CK_DT_FP16 */
+    int32_t interleaved;
+    int32_t reserved;       /* 0 */
+} ck_qk_args;
+
+ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipStream_t stream);
+
+/*
+ * Attention of one new token per sequence over a paged cache:
+ *   out[b, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b, h] . k_j - m),
+ * m the largest score, over the visible tokens j of sequence b, of key head
+ * h / (hq / hk).  Visible are j < lens[b], and with window > 0 of those only
+ * the last `window` and the first `sinks`.  Scores, exponentials and sums are
+ * fp32, the products on the matrix cores with p_j in two 16-bit parts (see
+ * the kernel).  A sequence without visible tokens gives zeros.
+ *
+ * q          [in]  16-bit [batch, hq, head_dim], rows at b * q_batch_stride +
+ *                  h * q_head_stride.
+ * cache      [in]  16-bit of q's type, or int8; hq a multiple of its heads.
+ * table      [in]  int32 [batch, table_width], rows table_stride apart: token
+ *                  j of sequence b is token j % page_size of page
+ *                  table[b, j / page_size].
+ * lens       [in]  int32 [batch], on the device; values past
+ *                  table_width * page_size count as that, negative ones as 0.
+ * A visible token whose page is outside [0, pages) is an error of its
+ * sequence, and its output rows are NaN; nothing outside the cache is read.
+ * Cache rows that are not visible are never used, whatever they hold.
+ * workspace  [tmp] device memory of ck_paged_attention_workspace bytes, 256-B
+ *                  aligned, owned by the caller and used by one call at a
+ *                  time; its contents do not matter.  NULL if that is 0.
+ * The work of a sequence is split over its length by a rule on the sizes
+ * above (not on lens) and joined in a fixed order: results do not vary from
+ * call to call.
+ */
+typedef struct {
+    const void* q;
+    void* out;
+    const int32_t* table;
+    const int32_t* lens;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t q_batch_stride, q_head_stride, out_batch_stride, out_head_stride, table_stride;
+    int64_t batch, hq, table_width, window, sinks;
+    float scale;
+    int32_t dtype;          /* of q and out */
+} ck_attention_args;
+
+ck_status ck_paged_attention(const ck_attention_args* args, const ck_kv_cache* cache,
+                             hipStream_t stream);
+
+/* Bytes of workspace that ck_paged_attention needs for these sizes (host
+ * only); -1 for sizes that it refuses. */
+int64_t ck_paged_attention_workspace(int64_t batch, int64_t hq, int64_t hk, int64_t head_dim,
+                                     int64_t table_width, int64_t page_size, int64_t window,
+                                     int64_t sinks);
+
+/*
+ * Lay out 4-bit weights for ck_int4_linear, once, when they are loaded.
+ *
+ * codes   [in]  [n, ldc] bytes, two codes a byte: column 2 i in the lower
+ *               half, 2 i + 1 in the upper half; k even, ldc >= k / 2.
+ * scales  [in]  16-bit [n, lds], one per group of `group` columns (the last
+ *               group may be shorter); lds >= ceil(k / group).
+ * zeros   [in]  bytes [n, ldz], or NULL for 8 everywhere.
+ * w       [out] ceil(n / 16) * ceil(k / 128) * 1024 bytes, 16-B aligned.
+ * w_scale [out] 16-bit, ceil(n / 16) * G * 16 values, G = ceil(k / group).
+ * w_zero  [out] as many bytes; NULL exactly when zeros is NULL.
+ * group   32, 64 or 128; k a multiple of 8.
+ *
+ * Layout of w: row tiles of 16, each a sequence of 1 KiB blocks of 128
+ * columns.  Byte 16 l + 4 i + b of a block belongs to row l % 16 and columns
+ * 32 i + 8 (l / 16) + 0 .. 7; in those four bytes, as a little-endian word,
+ * the codes of columns 0, 2, 4, 6, 1, 3, 5, 7 follow each other from bit 0
+ * up.  Rows and columns past n and k hold code 0.  Scales and zeros: [row
+ * tile][group][16 rows], 0 past n.
+ */
+ck_status ck_int4_pack(const uint8_t* codes, int64_t ldc, const uint16_t* scales, int64_t lds,
+                       const uint8_t* zeros, int64_t ldz, uint8_t* w, uint16_t* w_scale,
+                       uint8_t* w_zero, int64_t n, int64_t k, int64_t group, hipStream_t stream);
+
+/*
+ * out[i, j] = round_out( sum_t x[i, t] (c[j, t] - z[j, g]) s[j, g] + bias[j] ),
+ * g = t / group, on the packed weights of ck_int4_pack: W4A16, x not
+ * quantised.  Codes and zero points are exact in the products; a group's sum
+ * is formed in fp32 before its scale is applied, also in fp32.
+ *
+ * x        [in]  16-bit (dtype) [m, ldx]; ldx >= k, ldx % 8 == 0, 16-B aligned.
+ * w, w_scale, w_zero  from ck_int4_pack, scales of x's type.
+ * bias     [in]  [n] of out's type, or NULL.
+ * out      [out] [m, ldo] of out_dtype.
+ * m == 0 or n == 0 is a no-op; k == 0 gives the bias (or 0).
+ */
+ck_status ck_int4_linear(const void* x, int64_t ldx, ck_dtype dtype, const uint8_t* w,
+                         const uint16_t* w_scale, const uint8_t* w_zero, const void* bias, void* out,
+                         int64_t ldo, ck_out_dtype out_dtype, int64_t m, int64_t n, int64_t k,
+                         int64_t group, hipStream_t stream);
+
 /* Name of a status code (static string). */
 const char* ck_status_string(ck_status s);
 
@@ -431,7 +617,7 @@ const char* ck_last_error(void);
 /* ABI version of this header: bumped when a signature changes. */
 int ck_abi_version(void);
 
-#define CK_ABI_VERSION 11
+#define CK_ABI_VERSION 12
 
 #ifdef __cplusplus
 }

@@ -31,7 +31,11 @@ CK_OUT_FP32 = 2
 
 CK_MAX_K = 132104
 CK_NUM_TILES = 14
-CK_ABI_VERSION = 11
+CK_ABI_VERSION = 12
+
+CK_DT_BF16 = 0
+CK_DT_FP16 = 1
+CK_DT_INT8 = 2
 
 EXPORTED = (
     "ck_quantize_int8_rowwise", "ck_quantize_int8_rotated", "ck_int8_linear",
@@ -39,7 +43,39 @@ EXPORTED = (
     "ck_hbm_stream", "ck_mfma_ceiling", "ck_status_string", "ck_last_error", "ck_abi_version",
     "ck_int8_table_set", "ck_int8_table_clear", "ck_int8_table_size",
     "ck_int8_set_forced_tile", "ck_int8_forced_tile", "ck_int8_set_path_log",
+    "ck_qk_norm_rope", "ck_paged_attention", "ck_paged_attention_workspace", "ck_int4_pack", "ck_int4_linear",
 )
+
+
+def _fields(*groups):
+    return [(n, t) for t, names in groups for n in names.split()]
+
+
+class CkKvCache(ctypes.Structure):
+    """ck_kv_cache of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "k v k_scale v_scale"),
+                       (ctypes.c_int64, "pages page_size heads head_dim page_stride head_stride token_stride "
+                                        "scale_page_stride scale_head_stride scale_token_stride"),
+                       (ctypes.c_int32, "dtype reserved"))
+
+
+class CkQkArgs(ctypes.Structure):
+    """ck_qk_args of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "q k v positions cos_sin q_weight k_weight q_out k_out slots"),
+                       (ctypes.c_int64, "q_token_stride q_head_stride k_token_stride k_head_stride "
+                                        "v_token_stride v_head_stride q_out_token_stride q_out_head_stride "
+                                        "k_out_token_stride k_out_head_stride tokens hq hk head_dim rot table_rows"),
+                       (ctypes.c_float, "eps"),
+                       (ctypes.c_int32, "dtype interleaved reserved"))
+
+
+class CkAttentionArgs(ctypes.Structure):
+    """ck_attention_args of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "q out table lens workspace"),
+                       (ctypes.c_int64, "workspace_bytes q_batch_stride q_head_stride out_batch_stride "
+                                        "out_head_stride table_stride batch hq table_width window sinks"),
+                       (ctypes.c_float, "scale"),
+                       (ctypes.c_int32, "dtype"))
 
 
 class CKError(RuntimeError):
@@ -103,6 +139,16 @@ def lib():
     L.ck_int8_forced_tile.restype = ci
     L.ck_int8_set_path_log.argtypes = [ci]
     L.ck_int8_set_path_log.restype = ci
+    L.ck_qk_norm_rope.argtypes = [p, p, p]
+    L.ck_qk_norm_rope.restype = ci
+    L.ck_paged_attention.argtypes = [p, p, p]
+    L.ck_paged_attention.restype = ci
+    L.ck_paged_attention_workspace.argtypes = [i64] * 8
+    L.ck_paged_attention_workspace.restype = i64
+    L.ck_int4_pack.argtypes = [p, i64, p, i64, p, i64, p, p, p, i64, i64, i64, p]
+    L.ck_int4_pack.restype = ci
+    L.ck_int4_linear.argtypes = [p, i64, ci, p, p, p, p, p, i64, ci, i64, i64, i64, i64, p]
+    L.ck_int4_linear.restype = ci
     L.ck_status_string.argtypes = [ci]
     L.ck_status_string.restype = ctypes.c_char_p
     L.ck_last_error.argtypes = []
@@ -174,6 +220,31 @@ def ck_int8_linear_dequant(x, ldx, w, ldw, w_scale, w_mode, bias, out, ldo, out_
 def ck_int8_gemm_i32(q, ldq, w, ldw, acc, ldacc, m, n, k, tile=-1, stream=0):
     _check(lib().ck_int8_gemm_i32(q, ldq, w, ldw, acc, ldacc, m, n, k, tile, stream),
            "ck_int8_gemm_i32")
+
+
+def ck_qk_norm_rope(args, cache=None, stream=0):
+    """args a CkQkArgs, cache a CkKvCache or None."""
+    _check(lib().ck_qk_norm_rope(ctypes.byref(args), None if cache is None else ctypes.byref(cache), stream),
+           "ck_qk_norm_rope")
+
+
+def ck_paged_attention(args, cache, stream=0):
+    """args a CkAttentionArgs, cache a CkKvCache."""
+    _check(lib().ck_paged_attention(ctypes.byref(args), ctypes.byref(cache), stream), "ck_paged_attention")
+
+
+def ck_paged_attention_workspace(batch, hq, hk, head_dim, table_width, page_size, window=0, sinks=0) -> int:
+    return int(lib().ck_paged_attention_workspace(batch, hq, hk, head_dim, table_width, page_size, window, sinks))
+
+
+def ck_int4_pack(codes, ldc, scales, lds, zeros, ldz, w, w_scale, w_zero, n, k, group, stream=0):
+    _check(lib().ck_int4_pack(codes, ldc, scales, lds, zeros, ldz, w, w_scale, w_zero, n, k, group, stream),
+           "ck_int4_pack")
+
+
+def ck_int4_linear(x, ldx, dtype, w, w_scale, w_zero, bias, out, ldo, out_dtype, m, n, k, group, stream=0):
+    _check(lib().ck_int4_linear(x, ldx, dtype, w, w_scale, w_zero, bias, out, ldo, out_dtype, m, n, k, group,
+                                stream), "ck_int4_linear")
 
 
 def ck_hbm_stream(src, chunks, dst, blocks, unroll, stream=0):
@@ -495,3 +566,9 @@ def int8_gemm_i32(q, w, tile: int = -1, out=None):
     ck_int8_gemm_i32(q.data_ptr(), q.stride(0), w.data_ptr(), w.stride(0), out.data_ptr(),
                      out.stride(0), m, n, k, tile, _stream(q))
     return out
+
+
+# ------------------------------------------------------- decode-step operators
+
+from .decode import (Int4Weight, KVCache, int4_linear, int4_pack, paged_attention,  # noqa: E402
+                     paged_attention_workspace, qk_norm_rope, rope_table)

@@ -2,7 +2,7 @@
 
     python -m int8_weight_quantized_amd.build
 
-compiles csrc/ck_int8.hip with hipcc into the package directory, where the
+compiles csrc/library.hip (which includes the other sources) with hipcc into the package directory, where the
 binding loads it from.  Always recompiles.
 """
 from __future__ import annotations
@@ -13,7 +13,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "ck_int8.hip")
+SRC = os.path.join(PKG, "csrc", "library.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libck_int8.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

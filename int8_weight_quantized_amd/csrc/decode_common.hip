@@ -1,0 +1,67 @@
+// decode_common.hip -- what the decode-step operators share: 16-bit element
+// types and the checks of a paged cache.
+
+// Two 16-bit values of a word to fp32 (exact), `lo` in bits 0..15.
+template <int DT>
+__device__ __forceinline__ float2 widen2(uint32_t w)
+{
+    if constexpr (DT == CK_DT_FP16) {
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        return make_float2((float)h[0], (float)h[1]);
+    } else {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+}
+
+// Two fp32 values to a word of 16-bit ones, each rounded to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi)
+{
+    return pack2<DT == CK_DT_FP16 ? EPI_F16 : EPI_BF16>(lo, hi);
+}
+
+// The quiet NaN of a 16-bit type, twice.
+template <int DT>
+constexpr uint32_t kNan2 = DT == CK_DT_FP16 ? 0x7e007e00u : 0x7fc07fc0u;
+
+namespace {
+
+bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
+
+int ilog2(int64_t v)
+{
+    int l = 0;
+    while ((int64_t(1) << (l + 1)) <= v) ++l;
+    return l;
+}
+
+// A paged cache for activations of type dtype; `align` bytes between rows.
+ck_status check_cache(const ck_kv_cache* c, int dtype, int64_t head_dim, int align)
+{
+    if (c->dtype != CK_DT_INT8 && c->dtype != dtype)
+        return fail(CK_ERR_INVALID_ARG, "the cache is neither int8 nor of the activations' type");
+    if (c->pages < 0 || c->heads < 1) return fail(CK_ERR_INVALID_ARG, "bad cache sizes");
+    if (!is_pow2(c->page_size) || c->page_size > 32768)
+        return fail(CK_ERR_INVALID_ARG, "page_size must be a power of two up to 32768");
+    if (c->pages > (int64_t(1) << 31) - 1) return fail(CK_ERR_UNSUPPORTED, "too many pages");
+    if (c->head_dim != head_dim) return fail(CK_ERR_INVALID_ARG, "cache and heads disagree on head_dim");
+    if (c->pages > 0 && (!c->k || !c->v)) return fail(CK_ERR_INVALID_ARG, "NULL cache");
+    if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->scale_page_stride < 0 ||
+        c->scale_head_stride < 0 || c->scale_token_stride < 0)
+        return fail(CK_ERR_INVALID_ARG, "negative cache stride");
+    if (c->page_size > 1 && c->token_stride < head_dim)
+        return fail(CK_ERR_INVALID_ARG, "token_stride smaller than head_dim");
+    const int esz = c->dtype == CK_DT_INT8 ? 1 : 2;
+    if (!aligned(c->k, align) || !aligned(c->v, align) || c->page_stride * esz % align != 0 ||
+        c->head_stride * esz % align != 0 || c->token_stride * esz % align != 0)
+        return fail(CK_ERR_UNSUPPORTED, "cache rows must start %d bytes apart", align);
+    if (c->dtype == CK_DT_INT8) {
+        if (c->pages > 0 && (!c->k_scale || !c->v_scale))
+            return fail(CK_ERR_INVALID_ARG, "an int8 cache needs k_scale and v_scale");
+        if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+            return fail(CK_ERR_UNSUPPORTED, "misaligned cache scales");
+    }
+    return CK_OK;
+}
+
+}  // namespace

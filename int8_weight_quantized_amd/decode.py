@@ -1,0 +1,303 @@
+"""Tensor-level entry points of the decode-step operators.
+
+What a model served with the int8 layers runs between its projections: norm
+and rotation of query and key heads with the write into a paged cache
+(``qk_norm_rope``), attention of one new token per sequence over that cache
+(``paged_attention``), and a projection with 4-bit weights
+(``int4_pack``, ``int4_linear``).  As for the int8 layer these helpers check
+their arguments, allocate outputs with torch and pass pointers and the
+current stream; every step runs in the library's HIP kernels.
+"""
+from __future__ import annotations
+
+import int8_weight_quantized_amd as _ck
+
+
+def _dtype16(t, name):
+    """CK_DT_* of a 16-bit floating tensor."""
+    import torch
+    if isinstance(t, torch.Tensor):
+        if t.dtype == torch.bfloat16:
+            return _ck.CK_DT_BF16
+        if t.dtype == torch.float16:
+            return _ck.CK_DT_FP16
+    raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
+
+
+def _strides(t):
+    """t's strides, 0 for dimensions of one element (torch leaves any value there)."""
+    return tuple(s if n > 1 else 0 for n, s in zip(t.shape, t.stride()))
+
+
+def _need_heads(t, dtype, name, tokens, heads, d, device):
+    """A [tokens, heads, d] view with unit stride in its last dimension."""
+    _ck._need(t, dtype, name, device)
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
+
+
+class KVCache:
+    """A paged key/value cache of one layer.
+
+    k, v: [pages, heads, page_size, head_dim], bfloat16, float16 or int8; any
+    strides with the last dimension contiguous (the same for both), so a view
+    of [pages, page_size, heads, head_dim] storage is fine.  An int8 cache has
+    fp32 k_scale and v_scale [pages, heads, page_size]: a row is its codes
+    times its scale.  The tensors stay the caller's; the object holds them.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if not isinstance(k, torch.Tensor) or k.dtype not in (torch.bfloat16, torch.float16, torch.int8):
+            raise TypeError("k must be a bfloat16, float16 or int8 tensor")
+        _ck._need(k, k.dtype, "k")
+        _ck._need(v, k.dtype, "v", k.device)
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [pages, heads, page_size, head_dim]")
+        if _strides(v) != _strides(k):
+            raise ValueError("k and v must have the same strides")
+        int8 = k.dtype == torch.int8
+        if int8 != (k_scale is not None) or int8 != (v_scale is not None):
+            raise ValueError("an int8 cache, and no other, has k_scale and v_scale")
+        if int8:
+            for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or s.device != k.device:
+                    raise TypeError(f"{name} must be a float32 tensor on {k.device}")
+                if s.shape != k.shape[:3]:
+                    raise ValueError(f"{name} has shape {tuple(s.shape)}, expected {tuple(k.shape[:3])}")
+            if _strides(k_scale) != _strides(v_scale):
+                raise ValueError("k_scale and v_scale must have the same strides")
+        pages, heads, page_size, d = k.shape
+        if page_size < 1 or page_size & (page_size - 1) or page_size > 32768:
+            raise ValueError("page_size must be a power of two up to 32768")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, d
+        self.device, self.dtype = k.device, k.dtype
+        code = {torch.bfloat16: _ck.CK_DT_BF16, torch.float16: _ck.CK_DT_FP16, torch.int8: _ck.CK_DT_INT8}[k.dtype]
+        ss = _strides(k_scale) if int8 else (0, 0, 0)
+        self.struct = _ck.CkKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if int8 else 0,
+                                    v_scale.data_ptr() if int8 else 0, pages, page_size, heads, d,
+                                    *_strides(k)[:3], *ss, code, 0)
+
+    @classmethod
+    def empty(cls, pages, heads, page_size, head_dim, dtype="bf16", device="cuda"):
+        """A new cache of dtype "bf16", "fp16" or "int8", zero-filled."""
+        import torch
+        types = {"bf16": torch.bfloat16, "fp16": torch.float16, "int8": torch.int8}
+        if dtype not in types:
+            raise ValueError(f"dtype must be 'bf16', 'fp16' or 'int8', not {dtype!r}")
+        shape = (pages, heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=types[dtype], device=device) for _ in range(2))
+        if dtype != "int8":
+            return cls(k, v)
+        return cls(k, v, *(torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def rope_table(rows: int, rot: int, base: float = 10000.0, device="cuda"):
+    """cos and sin of position * base^(-2 i / rot) as qk_norm_rope reads them:
+    fp32 [rows, rot], the cosines of the rot / 2 angles, then their sines.
+    Made once per model; the angles are formed in 64 bits (an fp32 angle of
+    position 131072 is off by up to 2^-8 radians)."""
+    import torch
+    if rows < 0 or rot < 0 or rot % 2:
+        raise ValueError("rows and rot must not be negative, rot even")
+    freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / max(rot, 1))
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def qk_norm_rope(q, k, v, positions, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, cache=None, slots=None, q_out=None, k_out=None):
+    """RMS norm of every query and key head, the position rotation, and the
+    write of keys and values into a paged cache, in one pass.
+
+    q [tokens, hq, d], k and v [tokens, hk, d]: bf16 or fp16, views of a fused
+    projection are fine.  positions int64 [tokens]; cos_sin from rope_table
+    (its width is the number of elements rotated), None for no rotation.
+    q_weight, k_weight fp32 [d]; None skips that norm.  interleaved rotates
+    neighbouring elements together, else the halves.  With a cache, keys and
+    values go to slots (int64 [tokens], page * page_size + offset, -1 for
+    none); keys also go to k_out when it is given or there is no cache.
+    q_out = q and k_out = k work in place.
+    -> (q_out, k_out or None)."""
+    import torch
+    dt = _dtype16(q, "q")
+    _ck._need(q, q.dtype, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D [tokens, heads, head_dim]")
+    dev, tt = q.device, q.dtype
+    tokens, hq, d = q.shape
+    if k is None:
+        if v is not None or cache is not None or k_out is not None:
+            raise ValueError("without k there is no v, cache or k_out")
+        hk = 0
+    else:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be 3-D [tokens, heads, head_dim]")
+        hk = k.shape[1]
+        _need_heads(k, tt, "k", tokens, hk, d, dev)
+    ws = []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _ck._need_vector(w, torch.float32, name, (d,), dev)
+        ws.append(0 if w is None else w.data_ptr())
+    rot = rows = pos_p = table_p = 0
+    if cos_sin is not None:
+        _ck._need(cos_sin, torch.float32, "cos_sin", dev)
+        if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous [rows, rot] tensor")
+        rows, rot = cos_sin.shape
+        _ck._need_vector(positions, torch.int64, "positions", (tokens,), dev)
+        pos_p, table_p = positions.data_ptr(), cos_sin.data_ptr()
+    vp = vt = vh = sp = 0
+    if cache is not None:
+        if not isinstance(cache, KVCache):
+            raise TypeError("cache must be a KVCache")
+        if cache.device != dev:
+            raise ValueError(f"the cache is on {cache.device}, q on {dev}")
+        if v is None or slots is None:
+            raise ValueError("a cache needs v and slots")
+        _need_heads(v, tt, "v", tokens, hk, d, dev)
+        _ck._need_vector(slots, torch.int64, "slots", (tokens,), dev)
+        vp, sp = v.data_ptr(), slots.data_ptr()
+        vt, vh, _ = _strides(v)
+    if q_out is None:
+        q_out = torch.empty((tokens, hq, d), dtype=tt, device=dev)
+    else:
+        _need_heads(q_out, tt, "q_out", tokens, hq, d, dev)
+    kp = kt = kh = kop = kot = koh = 0
+    if k is not None:
+        kp, (kt, kh, _) = k.data_ptr(), _strides(k)
+        if k_out is not None:
+            _need_heads(k_out, tt, "k_out", tokens, hk, d, dev)
+        elif cache is None:
+            k_out = torch.empty((tokens, hk, d), dtype=tt, device=dev)
+        if k_out is not None:
+            kop, (kot, koh, _) = k_out.data_ptr(), _strides(k_out)
+    args = _ck.CkQkArgs(q.data_ptr(), kp, vp, pos_p, table_p, ws[0], ws[1], q_out.data_ptr(), kop, sp,
+                        *_strides(q)[:2], kt, kh, vt, vh, *_strides(q_out)[:2], kot, koh,
+                        tokens, hq, hk, d, rot, rows, eps, dt, 1 if interleaved else 0, 0)
+    _ck.ck_qk_norm_rope(args, None if cache is None else cache.struct, _ck._stream(q))
+    return q_out, k_out
+
+
+def paged_attention_workspace(q, cache, table, window: int = 0, sinks: int = 0):
+    """A workspace tensor for paged_attention calls of these shapes (or None
+    if they need none): one per stream, kept for any number of calls."""
+    import torch
+    n = _ck.ck_paged_attention_workspace(q.shape[0], q.shape[1], cache.heads, cache.head_dim, table.shape[1],
+                                         cache.page_size, window, sinks)
+    if n < 0:
+        raise ValueError("sizes that paged_attention does not take")
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def paged_attention(q, cache, table, lens, scale=None, window: int = 0, sinks: int = 0, out=None, workspace=None):
+    """Attention of one new token per sequence over a paged cache.
+
+    q [batch, hq, d] bf16 or fp16, hq a multiple of the cache's heads; table
+    int32 [batch, width], the pages of each sequence in order; lens int32
+    [batch], the tokens of each, the new one included (0 gives zeros).  scale
+    defaults to d ** -0.5.  With window > 0 only the last `window` and the
+    first `sinks` tokens are visible.  workspace: from
+    paged_attention_workspace; allocated here when None.  -> [batch, hq, d]."""
+    import torch
+    dt = _dtype16(q, "q")
+    _ck._need(q, q.dtype, "q")
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    dev = q.device
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [batch, heads, head_dim] with the cache's head_dim")
+    if cache.device != dev:
+        raise ValueError(f"the cache is on {cache.device}, q on {dev}")
+    batch, hq, d = q.shape
+    _ck._need(table, torch.int32, "table", dev)
+    if table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError("table must be [batch, pages of a sequence]")
+    _ck._need_vector(lens, torch.int32, "lens", (batch,), dev)
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    if out is None:
+        out = torch.empty((batch, hq, d), dtype=q.dtype, device=dev)
+    else:
+        _need_heads(out, q.dtype, "out", batch, hq, d, dev)
+    if workspace is None:
+        workspace = paged_attention_workspace(q, cache, table, window, sinks)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    args = _ck.CkAttentionArgs(q.data_ptr(), out.data_ptr(), table.data_ptr(), lens.data_ptr(), wp, wn,
+                               *_strides(q)[:2], *_strides(out)[:2], table.stride(0), batch, hq,
+                               table.shape[1], window, sinks, d ** -0.5 if scale is None else scale, dt)
+    _ck.ck_paged_attention(args, cache.struct, _ck._stream(q))
+    return out
+
+
+class Int4Weight:
+    """4-bit weights laid out for int4_linear (see int4_pack)."""
+
+    def __init__(self, w, scales, zeros, n, k, group, dtype):
+        self.w, self.scales, self.zeros = w, scales, zeros
+        self.n, self.k, self.group, self.dtype = n, k, group, dtype
+        self.device = w.device
+
+
+def int4_pack(codes, scales, zeros=None, group: int = 128):
+    """Lay out 4-bit weights for int4_linear, once, when they are loaded.
+
+    codes uint8 [n, k / 2]: two codes a byte, the even column in the lower
+    half.  scales bf16 or fp16 [n, ceil(k / group)] and zeros uint8 of the
+    same shape (None: 8 everywhere); a weight is (code - zero) * scale.
+    group 32, 64 or 128; k a multiple of 8.  -> Int4Weight."""
+    import torch
+    _ck._need(codes, torch.uint8, "codes")
+    if codes.dim() != 2:
+        raise ValueError("codes must be 2-D [n, k / 2]")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    dev = codes.device
+    n, k = codes.shape[0], 2 * codes.shape[1]
+    if k % 8:
+        raise ValueError("k must be a multiple of 8")
+    groups = -(-k // group)
+    _dtype16(scales, "scales")
+    _ck._need_matrix(scales, scales.dtype, "scales", (n, groups), dev)
+    if zeros is not None:
+        _ck._need_matrix(zeros, torch.uint8, "zeros", (n, groups), dev)
+    tiles, chunks = -(-n // 16), -(-k // 128)
+    w = torch.empty(tiles * chunks * 1024, dtype=torch.uint8, device=dev)
+    s = torch.empty((tiles, groups, 16), dtype=scales.dtype, device=dev)
+    z = None if zeros is None else torch.empty((tiles, groups, 16), dtype=torch.uint8, device=dev)
+    ldc, lds, ldz = (t.stride(0) if t is not None and n > 1 else groups for t in (codes, scales, zeros))
+    _ck.ck_int4_pack(codes.data_ptr(), max(ldc, k // 2), scales.data_ptr(), lds,
+                     0 if z is None else zeros.data_ptr(), ldz, w.data_ptr(), s.data_ptr(),
+                     0 if z is None else z.data_ptr(), n, k, group, _ck._stream(codes))
+    return Int4Weight(w, s, z, n, k, group, scales.dtype)
+
+
+def int4_linear(x, weight, bias=None, out=None, out_dtype=None):
+    """bf16 or fp16 x [m, k] times the 4-bit weight [n, k] (of int4_pack,
+    with scales of x's type) -> [m, n] of out_dtype ("bf16", "fp16" or "fp32";
+    x's type when None).  bias [n] has the output's type."""
+    import torch
+    if not isinstance(weight, Int4Weight):
+        raise TypeError("weight must be an Int4Weight (see int4_pack)")
+    dt = _dtype16(x, "x")
+    _ck._need(x, weight.dtype, "x", weight.device)
+    code, tdt = _ck._out_dtype(("bf16", "fp16")[dt] if out_dtype is None else out_dtype)
+    if x.dim() != 2 or x.shape[1] != weight.k:
+        raise ValueError(f"x must be [m, {weight.k}]")
+    m, n, dev = x.shape[0], weight.n, x.device
+    if bias is not None:
+        _ck._need_vector(bias, tdt, "bias", (n,), dev)
+    if out is None:
+        out = torch.empty((m, n), dtype=tdt, device=dev)
+    else:
+        _ck._need_matrix(out, tdt, "out", (m, n), dev)
+    # one row has no stride of its own
+    ldx, ldo = (x.stride(0), out.stride(0)) if m > 1 else ((weight.k + 7) // 8 * 8, n)
+    _ck.ck_int4_linear(x.data_ptr(), ldx, dt, weight.w.data_ptr(), weight.scales.data_ptr(),
+                       0 if weight.zeros is None else weight.zeros.data_ptr(), 0 if bias is None else bias.data_ptr(),
+                       out.data_ptr(), ldo, code, m, n, weight.k, weight.group, _ck._stream(x))
+    return out

@@ -1,0 +1,423 @@
+"""The decode-step operators on the host: the C entry points and the binding
+refuse bad arguments before any HIP call (no GPU needed)."""
+import ctypes
+import re
+
+import pytest
+import torch
+
+import int8_weight_quantized_amd as ck
+from tests.test_abi import HEADER
+
+P = 4096          # a stand-in device address: validation never dereferences it
+BAD, UNS, OK, HIP = ck.CK_ERR_INVALID_ARG, ck.CK_ERR_UNSUPPORTED, ck.CK_OK, ck.CK_ERR_HIP
+
+
+def no_gpu(status):
+    if status == HIP and torch.cuda.is_available():
+        pytest.skip("needs the no-GPU host")
+
+
+def cache(**kw):
+    a = dict(k=P, v=P, k_scale=0, v_scale=0, pages=10, page_size=16, heads=2, head_dim=128, page_stride=4096,
+             head_stride=2048, token_stride=128, dtype=ck.CK_DT_BF16)
+    a.update(kw)
+    return ck.CkKvCache(**a)
+
+
+CACHES = [
+    (dict(), HIP),
+    (dict(dtype=ck.CK_DT_FP16), BAD),                # not q's type
+    (dict(dtype=7), BAD),
+    (dict(dtype=ck.CK_DT_INT8), BAD),                # no scales
+    (dict(dtype=ck.CK_DT_INT8, k_scale=P, v_scale=P), HIP),
+    (dict(dtype=ck.CK_DT_INT8, k_scale=P + 2, v_scale=P), UNS),
+    (dict(k=0), BAD),
+    (dict(v=0), BAD),
+    (dict(pages=-1), BAD),
+    (dict(pages=1 << 31), UNS),
+    (dict(heads=0), BAD),
+    (dict(page_size=0), BAD),
+    (dict(page_size=24), BAD),
+    (dict(page_size=65536), BAD),
+    (dict(head_dim=64), BAD),
+    (dict(token_stride=120), BAD),
+    (dict(page_stride=-4096), BAD),
+    (dict(k=P + 8), UNS),
+    (dict(token_stride=132), UNS),
+    (dict(head_stride=2052), UNS),
+    (dict(page_stride=4100), UNS),
+]
+
+
+def qk_args(**kw):
+    a = dict(q=P, k=P, v=P, positions=P, cos_sin=P, q_weight=P, k_weight=P, q_out=P, k_out=0, slots=P,
+             q_token_stride=1024, q_head_stride=128, k_token_stride=256, k_head_stride=128, v_token_stride=256,
+             v_head_stride=128, q_out_token_stride=1024, q_out_head_stride=128, k_out_token_stride=256,
+             k_out_head_stride=128, tokens=4, hq=8, hk=2, head_dim=128, rot=128, table_rows=100, eps=1e-6,
+             dtype=ck.CK_DT_BF16)
+    a.update(kw)
+    return ck.CkQkArgs(**a)
+
+
+def call_qk(a, c):
+    return ck.lib().ck_qk_norm_rope(ctypes.byref(a), None if c is None else ctypes.byref(c), 0)
+
+
+@pytest.mark.parametrize("kw,status", CACHES)
+def test_rope_cache_validation(kw, status):
+    no_gpu(status)
+    assert call_qk(qk_args(), cache(**kw)) == status
+    assert status == OK or ck.ck_last_error() != ""
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), HIP),
+    (dict(dtype=2), BAD),
+    (dict(tokens=-1), BAD),
+    (dict(tokens=0), OK),
+    (dict(tokens=0, q=0, q_out=0), OK),
+    (dict(q=0), BAD),
+    (dict(q_out=0), BAD),
+    (dict(k=0), BAD),
+    (dict(v=0), BAD),
+    (dict(slots=0), BAD),
+    (dict(positions=0), BAD),
+    (dict(cos_sin=0), BAD),
+    (dict(table_rows=0), BAD),
+    (dict(rot=0, positions=0, cos_sin=0), HIP),
+    (dict(rot=24), UNS),
+    (dict(rot=144), BAD),
+    (dict(head_dim=132), UNS),
+    (dict(head_dim=520), UNS),
+    (dict(hk=3), BAD),                       # the cache has two heads
+    (dict(eps=-1.0), BAD),
+    (dict(eps=float("nan")), BAD),
+    (dict(q=P + 2), UNS),
+    (dict(q_token_stride=1028), UNS),
+    (dict(q_out_head_stride=132), UNS),
+    (dict(k_head_stride=129), UNS),
+    (dict(k_out=P + 4), UNS),
+    (dict(v_token_stride=257), UNS),
+    (dict(q_weight=P + 4), UNS),
+    (dict(positions=P + 4), UNS),
+    (dict(q_weight=0, k_weight=0), HIP),
+    (dict(tokens=1 << 42), UNS),
+])
+def test_rope_validation(kw, status):
+    no_gpu(status)
+    assert call_qk(qk_args(**kw), cache()) == status
+
+
+def test_rope_without_a_cache():
+    assert call_qk(qk_args(v=0, slots=0), None) == BAD                      # no place for the keys
+    assert ck.lib().ck_qk_norm_rope(None, None, 0) == BAD
+    if not torch.cuda.is_available():
+        assert call_qk(qk_args(v=0, slots=0, k_out=P), None) == HIP
+        assert call_qk(qk_args(v=0, slots=0, k=0, hk=0), None) == HIP       # queries alone
+
+
+def attn_args(**kw):
+    a = dict(q=P, out=P, table=P, lens=P, workspace=P, workspace_bytes=1 << 40, q_batch_stride=1024, q_head_stride=128,
+             out_batch_stride=1024, out_head_stride=128, table_stride=63, batch=3, hq=8, table_width=63, window=0,
+             sinks=0, scale=0.1, dtype=ck.CK_DT_BF16)
+    a.update(kw)
+    return ck.CkAttentionArgs(**a)
+
+
+@pytest.mark.parametrize("kw,status", CACHES)
+def test_attention_cache_validation(kw, status):
+    no_gpu(status)
+    if "head_dim" in kw:
+        pytest.skip("the cache's head_dim is q's here")
+    assert ck.lib().ck_paged_attention(ctypes.byref(attn_args()), ctypes.byref(cache(**kw)), 0) == status
+
+
+@pytest.mark.parametrize("kw,ckw,status", [
+    (dict(), dict(), HIP),
+    (dict(dtype=2), dict(), BAD),
+    (dict(batch=-1), dict(), BAD),
+    (dict(batch=0), dict(), OK),
+    (dict(hq=0), dict(), OK),
+    (dict(hq=7), dict(), BAD),
+    (dict(window=-1), dict(), BAD),
+    (dict(sinks=-1), dict(), BAD),
+    (dict(table_width=-1), dict(), BAD),
+    (dict(q=0), dict(), BAD),
+    (dict(out=0), dict(), BAD),
+    (dict(lens=0), dict(), BAD),
+    (dict(table=0), dict(), BAD),
+    (dict(table=0, table_width=0), dict(), HIP),
+    (dict(table_stride=62), dict(), BAD),
+    (dict(table_stride=0, batch=1), dict(), HIP),
+    (dict(q=P + 2), dict(), UNS),
+    (dict(q_head_stride=129), dict(), UNS),
+    (dict(out_batch_stride=1025), dict(), UNS),
+    (dict(lens=P + 2), dict(), UNS),
+    (dict(scale=float("nan")), dict(), BAD),
+    (dict(batch=(1 << 20) + 1), dict(), UNS),
+    (dict(table_width=1 << 31, table_stride=1 << 31), dict(), UNS),
+    (dict(), dict(head_dim=80, token_stride=80), UNS),
+    (dict(), dict(head_dim=512, token_stride=512), UNS),
+    (dict(), dict(dtype=ck.CK_DT_INT8, k_scale=P, v_scale=P, k=P + 8), UNS),     # int8 rows 16 bytes apart here
+])
+def test_attention_validation(kw, ckw, status):
+    no_gpu(status)
+    assert ck.lib().ck_paged_attention(ctypes.byref(attn_args(**kw)), ctypes.byref(cache(**ckw)), 0) == status
+
+
+def test_attention_workspace():
+    L = ck.lib()
+    a, c = attn_args(batch=2, table_width=4096, table_stride=4096), cache()
+    need = ck.ck_paged_attention_workspace(2, 8, 2, 128, 4096, 16, 0, 0)
+    assert need > 0
+    for kw, status in ((dict(workspace=0), BAD), (dict(workspace_bytes=need - 1), BAD), (dict(workspace=P + 16), UNS)):
+        b = attn_args(batch=2, table_width=4096, table_stride=4096, **kw)
+        assert L.ck_paged_attention(ctypes.byref(b), ctypes.byref(c), 0) == status
+    if not torch.cuda.is_available():
+        a.workspace_bytes = need
+        assert L.ck_paged_attention(ctypes.byref(a), ctypes.byref(c), 0) == HIP
+    # never more for a window than for the whole length; refused sizes
+    assert 0 <= ck.ck_paged_attention_workspace(2, 8, 2, 128, 4096, 16, 1000, 4) <= need
+    for bad in ((-1, 8, 2, 128, 4, 16), (2, 7, 2, 128, 4, 16), (2, 8, 0, 128, 4, 16), (2, 8, 2, 100, 4, 16),
+                (2, 8, 2, 128, -4, 16), (2, 8, 2, 128, 4, 12), (2, 8, 2, 128, 4, 16, -1), (2, 8, 2, 128, 4, 16, 1, -1)):
+        assert ck.ck_paged_attention_workspace(*bad) == -1
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), HIP),
+    (dict(n=0, codes=0, w=0), OK),
+    (dict(n=-1), BAD),
+    (dict(k=-8), BAD),
+    (dict(group=48), UNS),
+    (dict(k=132), UNS),
+    (dict(codes=0), BAD),
+    (dict(scales=0), BAD),
+    (dict(w=0), BAD),
+    (dict(w_scale=0), BAD),
+    (dict(zeros=P), BAD),                    # zeros without w_zero
+    (dict(w_zero=P), BAD),
+    (dict(zeros=P, ldz=4, w_zero=P), HIP),
+    (dict(zeros=P, ldz=3, w_zero=P), BAD),
+    (dict(ldc=255), BAD),
+    (dict(lds=3), BAD),
+    (dict(w=P + 8), UNS),
+    (dict(w_scale=P + 8), UNS),
+    (dict(scales=P + 1), UNS),
+    (dict(n=1 << 31), UNS),
+])
+def test_int4_pack_validation(kw, status):
+    no_gpu(status)
+    a = dict(codes=P, ldc=256, scales=P, lds=4, zeros=0, ldz=0, w=P, w_scale=P, w_zero=0, n=64, k=512, group=128)
+    a.update(kw)
+    assert ck.lib().ck_int4_pack(*a.values(), 0) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), HIP),
+    (dict(m=0, x=0, out=0), OK),
+    (dict(n=0, out=0), OK),
+    (dict(m=-1), BAD),
+    (dict(n=-1), BAD),
+    (dict(dtype=2), BAD),
+    (dict(out_dtype=3), BAD),
+    (dict(group=16), UNS),
+    (dict(k=508, ldx=512), UNS),
+    (dict(x=0), BAD),
+    (dict(w=0), BAD),
+    (dict(w_scale=0), BAD),
+    (dict(out=0), BAD),
+    (dict(ldx=504), BAD),
+    (dict(ldx=516), UNS),
+    (dict(ldo=63), BAD),
+    (dict(x=P + 8), UNS),
+    (dict(w=P + 8), UNS),
+    (dict(w_zero=P + 4), UNS),
+    (dict(out=P + 2, out_dtype=2), UNS),
+    (dict(bias=P + 1), UNS),
+    (dict(k=0, x=0, w=0, w_scale=0), HIP),   # the bias alone
+])
+def test_int4_linear_validation(kw, status):
+    no_gpu(status)
+    a = dict(x=P, ldx=512, dtype=0, w=P, w_scale=P, w_zero=0, bias=0, out=P, ldo=64, out_dtype=0, m=3, n=64, k=512,
+             group=128)
+    a.update(kw)
+    assert ck.lib().ck_int4_linear(*a.values(), 0) == status
+
+
+def test_struct_fields_follow_the_header():
+    """The binding's structures have the header's fields, in its order."""
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    for name, cls in (("ck_kv_cache", ck.CkKvCache), ("ck_qk_args", ck.CkQkArgs), ("ck_attention_args", ck.CkAttentionArgs)):
+        body = re.search(r"typedef struct \{([^}]*)\} %s;" % name, text).group(1)
+        want = []
+        for line in body.split(";"):
+            if line.strip():
+                kind = "ptr" if "*" in line else re.search(r"\b(int64_t|int32_t|float)\b", line).group(1)
+                names = re.sub(r"\b(const|void|float|int64_t|int32_t)\b|\*", " ", line)
+                want += [(n.strip(), kind) for n in names.split(",")]
+        kinds = {ctypes.c_void_p: "ptr", ctypes.c_int64: "int64_t", ctypes.c_int32: "int32_t", ctypes.c_float: "float"}
+        assert [(n, kinds[t]) for n, t in cls._fields_] == want
+
+
+# ------------------------------------------------------------- the binding
+
+@pytest.fixture
+def host(monkeypatch):
+    class Launched(Exception):
+        pass
+
+    def launched(*a, **k):
+        raise Launched()
+
+    monkeypatch.setattr(ck, "_DEVICE_TYPE", "cpu")
+    monkeypatch.setattr(ck, "_stream", lambda t: 0)
+    for f in ("ck_qk_norm_rope", "ck_paged_attention", "ck_int4_pack", "ck_int4_linear"):
+        monkeypatch.setattr(ck, f, launched)
+    return Launched
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def test_binding_kv_cache(host):
+    c = ck.KVCache.empty(5, 2, 16, 128, "int8", "cpu")
+    assert (c.pages, c.heads, c.page_size, c.head_dim) == (5, 2, 16, 128)
+    assert c.struct.token_stride == 128 and c.struct.scale_token_stride == 1 and c.struct.dtype == ck.CK_DT_INT8
+    nhd = ck.KVCache(bf(5, 16, 2, 128).transpose(1, 2), bf(5, 16, 2, 128).transpose(1, 2))
+    assert (nhd.struct.page_stride, nhd.struct.head_stride, nhd.struct.token_stride) == (4096, 128, 256)
+    s = torch.zeros(5, 2, 16)
+    i8 = torch.zeros((5, 2, 16, 128), dtype=torch.int8)
+    for exc, args in [
+        (TypeError, (bf(5, 2, 16, 128).float(), bf(5, 2, 16, 128).float())),
+        (TypeError, (bf(5, 2, 16, 128), bf(5, 2, 16, 128).half())),
+        (ValueError, (bf(5, 2, 16, 128), bf(5, 2, 16, 64))),
+        (ValueError, (bf(5, 2, 128), bf(5, 2, 128))),
+        (ValueError, (bf(5, 2, 12, 128), bf(5, 2, 12, 128))),
+        (ValueError, (bf(5, 2, 128, 16).transpose(2, 3), bf(5, 2, 128, 16).transpose(2, 3))),
+        (ValueError, (bf(5, 2, 16, 128), bf(5, 16, 2, 128).transpose(1, 2))),
+        (ValueError, (i8, i8)),
+        (ValueError, (bf(5, 2, 16, 128), bf(5, 2, 16, 128), s, s)),
+        (TypeError, (i8, i8, s.half(), s)),
+        (ValueError, (i8, i8, s[:4], s)),
+        (ValueError, (i8, i8, s, torch.zeros(5, 16, 2).transpose(1, 2))),
+    ]:
+        with pytest.raises(exc):
+            ck.KVCache(*args)
+    with pytest.raises(ValueError):
+        ck.KVCache.empty(5, 2, 16, 128, "fp8", "cpu")
+
+
+def test_binding_rope(host):
+    q, k, v = bf(4, 8, 128), bf(4, 2, 128), bf(4, 2, 128)
+    pos, table, w = torch.zeros(4, dtype=torch.int64), ck.rope_table(50, 128, device="cpu"), torch.ones(128)
+    c = ck.KVCache.empty(3, 2, 16, 128, "bf16", "cpu")
+    good = dict(q=q, k=k, v=v, positions=pos, cos_sin=table, q_weight=w, k_weight=w, cache=c, slots=pos)
+    with pytest.raises(host):
+        ck.qk_norm_rope(**good)
+    with pytest.raises(host):
+        ck.qk_norm_rope(q, None, None, pos, table, w)
+    with pytest.raises(host):
+        ck.qk_norm_rope(q, k, None, None, None, w, w)
+    for exc, kw in [
+        (TypeError, dict(q=q.float())),
+        (ValueError, dict(q=bf(4, 1024))),
+        (TypeError, dict(k=k.half())),
+        (ValueError, dict(k=bf(3, 2, 128))),
+        (ValueError, dict(k=bf(4, 2, 64))),
+        (ValueError, dict(v=bf(4, 1, 128))),
+        (ValueError, dict(v=None)),
+        (ValueError, dict(slots=None)),
+        (TypeError, dict(slots=pos.int())),
+        (ValueError, dict(slots=pos[:3])),
+        (TypeError, dict(positions=pos.int())),
+        (TypeError, dict(positions=None)),
+        (TypeError, dict(cos_sin=table.double())),
+        (ValueError, dict(cos_sin=table.t())),
+        (TypeError, dict(q_weight=w.bfloat16())),
+        (ValueError, dict(k_weight=w[:64])),
+        (TypeError, dict(cache=c.k)),
+        (ValueError, dict(q_out=bf(4, 8, 64))),
+        (ValueError, dict(k_out=bf(4, 8, 128))),
+        (ValueError, dict(k=None)),
+        (TypeError, dict(q_weight=torch.ones(128, device="meta"))),
+    ]:
+        with pytest.raises(exc):
+            ck.qk_norm_rope(**{**good, **kw})
+
+
+def test_binding_attention(host):
+    c = ck.KVCache.empty(9, 2, 16, 128, "bf16", "cpu")
+    good = dict(q=bf(3, 8, 128), cache=c, table=torch.zeros((3, 4), dtype=torch.int32),
+                lens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(host):
+        ck.paged_attention(**good)
+    with pytest.raises(host):
+        ck.paged_attention(**good, window=100, sinks=4, scale=1.0, out=bf(3, 8, 128))
+    for exc, kw in [
+        (TypeError, dict(q=good["q"].float())),
+        (ValueError, dict(q=bf(3, 8, 64))),
+        (ValueError, dict(q=bf(3, 1024))),
+        (TypeError, dict(cache=c.k)),
+        (TypeError, dict(table=good["table"].long())),
+        (ValueError, dict(table=good["table"][:2])),
+        (TypeError, dict(lens=good["lens"].long())),
+        (ValueError, dict(lens=good["lens"][:2])),
+        (ValueError, dict(window=-1)),
+        (ValueError, dict(sinks=-1)),
+        (ValueError, dict(q=bf(3, 7, 128))),
+        (ValueError, dict(out=bf(3, 8, 64))),
+        (TypeError, dict(out=bf(3, 8, 128).half())),
+        (TypeError, dict(workspace=torch.zeros(1 << 20))),
+    ]:
+        with pytest.raises(exc):
+            ck.paged_attention(**{**good, **kw})
+
+
+def test_binding_int4(host):
+    codes, scales = torch.zeros((32, 128), dtype=torch.uint8), bf(32, 2)
+    with pytest.raises(host):
+        ck.int4_pack(codes, scales)
+    for exc, kw in [
+        (TypeError, dict(codes=codes.to(torch.int8))),
+        (ValueError, dict(codes=codes[0])),
+        (ValueError, dict(codes=codes[:, :127])),
+        (TypeError, dict(scales=scales.float())),
+        (ValueError, dict(scales=bf(32, 3))),
+        (ValueError, dict(group=64)),
+        (ValueError, dict(group=100)),
+        (TypeError, dict(zeros=torch.zeros((32, 2)))),
+        (ValueError, dict(zeros=torch.zeros((31, 2), dtype=torch.uint8))),
+    ]:
+        with pytest.raises(exc):
+            ck.int4_pack(**{**dict(codes=codes, scales=scales), **kw})
+    w = ck.Int4Weight(torch.zeros(4096, dtype=torch.uint8), bf(2, 2, 16), None, 32, 256, 128, torch.bfloat16)
+    with pytest.raises(host):
+        ck.int4_linear(bf(3, 256), w, bf(32))
+    with pytest.raises(host):
+        ck.int4_linear(bf(3, 256), w, bf(32).float(), out_dtype="fp32")
+    for exc, kw in [
+        (TypeError, dict(x=bf(3, 256).float())),
+        (TypeError, dict(x=bf(3, 256).half())),
+        (ValueError, dict(x=bf(3, 248))),
+        (ValueError, dict(x=bf(256))),
+        (TypeError, dict(weight=codes)),
+        (TypeError, dict(bias=bf(32).float())),
+        (ValueError, dict(bias=bf(31))),
+        (ValueError, dict(out_dtype="int8")),
+        (ValueError, dict(out=bf(3, 31))),
+        (TypeError, dict(out=bf(3, 32).half())),
+    ]:
+        with pytest.raises(exc):
+            ck.int4_linear(**{**dict(x=bf(3, 256), weight=w), **kw})
+
+
+def test_rope_table():
+    t = ck.rope_table(1000, 64, 500000.0, device="cpu")
+    assert t.shape == (1000, 64) and t.dtype == torch.float32
+    angle = 999 * 500000.0 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64)
+    assert (t[999, :32].double() - angle.cos()).abs().max() <= 2.0 ** -25 + 1e-12
+    assert (t[999, 32:].double() - angle.sin()).abs().max() <= 2.0 ** -25 + 1e-12
+    with pytest.raises(ValueError):
+        ck.rope_table(10, 7, device="cpu")

@@ -1,0 +1,506 @@
+"""The decode-step operators on the GPU against plain references in 64 bits:
+qk_norm_rope, paged_attention, int4_pack and int4_linear."""
+import pytest
+import torch
+
+import int8_weight_quantized_amd as ck
+from tests import decode_ref as ref
+from tests.gpu_util import cuda_device
+
+pytestmark = pytest.mark.gpu
+DT = ref.TYPES
+
+
+def rand(*shape, dtype=torch.float32, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed + 7919 * len(shape) + sum(shape))
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+# ------------------------------------------------------------- qk_norm_rope
+
+def rope_inputs(tokens, hq, hk, d, rot, dtype, far, seed=1):
+    dev = cuda_device()
+    qkv = rand(tokens, (hq + 2 * hk) * d, dtype=DT[dtype], seed=seed).to(dev)
+    q = qkv[:, :hq * d].view(tokens, hq, d)
+    k = qkv[:, hq * d:(hq + hk) * d].view(tokens, hk, d)
+    v = qkv[:, (hq + hk) * d:].view(tokens, hk, d)
+    qw, kw = (1 + 0.3 * rand(d, seed=seed + 8)).to(dev), (1 + 0.3 * rand(d, seed=seed + 9)).to(dev)
+    pos = torch.randint(0, far, (tokens,), generator=torch.Generator().manual_seed(seed)).to(dev)
+    return q, k, v, qw, kw, pos, ck.rope_table(far, rot, device=dev) if rot else None
+
+
+@pytest.mark.parametrize("tokens,hq,hk,d,rot,interleaved,dtype,cache,page,norm", [
+    (1, 32, 8, 128, 128, False, "bf16", "bf16", 16, True),
+    (3, 4, 4, 64, 64, False, "fp16", "int8", 1, True),
+    (65, 7, 1, 96, 48, False, "bf16", "int8", 8, True),
+    (33, 16, 2, 256, 128, True, "fp16", "fp16", 32, True),
+    (17, 2, 1, 512, 512, True, "bf16", "bf16", 64, False),
+    (9, 5, 5, 80, 32, False, "fp16", "fp16", 16, True),
+    (31, 3, 1, 8, 0, False, "bf16", "int8", 16, True),
+    (20, 6, 2, 192, 192, True, "bf16", "int8", 128, False),
+    (700, 24, 8, 128, 64, False, "bf16", "bf16", 16, True),
+])
+def test_rope(tokens, hq, hk, d, rot, interleaved, dtype, cache, page, norm):
+    dev = cuda_device()
+    q, k, v, qw, kw, pos, table = rope_inputs(tokens, hq, hk, d, rot, dtype, 5000)
+    qw, kw = (qw, kw) if norm else (None, None)
+    pages = -(-tokens // page) + 2
+    c = ck.KVCache.empty(pages, hk, page, d, cache, dev)
+    for t in (c.k, c.v, c.k_scale, c.v_scale):
+        if t is not None:
+            t.fill_(7)
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(3))[:tokens]
+    if tokens > 2:
+        slots[1] = -1
+        slots[2] = pages * page          # outside: not written
+    qo, ko = ck.qk_norm_rope(q, k, v, pos if rot else None, table, qw, kw, eps=1e-5, interleaved=interleaved,
+                             cache=c, slots=slots.to(dev), k_out=torch.empty_like(k))
+    want_q, slack_q = ref.rope(q, qw, table, pos, rot, interleaved, 1e-5)
+    want_k, slack_k = ref.rope(k, kw, table, pos, rot, interleaved, 1e-5)
+    ref.assert_within(qo, want_q, slack_q, "q")
+    ref.assert_within(ko, want_k, slack_k, "k_out")
+    used = (slots >= 0) & (slots < pages * page)
+    for name, t, sc, want, slack in (("k", c.k, c.k_scale, want_k, slack_k),
+                                     ("v", c.v, c.v_scale, v.cpu().double(), torch.zeros(()))):
+        flat = t.cpu().transpose(1, 2).reshape(pages * page, hk, d)
+        rest = torch.ones(pages * page, dtype=torch.bool)
+        rest[slots[used]] = False
+        assert (flat[rest] == 7).all(), f"{name}: a row of the cache that no token has was written"
+        got, w = flat[slots[used]], want[used]
+        if cache != "int8":
+            ref.assert_within(got, w, slack[used] if slack.dim() else torch.zeros_like(w), f"cache {name}")
+            continue
+        scale = sc.cpu().transpose(1, 2).reshape(pages * page, hk)[slots[used]].double()
+        if name == "v":                  # given values: the row quantisation's codes and scales, bit for bit
+            x = v.cpu()[used].float()
+            scales = x.abs().amax(-1) / 127
+            assert torch.equal(scale, scales.double())
+            assert torch.equal(got, torch.round(x / scales[..., None]).clamp(-127, 127).to(torch.int8))
+            continue
+        amax = w.abs().amax(-1)
+        e = slack[used].amax(-1)
+        assert ((scale - amax / 127).abs() <= (e + amax * 2 * ref.U32) / 127 + 2.0 ** -149).all(), f"scale of {name}"
+        # a code is the nearest: half a scale off, and what the value and the scale are off themselves
+        off = (got.double() * scale[..., None] - w).abs()
+        assert (off <= 0.5 * scale[..., None] * (1 + 2.0 ** -20) + 2 * e[..., None]).all(), f"codes of {name}"
+        assert got.abs().max() <= 127
+
+
+def test_rope_int8_values_are_the_row_quantisation():
+    """The values of an int8 cache are ck_quantize_int8_rowwise's codes and scales, bit for bit."""
+    dev = cuda_device()
+    q, k, v, qw, kw, pos, table = rope_inputs(37, 4, 2, 128, 128, "bf16", 100)
+    v[5, 1] = 0
+    c = ck.KVCache.empty(5, 2, 8, 128, "int8", dev)
+    ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=c, slots=torch.arange(37, device=dev))
+    codes, scales = ck.quantize_int8_rowwise(v.reshape(-1, 128).contiguous())
+    flat = c.v.transpose(1, 2).reshape(40, 2, 128)[:37]
+    assert torch.equal(flat.reshape(-1, 128), codes)
+    assert torch.equal(c.v_scale.transpose(1, 2).reshape(40, 2)[:37].reshape(-1), scales)
+
+
+def test_rope_in_place_and_queries_alone():
+    q, k, v, qw, kw, pos, table = rope_inputs(50, 6, 2, 128, 128, "bf16", 300)
+    want_q, want_k = ck.qk_norm_rope(q, k, None, pos, table, qw, kw)
+    alone, none = ck.qk_norm_rope(q, None, None, pos, table, qw)
+    assert none is None and torch.equal(alone, want_q)
+    qq, kk = ck.qk_norm_rope(q, k, None, pos, table, qw, kw, q_out=q, k_out=k)
+    assert qq is q and kk is k and torch.equal(q, want_q) and torch.equal(k, want_k)
+
+
+def test_rope_positions_outside_the_table():
+    """Such a token's rows are NaN and the cache keeps its rows; the others are not touched."""
+    dev = cuda_device()
+    q, k, v, qw, kw, pos, table = rope_inputs(6, 3, 1, 96, 48, "bf16", 64)
+    good, good_k = ck.qk_norm_rope(q, k, None, pos, table, qw, kw)
+    pos[1], pos[4] = -1, 64
+    c = ck.KVCache.empty(1, 1, 8, 96, "bf16", dev)
+    c.k.fill_(7)
+    c.v.fill_(7)
+    qo, ko = ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=c, slots=torch.arange(6, device=dev), k_out=torch.empty_like(k))
+    for t in range(6):
+        if t in (1, 4):
+            assert qo[t].isnan().all() and ko[t].isnan().all()
+            assert (c.k[0, 0, t] == 7).all() and (c.v[0, 0, t] == 7).all()
+        else:
+            assert torch.equal(qo[t], good[t]) and torch.equal(ko[t], good_k[t])
+            assert torch.equal(c.k[0, 0, t], good_k[t, 0]) and torch.equal(c.v[0, 0, t], v[t, 0])
+
+
+def test_rope_zero_tokens_and_zero_rows():
+    q, k, v, qw, kw, pos, table = rope_inputs(4, 2, 2, 64, 64, "fp16", 64)
+    qo, ko = ck.qk_norm_rope(q[:0], k[:0], None, pos[:0], table, qw, kw)
+    assert qo.shape == (0, 2, 64) and ko.shape == (0, 2, 64)
+    q.zero_()
+    qo, _ = ck.qk_norm_rope(q, k, None, pos, table, qw, kw)
+    assert (qo == 0).all()
+
+
+def test_rope_far_cache_rows():
+    """A row past 2^31 elements of the cache."""
+    dev = cuda_device()
+    pages = (1 << 31) // (16 * 128) + 3
+    c = ck.KVCache(*(torch.zeros((pages, 1, 16, 128), dtype=torch.int8, device=dev) for _ in range(2)),
+                   *(torch.zeros((pages, 1, 16), device=dev) for _ in range(2)))
+    q, k, v, qw, kw, pos, table = rope_inputs(2, 1, 1, 128, 128, "bf16", 64)
+    slots = torch.tensor([pages * 16 - 1, 0], device=dev)
+    ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=c, slots=slots)
+    codes, scales = ck.quantize_int8_rowwise(v.reshape(2, 128).contiguous())
+    assert torch.equal(c.v[-1, 0, 15], codes[0]) and torch.equal(c.v[0, 0, 0], codes[1])
+    assert c.v_scale[-1, 0, 15] == scales[0] and c.k_scale[-1, 0, 15] > 0
+    assert int((c.v_scale != 0).sum()) == 2
+
+
+# ---------------------------------------------------------- paged_attention
+
+def make_cache(pages, hk, page, d, cache, dtype, layout="hnd", seed=5):
+    dev = cuda_device()
+    shape = (pages, hk, page, d) if layout == "hnd" else (pages, page, hk, d)
+    k, v = rand(*shape, seed=seed).to(dev), rand(*shape, seed=seed + 1).to(dev)
+    if cache == "int8":
+        ks, vs = (t.abs().amax(-1) / 127 for t in (k, v))
+        k, v = (torch.round(t / s[..., None]).to(torch.int8) for t, s in ((k, ks), (v, vs)))
+    else:
+        k, v, ks, vs = k.to(DT[dtype]), v.to(DT[dtype]), None, None
+    if layout != "hnd":
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+        ks, vs = (None if t is None else t.transpose(1, 2) for t in (ks, vs))
+    return ck.KVCache(k, v, ks, vs)
+
+
+def tables(lens, page, pages, seed=11):
+    """Every sequence's pages, all different, the table's unused entries far outside the cache."""
+    width = max(1, max(-(-n // page) for n in lens))
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(seed)).int()
+    t = torch.full((len(lens), width), 1 << 30, dtype=torch.int32)
+    at = 0
+    for i, n in enumerate(lens):
+        c = -(-n // page)
+        t[i, :c] = order[at:at + c]
+        at += c
+    return t.to(cuda_device()), torch.tensor(lens, dtype=torch.int32, device=cuda_device())
+
+
+def poison(cache, table, lens, window=0, sinks=0):
+    """Rows that no sequence sees become NaN (codes 127 with a NaN scale)."""
+    page = cache.page_size
+    seen = torch.zeros((cache.pages, page), dtype=torch.bool)
+    for i, n in enumerate(lens.tolist()):
+        at = ref.visible_tokens(n, window, sinks)
+        seen[table[i].cpu().long()[at // page], at % page] = True
+    hide = ~seen.to(cache.device)[:, None, :].expand(-1, cache.heads, -1)
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        t[hide] = 127 if s is not None else float("nan")
+        if s is not None:
+            s[hide] = float("nan")
+
+
+def check_attention(q, cache, table, lens, scale=None, window=0, sinks=0, **kw):
+    out = ck.paged_attention(q, cache, table, lens, scale, window=window, sinks=sinks, **kw)
+    want, slack = ref.attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, lens,
+                                q.shape[2] ** -0.5 if scale is None else scale, window, sinks)
+    ref.assert_within(out, want, slack, "attention")
+    return out
+
+
+@pytest.mark.parametrize("hq,hk,d,dtype,cache,page", [
+    (8, 8, 128, "bf16", "bf16", 16),
+    (32, 8, 128, "bf16", "int8", 16),
+    (6, 2, 64, "fp16", "fp16", 8),
+    (7, 1, 96, "fp16", "int8", 1),
+    (16, 1, 192, "bf16", "bf16", 32),
+    (16, 2, 256, "fp16", "int8", 64),
+    (20, 1, 128, "bf16", "bf16", 128),
+    (33, 1, 64, "bf16", "int8", 2),
+    (40, 2, 256, "bf16", "bf16", 4),
+])
+def test_attention_lengths(hq, hk, d, dtype, cache, page):
+    """Lengths about the borders of pages, tiles and splits, 0 and 1 among them; unseen rows are NaN."""
+    lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513, 1500]
+    pages = sum(-(-n // page) for n in lens) + 1
+    c = make_cache(pages, hk, page, d, cache, dtype)
+    table, n = tables(lens, page, pages)
+    poison(c, table, n)
+    q = rand(len(lens), hq, d, dtype=DT[dtype], scale=2.0).to(cuda_device())
+    out = check_attention(q, c, table, n)
+    assert (out[0] == 0).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 16), (100, 4), (333, 37), (1000, 2000), (4096, 4)])
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("int8", 64)])
+def test_attention_window_and_sinks(window, sinks, cache, d):
+    lens = [0, 1, 4, 5, 6, 50, 104, 105, 333, 370, 371, 1001, 2500]
+    pages = sum(-(-n // 16) for n in lens) + 1
+    c = make_cache(pages, 2, 16, d, cache, "bf16")
+    table, n = tables(lens, 16, pages)
+    poison(c, table, n, window, sinks)
+    check_attention(rand(len(lens), 8, d, dtype=torch.bfloat16, scale=2.0).to(cuda_device()), c, table, n,
+                    window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_long(dtype):
+    """One long sequence among short ones: many splits, most of them empty for the short ones."""
+    lens = [40000, 3, 9000, 0]
+    pages = sum(-(-n // 16) for n in lens)
+    c = make_cache(pages, 2, 16, 128, dtype, dtype)
+    table, n = tables(lens, 16, pages)
+    check_attention(rand(4, 8, 128, dtype=DT[dtype], scale=2.0).to(cuda_device()), c, table, n)
+
+
+def test_attention_peaked_and_growing_scores():
+    """Scores that rise along the sequence by hundreds, and one token that outweighs all others."""
+    c = make_cache(40, 1, 16, 128, "bf16", "bf16")
+    table, n = tables([640], 16, 40)
+    order = table[0].long()
+    ramp = torch.linspace(-6, 6, 640, device=cuda_device()).to(torch.bfloat16)
+    c.k[order, 0] = ramp.view(40, 16, 1).expand(40, 16, 128)
+    q = torch.ones((1, 4, 128), dtype=torch.bfloat16, device=cuda_device())
+    q[0, 1] = -1
+    q[0, 2] = 0.01
+    q[0, 3] = 0
+    check_attention(q, c, table, n, scale=0.5)
+    check_attention(q, c, table, n, scale=-0.5)
+    check_attention(q, c, table, n, scale=0.0)
+
+
+def test_attention_lowest_finite_scores():
+    """Scores near the lowest that fp32 holds, all alike: the mean of the values."""
+    c = make_cache(10, 1, 16, 64, "bf16", "bf16")
+    table, n = tables([100], 16, 10)
+    c.k.fill_(-1.0)
+    q = torch.full((1, 2, 64), 2.0 ** 60, dtype=torch.bfloat16, device=cuda_device())
+    out = ck.paged_attention(q, c, table, n, 2.0 ** 60)
+    want, slack = ref.attention(q * 0, c.k, c.v, None, None, table, n, 1.0, 0, 0)
+    ref.assert_within(out, want, slack, "mean")
+
+
+def test_attention_bad_pages():
+    """A visible page outside the cache makes that sequence NaN, and no other."""
+    lens = [100, 100, 100, 100]
+    c = make_cache(28, 2, 16, 128, "bf16", "bf16")
+    table, n = tables(lens, 16, 28)
+    q = rand(4, 4, 128, dtype=torch.bfloat16).to(cuda_device())
+    good = check_attention(q, c, table, n)
+    bad = table.clone()
+    bad[1, 3] = -1
+    bad[2, 6] = 28                       # tokens 96 .. 99
+    out = ck.paged_attention(q, c, bad, n)
+    assert out[1].isnan().all() and out[2].isnan().all()
+    assert torch.equal(out[0], good[0]) and torch.equal(out[3], good[3])
+    out = ck.paged_attention(q, c, bad, n, window=4)         # tokens 96 .. 99 only
+    assert out[2].isnan().all() and not out[1].isnan().any()
+    c8 = make_cache(28, 2, 16, 128, "int8", "bf16")
+    out = ck.paged_attention(q, c8, bad, n)
+    assert out[1].isnan().all() and out[2].isnan().all() and not out[0].isnan().any()
+
+
+def test_attention_lens_outside_the_table():
+    c = make_cache(8, 1, 16, 128, "bf16", "bf16")
+    table, _ = tables([32, 32, 32], 16, 8)
+    q = rand(3, 2, 128, dtype=torch.bfloat16).to(cuda_device())
+    n = torch.tensor([1000, -5, 32], dtype=torch.int32, device=cuda_device())
+    out = check_attention(q, c, table, n)
+    assert (out[1] == 0).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+def test_attention_strides(cache):
+    """[page, head] inner layouts, strided q, out and table: the same bits as contiguous ones."""
+    lens = [70, 9, 300]
+    c = make_cache(40, 4, 16, 128, cache, "bf16", layout="nhd")
+    flat = ck.KVCache(c.k.contiguous(), c.v.contiguous(), *(None if t is None else t.contiguous() for t in (c.k_scale, c.v_scale)))
+    table, n = tables(lens, 16, 40)
+    q = rand(3, 12, 128, dtype=torch.bfloat16).to(cuda_device())
+    want = check_attention(q, flat, table, n)
+    wide = torch.zeros((3, 20, 136), dtype=torch.bfloat16, device=q.device)[:, 3:15, :128]
+    wide.copy_(q)
+    t2 = torch.zeros((3, table.shape[1] + 5), dtype=torch.int32, device=q.device)[:, :table.shape[1]]
+    t2.copy_(table)
+    out = torch.zeros((3, 24, 128), dtype=torch.bfloat16, device=q.device)[:, ::2]
+    got = ck.paged_attention(wide, c, t2, n, out=out)
+    assert got is out and torch.equal(out, want)
+
+
+def test_attention_far_pages():
+    """Rows past 2^31 elements of the cache."""
+    dev = cuda_device()
+    pages = (1 << 31) // (64 * 128) + 4
+    k, v = (torch.zeros((pages, 1, 64, 128), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    k[-2:], v[-2:] = rand(2, 1, 64, 128, dtype=torch.bfloat16).to(dev), rand(2, 1, 64, 128, dtype=torch.bfloat16, seed=4).to(dev)
+    c = ck.KVCache(k, v)
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device=dev)
+    n = torch.tensor([100], dtype=torch.int32, device=dev)
+    q = rand(1, 4, 128, dtype=torch.bfloat16).to(dev)
+    out = ck.paged_attention(q, c, table, n)
+    small = ck.KVCache(k[-2:].contiguous(), v[-2:].contiguous())
+    want, slack = ref.attention(q, small.k, small.v, None, None, table - (pages - 2), n, 128 ** -0.5, 0, 0)
+    ref.assert_within(out, want, slack, "far pages")
+
+
+def test_attention_same_bits_each_call_and_dirty_workspace():
+    lens = [3000, 100, 0]
+    c = make_cache(220, 2, 16, 128, "int8", "bf16")
+    table, n = tables(lens, 16, 220)
+    q = rand(3, 16, 128, dtype=torch.bfloat16).to(cuda_device())
+    ws = ck.paged_attention_workspace(q, c, table)
+    want = check_attention(q, c, table, n)
+    for byte in (0, 255):
+        if ws is not None:
+            ws.fill_(byte)
+        for _ in range(3):
+            assert torch.equal(ck.paged_attention(q, c, table, n, workspace=ws), want)
+
+
+def test_decode_on_a_side_stream_and_in_a_graph():
+    """All three operators captured into one graph, replayed over changed
+    inputs with eager calls between, each replay against the eager result."""
+    dev = cuda_device()
+    q, k, v, qw, kw, pos, table = rope_inputs(4, 8, 2, 128, 128, "bf16", 500)
+    lens = [90, 33, 1, 700]
+    c = make_cache(60, 2, 16, 128, "bf16", "bf16")
+    pt, n = tables(lens, 16, 60)
+    slots = torch.stack([pt[i, (x - 1) // 16].long() * 16 + (x - 1) % 16 for i, x in enumerate(lens)])
+    codes = torch.randint(0, 256, (200, 512), dtype=torch.uint8, device=dev)
+    w = ck.int4_pack(codes, (rand(200, 8).abs() * 0.01).to(torch.bfloat16).to(dev), group=128)
+    ws = ck.paged_attention_workspace(q, c, pt)
+
+    def step():
+        qo, _ = ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=c, slots=slots)
+        o = ck.paged_attention(qo, c, pt, n, workspace=ws)
+        return ck.int4_linear(o.view(4, 1024), w)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first = step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(first, step())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(4):
+        q.copy_(rand(4, 8, 128, dtype=torch.bfloat16, seed=50 + i))
+        v.copy_(rand(4, 2, 128, dtype=torch.bfloat16, seed=60 + i))
+        want = step().clone()
+        torch.cuda.synchronize()
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), i
+
+
+# -------------------------------------------------------------- int4_linear
+
+def int4_inputs(m, n, k, group, zeros, bias, dtype, out_dtype=None, seed=2):
+    dev = cuda_device()
+    g = torch.Generator().manual_seed(seed + m + n + k)
+    codes = torch.randint(0, 256, (n, k // 2), generator=g, dtype=torch.uint8).to(dev)
+    groups = -(-k // group)
+    scales = (0.02 * (0.5 + torch.rand((n, groups), generator=g))).to(DT[dtype]).to(dev)
+    z = torch.randint(0, 16, (n, groups), generator=g, dtype=torch.uint8).to(dev) if zeros else None
+    b = rand(n, dtype=DT[out_dtype or dtype], seed=seed).to(dev) if bias else None
+    return rand(m, k, dtype=DT[dtype], seed=seed).to(dev), codes, scales, z, b
+
+
+@pytest.mark.parametrize("m,n,k,group,zeros,bias,dtype,out", [
+    (1, 64, 128, 128, False, False, "bf16", None),
+    (1, 4096, 4096, 128, False, False, "bf16", None),
+    (1, 1000, 2048, 32, True, True, "fp16", None),
+    (2, 17, 136, 32, True, False, "bf16", "fp32"),
+    (3, 1, 8, 64, True, True, "bf16", None),
+    (5, 33, 1000, 128, True, True, "fp16", "fp32"),
+    (8, 300, 5376, 64, False, True, "bf16", "fp16"),
+    (15, 257, 4104, 128, True, False, "bf16", None),
+    (16, 512, 2048, 32, False, False, "fp16", "bf16"),
+    (17, 272, 2056, 64, True, True, "bf16", None),
+    (33, 1040, 1024, 128, False, True, "fp16", None),
+    (64, 160, 5376, 32, True, True, "bf16", None),
+    (65, 100, 640, 64, True, False, "bf16", "fp32"),
+    (128, 528, 1928, 128, True, True, "bf16", None),
+    (200, 48, 384, 32, False, False, "fp16", None),
+    (513, 80, 256, 128, True, True, "bf16", None),
+])
+def test_int4(m, n, k, group, zeros, bias, dtype, out):
+    x, codes, scales, z, b = int4_inputs(m, n, k, group, zeros, bias, dtype, out)
+    w = ck.int4_pack(codes, scales, z, group=group)
+    got = ck.int4_linear(x, w, b, out_dtype=out)
+    assert got.dtype == DT[out or dtype]
+    want, slack = ref.int4(x, codes, scales, z, b, group)
+    ref.assert_within(got, want, slack, "int4_linear")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m", [1, 16, 40, 130])
+def test_int4_exact_on_whole_numbers(m, group):
+    """Small whole x and scales of powers of two: every sum is exact in fp32, and so is the output."""
+    dev = cuda_device()
+    n, k = 70, 1000
+    _, codes, scales, z, _ = int4_inputs(m, n, k, group, True, False, "bf16")
+    g = torch.Generator().manual_seed(m)
+    x = torch.randint(-3, 4, (m, k), generator=g).to(torch.bfloat16).to(dev)
+    scales = (2.0 ** torch.randint(-2, 2, scales.shape, generator=g)).to(torch.bfloat16).to(dev)
+    got = ck.int4_linear(x, ck.int4_pack(codes, scales, z, group=group), out_dtype="fp32")
+    want, _ = ref.int4(x, codes, scales, z, None, group)
+    assert torch.equal(got.cpu().double(), want)
+
+
+def test_int4_pack_layout():
+    """The layout that include/ck_int8.h gives, word by word."""
+    n, k, group = 37, 200, 64
+    _, codes, scales, z, _ = int4_inputs(1, n, k, group, True, False, "fp16")
+    w = ck.int4_pack(codes, scales, z, group=group)
+    full = torch.zeros((48, 256), dtype=torch.int64)
+    full[:n, :k] = ref.unpack_codes(codes).long()
+    got = w.w.cpu().view(torch.int32).long().view(3, 2, 64, 4) & 0xffffffff
+    lane = torch.arange(64)
+    for e, at in enumerate((0, 4, 1, 5, 2, 6, 3, 7)):        # column e of a word is nibble `at`
+        nib = (got >> (4 * at)) & 15
+        for i in range(4):
+            cols = 32 * i + 8 * (lane // 16) + e
+            for t in range(3):
+                for c in range(2):
+                    assert torch.equal(nib[t, c, :, i], full[16 * t + lane % 16, 128 * c + cols])
+    groups = -(-k // group)
+    ws, wz = torch.zeros((48, groups)), torch.zeros((48, groups), dtype=torch.uint8)
+    ws[:n], wz[:n] = scales.cpu().float(), z.cpu()
+    assert torch.equal(w.scales.cpu().float(), ws.view(3, 16, groups).transpose(1, 2))
+    assert torch.equal(w.zeros.cpu(), wz.view(3, 16, groups).transpose(1, 2))
+
+
+def test_int4_strides_and_empty():
+    """Rows of x and out further apart, strided codes and scales; no rows; no columns of K."""
+    dev = cuda_device()
+    x, codes, scales, z, b = int4_inputs(9, 50, 264, 32, True, True, "bf16")
+    want = ck.int4_linear(x, ck.int4_pack(codes, scales, z, group=32), b)
+    wx = torch.full((9, 320), float("nan"), dtype=torch.bfloat16, device=dev)[:, 16:280]
+    wx.copy_(x)
+    out = torch.full((9, 61), 7.0, dtype=torch.bfloat16, device=dev)
+    wide = [torch.zeros((t.shape[0], t.shape[1] + 5), dtype=t.dtype, device=dev)[:, :t.shape[1]] for t in (codes, scales, z)]
+    for a, t in zip(wide, (codes, scales, z)):
+        a.copy_(t)
+    ck.int4_linear(wx, ck.int4_pack(*wide, group=32), b, out=out[:, 3:53])
+    assert torch.equal(out[:, 3:53], want)
+    assert (out[:, :3] == 7).all() and (out[:, 53:] == 7).all()
+    w = ck.int4_pack(codes, scales, z, group=32)
+    assert ck.int4_linear(x[:0], w).shape == (0, 50)
+    empty = ck.int4_pack(codes[:, :0], scales[:, :0], group=32)
+    got = ck.int4_linear(x[:, :0], empty, b)
+    assert torch.equal(got, b.expand(9, 50))
+
+
+def test_int4_same_bits_each_call():
+    x, codes, scales, z, b = int4_inputs(24, 2000, 4096, 64, True, True, "bf16")
+    w = ck.int4_pack(codes, scales, z, group=64)
+    want = ck.int4_linear(x, w, b)
+    for _ in range(3):
+        assert torch.equal(ck.int4_linear(x, w, b), want)
+
+
+def test_int4_row_results_do_not_depend_on_the_batch_tile():
+    """The rows of a batch within one row tile give the bits that they give on the same kernel in another order."""
+    x, codes, scales, z, b = int4_inputs(16, 300, 1024, 128, True, True, "bf16")
+    w = ck.int4_pack(codes, scales, z, group=128)
+    order = torch.randperm(16, generator=torch.Generator().manual_seed(1)).to(x.device)
+    assert torch.equal(ck.int4_linear(x[order].contiguous(), w, b), ck.int4_linear(x, w, b)[order])
