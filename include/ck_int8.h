@@ -444,7 +444,9 @@ typedef enum {
  * and the same for v, which has the same strides.  In an int8 cache such a
  * row is codes (-127 .. 127) times the row's scale,
  *   k_scale[p * scale_page_stride + h * scale_head_stride + t * scale_token_stride]
- * (v_scale alike), the codes and scale of ck_quantize_int8_rowwise.
+ * (v_scale alike).  ck_qk_norm_rope writes such rows with
+ *   s = amax * (1 / 127)  (two fp32 roundings; amax = max |x| over the row),
+ *   code = clamp(rint(x / s), -127, 127), 0 for s == 0.
  *
  * dtype       ck_dtype of the rows; a 16-bit cache has the activations' type.
  * page_size   tokens per page, a power of two from 1 to 32768.

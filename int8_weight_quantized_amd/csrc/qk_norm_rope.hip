@@ -48,6 +48,29 @@ __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
+// The sum of a row's d terms, eight a lane, in one particular order.  Below
+// 128 terms: those 64 apart, then neighbours, pairs of neighbours and so on.
+// From 128 on: those 128 (256 from d = 256 on) apart, then each four in
+// sequence, then neighbouring fours and so on.  It is the order in which
+// torch sums such rows on this device; with the root rounded from 64 bits, as
+// torch's is, the key codes of an int8 cache, which jump where a value lies
+// between two of them, are those of the same formula in torch operations.
+template <int L>
+__device__ __forceinline__ float group_sum_ordered(const float (&x)[8], int d)
+{
+    const bool fours = L >= 16 && d >= 128;
+    const int fold = L == 16 ? (fours ? 0 : 8) : L == 32 ? (d >= 256 ? 0 : 16) : L == 64 ? 32 : 0;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fold ? x[i] + __shfl_xor(x[i], fold) : x[i];
+    float sum = fours ? (((v[0] + v[1]) + v[2]) + v[3]) + (((v[4] + v[5]) + v[6]) + v[7])
+                      : ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+    for (int off = 1; off < L; off *= 2)
+        if (fold == 0 || off < fold) sum = sum + __shfl_xor(sum, off);
+    return sum;
+}
+
 template <int L>
 __device__ __forceinline__ float group_max(float v)
 {
@@ -124,9 +147,18 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a)
     }
     if (w) {
         float sum = 0.0f;
+        if constexpr (I8) {
+            float sq[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[i], y[i], sum);
-        const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(group_sum<L>(sum), a.inv_d, a.eps));
+            for (int i = 0; i < 8; ++i) sq[i] = y[i] * y[i];
+            sum = group_sum_ordered<L>(sq, a.d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[i], y[i], sum);
+            sum = group_sum<L>(sum);
+        }
+        const float mean = sum * a.inv_d + a.eps;
+        const float r = I8 ? (float)(1.0 / __builtin_sqrt((double)mean)) : rsqrtf(mean);
         float f[8];
         if (in) {
             load8(w + e0, f);
@@ -144,13 +176,13 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a)
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 const float u = y[i], v = y[i + 1];
-                y[i] = __builtin_fmaf(u, c[i], -(v * s[i]));
-                y[i + 1] = __builtin_fmaf(v, c[i], u * s[i]);
+                y[i] = u * c[i] - v * s[i];
+                y[i + 1] = v * c[i] + u * s[i];
             }
         } else {
             // first half: y c - other s; second half: y c + other s
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(y[i], c[i], second ? other[i] * s[i] : -(other[i] * s[i]));
+            for (int i = 0; i < 8; ++i) y[i] = y[i] * c[i] + (second ? other[i] * s[i] : -(other[i] * s[i]));
         }
     }
 
@@ -171,7 +203,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs a)
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = fmaxf(m, __builtin_fabsf(y[i]));
-        const float scale = group_max<L>(in ? m : 0.0f) / 127.0f;
+        const float scale = group_max<L>(in ? m : 0.0f) * (1.0f / 127.0f);
         uint32_t word[2] = {0u, 0u};
 #pragma unroll
         for (int i = 0; i < 8; ++i) word[i >> 2] |= (uint32_t)(quant_code(y[i], scale) & 0xff) << (8 * (i & 3));

@@ -73,7 +73,7 @@ def test_rope(tokens, hq, hk, d, rot, interleaved, dtype, cache, page, norm):
         scale = sc.cpu().transpose(1, 2).reshape(pages * page, hk)[slots[used]].double()
         if name == "v":                  # given values: the row quantisation's codes and scales, bit for bit
             x = v.cpu()[used].float()
-            scales = x.abs().amax(-1) / 127
+            scales = x.abs().amax(-1) * (torch.ones(()) / 127)
             assert torch.equal(scale, scales.double())
             assert torch.equal(got, torch.round(x / scales[..., None]).clamp(-127, 127).to(torch.int8))
             continue
@@ -86,17 +86,29 @@ def test_rope(tokens, hq, hk, d, rot, interleaved, dtype, cache, page, norm):
         assert got.abs().max() <= 127
 
 
-def test_rope_int8_values_are_the_row_quantisation():
-    """The values of an int8 cache are ck_quantize_int8_rowwise's codes and scales, bit for bit."""
+@pytest.mark.parametrize("hk,d,rot,interleaved", [(8, 96, 96, False), (4, 128, 64, True), (2, 64, 64, False),
+                                                  (8, 192, 192, False), (8, 256, 128, True)])
+def test_rope_int8_codes_are_the_formulas(hk, d, rot, interleaved):
+    """An int8 cache's codes and scales, keys' and values', are bit for bit
+    those of the same formula in fp32 torch operations on this device; a row
+    of zeros has scale 0 and codes 0."""
     dev = cuda_device()
-    q, k, v, qw, kw, pos, table = rope_inputs(37, 4, 2, 128, 128, "bf16", 100)
+    q, k, v, qw, kw, pos, table = rope_inputs(40, 4, hk, d, rot, "bf16", 100)
     v[5, 1] = 0
-    c = ck.KVCache.empty(5, 2, 8, 128, "int8", dev)
-    ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=c, slots=torch.arange(37, device=dev))
-    codes, scales = ck.quantize_int8_rowwise(v.reshape(-1, 128).contiguous())
-    flat = c.v.transpose(1, 2).reshape(40, 2, 128)[:37]
-    assert torch.equal(flat.reshape(-1, 128), codes)
-    assert torch.equal(c.v_scale.transpose(1, 2).reshape(40, 2)[:37].reshape(-1), scales)
+    k[6, 0] = 0
+    c = ck.KVCache.empty(5, hk, 8, d, "int8", dev)
+    ck.qk_norm_rope(q, k, v, pos, table, qw, kw, interleaved=interleaved, cache=c, slots=torch.arange(40, device=dev))
+    y = k.float()
+    y = y * torch.rsqrt((y * y).mean(-1, keepdim=True) + 1e-6) * kw
+    cos, sin = table[pos][:, None].split(rot // 2, -1)
+    x, z = (y[..., 0:rot:2], y[..., 1:rot:2]) if interleaved else (y[..., :rot // 2], y[..., rot // 2:rot])
+    turned = x * cos - z * sin, z * cos + x * sin
+    turned = torch.stack(turned, -1).flatten(-2) if interleaved else torch.cat(turned, -1)
+    for got, scale, y in ((c.k, c.k_scale, torch.cat([turned, y[..., rot:]], -1)), (c.v, c.v_scale, v.float())):
+        s = y.abs().amax(-1) * (torch.ones((), device=dev) / 127)
+        codes = torch.where(s[..., None] > 0, torch.round(y / s[..., None]), torch.zeros_like(y))
+        assert torch.equal(scale.transpose(1, 2).reshape(40, hk), s)
+        assert torch.equal(got.transpose(1, 2).reshape(40, hk, d), codes.clamp(-127, 127).to(torch.int8))
 
 
 def test_rope_in_place_and_queries_alone():
@@ -145,9 +157,10 @@ def test_rope_far_cache_rows():
     q, k, v, qw, kw, pos, table = rope_inputs(2, 1, 1, 128, 128, "bf16", 64)
     slots = torch.tensor([pages * 16 - 1, 0], device=dev)
     ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=c, slots=slots)
-    codes, scales = ck.quantize_int8_rowwise(v.reshape(2, 128).contiguous())
-    assert torch.equal(c.v[-1, 0, 15], codes[0]) and torch.equal(c.v[0, 0, 0], codes[1])
-    assert c.v_scale[-1, 0, 15] == scales[0] and c.k_scale[-1, 0, 15] > 0
+    near = ck.KVCache.empty(1, 1, 2, 128, "int8", dev)
+    ck.qk_norm_rope(q, k, v, pos, table, qw, kw, cache=near, slots=torch.arange(2, device=dev))
+    for far, t in ((c.k, near.k), (c.v, near.v), (c.k_scale, near.k_scale), (c.v_scale, near.v_scale)):
+        assert torch.equal(far[-1, 0, 15], t[0, 0, 0]) and torch.equal(far[0, 0, 0], t[0, 0, 1])
     assert int((c.v_scale != 0).sum()) == 2
 
 
