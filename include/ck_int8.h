@@ -427,7 +427,9 @@ ck_status ck_mfma_ceiling(int64_t iters, int mode, int32_t* out, uint32_t seed, 
  * between its projections.  Together they are one attention block's decode
  * step: the query/key/value projection (above), ck_qk_norm_rope into a paged
  * cache, ck_paged_attention over it, and an output projection
- * (ck_int8_layer, or ck_int4_linear with 4-bit weights).
+ * (ck_int8_layer, or ck_int4_linear with 4-bit weights).  Their many
+ * arguments come in structures, which are read before the call returns.  The
+ * stride of a dimension with one element is not looked at.
  */
 
 /* Element type of activations (16-bit) and of a paged cache. */
@@ -605,10 +607,19 @@ ck_status ck_int4_pack(const uint8_t* codes, int64_t ldc, const uint16_t* scales
  * out      [out] [m, ldo] of out_dtype.
  * m == 0 or n == 0 is a no-op; k == 0 gives the bias (or 0).
  */
-ck_status ck_int4_linear(const void* x, int64_t ldx, ck_dtype dtype, const uint8_t* w,
-                         const uint16_t* w_scale, const uint8_t* w_zero, const void* bias, void* out,
-                         int64_t ldo, ck_out_dtype out_dtype, int64_t m, int64_t n, int64_t k,
-                         int64_t group, hipStream_t stream);
+typedef struct {
+    const void* x;
+    const uint8_t* w;
+    const uint16_t* w_scale;
+    const uint8_t* w_zero;
+    const void* bias;
+    void* out;
+    int64_t ldx, ldo, m, n, k, group;
+    int32_t dtype;          /* of x: CK_DT_BF16 or CK_DT_FP16 */
+    int32_t out_dtype;      /* ck_out_dtype */
+} ck_int4_args;
+
+ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
 
 /* Name of a status code (static string). */
 const char* ck_status_string(ck_status s);

@@ -69,6 +69,13 @@ class CkQkArgs(ctypes.Structure):
                        (ctypes.c_int32, "dtype interleaved reserved"))
 
 
+class CkInt4Args(ctypes.Structure):
+    """ck_int4_args of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "x w w_scale w_zero bias out"),
+                       (ctypes.c_int64, "ldx ldo m n k group"),
+                       (ctypes.c_int32, "dtype out_dtype"))
+
+
 class CkAttentionArgs(ctypes.Structure):
     """ck_attention_args of include/ck_int8.h."""
     _fields_ = _fields((ctypes.c_void_p, "q out table lens workspace"),
@@ -147,7 +154,7 @@ def lib():
     L.ck_paged_attention_workspace.restype = i64
     L.ck_int4_pack.argtypes = [p, i64, p, i64, p, i64, p, p, p, i64, i64, i64, p]
     L.ck_int4_pack.restype = ci
-    L.ck_int4_linear.argtypes = [p, i64, ci, p, p, p, p, p, i64, ci, i64, i64, i64, i64, p]
+    L.ck_int4_linear.argtypes = [p, p]
     L.ck_int4_linear.restype = ci
     L.ck_status_string.argtypes = [ci]
     L.ck_status_string.restype = ctypes.c_char_p
@@ -222,15 +229,25 @@ def ck_int8_gemm_i32(q, ldq, w, ldw, acc, ldacc, m, n, k, tile=-1, stream=0):
            "ck_int8_gemm_i32")
 
 
+# The structures of the next three (ck_*_args and ck_kv_cache) come as ctypes
+# structures by reference or as the bytes of one; a cache also as its address.
+
 def ck_qk_norm_rope(args, cache=None, stream=0):
-    """args a CkQkArgs, cache a CkKvCache or None."""
-    _check(lib().ck_qk_norm_rope(ctypes.byref(args), None if cache is None else ctypes.byref(cache), stream),
-           "ck_qk_norm_rope")
+    s = (_lib or lib()).ck_qk_norm_rope(args, cache, stream)
+    if s:
+        _check(s, "ck_qk_norm_rope")
 
 
 def ck_paged_attention(args, cache, stream=0):
-    """args a CkAttentionArgs, cache a CkKvCache."""
-    _check(lib().ck_paged_attention(ctypes.byref(args), ctypes.byref(cache), stream), "ck_paged_attention")
+    s = (_lib or lib()).ck_paged_attention(args, cache, stream)
+    if s:
+        _check(s, "ck_paged_attention")
+
+
+def ck_int4_linear(args, stream=0):
+    s = (_lib or lib()).ck_int4_linear(args, stream)
+    if s:
+        _check(s, "ck_int4_linear")
 
 
 def ck_paged_attention_workspace(batch, hq, hk, head_dim, table_width, page_size, window=0, sinks=0) -> int:
@@ -240,11 +257,6 @@ def ck_paged_attention_workspace(batch, hq, hk, head_dim, table_width, page_size
 def ck_int4_pack(codes, ldc, scales, lds, zeros, ldz, w, w_scale, w_zero, n, k, group, stream=0):
     _check(lib().ck_int4_pack(codes, ldc, scales, lds, zeros, ldz, w, w_scale, w_zero, n, k, group, stream),
            "ck_int4_pack")
-
-
-def ck_int4_linear(x, ldx, dtype, w, w_scale, w_zero, bias, out, ldo, out_dtype, m, n, k, group, stream=0):
-    _check(lib().ck_int4_linear(x, ldx, dtype, w, w_scale, w_zero, bias, out, ldo, out_dtype, m, n, k, group,
-                                stream), "ck_int4_linear")
 
 
 def ck_hbm_stream(src, chunks, dst, blocks, unroll, stream=0):

@@ -35,6 +35,13 @@ int ilog2(int64_t v)
     return l;
 }
 
+// 16-bit rows of a [tokens, heads, head_dim] tensor that start 16 bytes apart
+// (the stride of a dimension with one element is not looked at).
+bool rows16(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t hs)
+{
+    return aligned(p, 16) && (tokens <= 1 || ts % 8 == 0) && (heads <= 1 || hs % 8 == 0);
+}
+
 // A paged cache for activations of type dtype; `align` bytes between rows.
 ck_status check_cache(const ck_kv_cache* c, int dtype, int64_t head_dim, int align)
 {
@@ -52,8 +59,8 @@ ck_status check_cache(const ck_kv_cache* c, int dtype, int64_t head_dim, int ali
     if (c->page_size > 1 && c->token_stride < head_dim)
         return fail(CK_ERR_INVALID_ARG, "token_stride smaller than head_dim");
     const int esz = c->dtype == CK_DT_INT8 ? 1 : 2;
-    if (!aligned(c->k, align) || !aligned(c->v, align) || c->page_stride * esz % align != 0 ||
-        c->head_stride * esz % align != 0 || c->token_stride * esz % align != 0)
+    if (!aligned(c->k, align) || !aligned(c->v, align) || (c->pages > 1 && c->page_stride * esz % align != 0) ||
+        (c->heads > 1 && c->head_stride * esz % align != 0) || (c->page_size > 1 && c->token_stride * esz % align != 0))
         return fail(CK_ERR_UNSUPPORTED, "cache rows must start %d bytes apart", align);
     if (c->dtype == CK_DT_INT8) {
         if (c->pages > 0 && (!c->k_scale || !c->v_scale))

@@ -336,40 +336,40 @@ extern "C" ck_status ck_int4_pack(const uint8_t* codes, int64_t ldc, const uint1
     return s == CK_OK ? ok() : s;
 }
 
-extern "C" ck_status ck_int4_linear(const void* x, int64_t ldx, ck_dtype dtype, const uint8_t* w,
-                                    const uint16_t* w_scale, const uint8_t* w_zero, const void* bias, void* out,
-                                    int64_t ldo, ck_out_dtype out_dtype, int64_t m, int64_t n, int64_t k,
-                                    int64_t group, hipStream_t stream)
+extern "C" ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream)
 {
-    if (dtype != CK_DT_BF16 && dtype != CK_DT_FP16) return fail(CK_ERR_INVALID_ARG, "bad dtype");
-    if (out_dtype != CK_OUT_BF16 && out_dtype != CK_OUT_FP16 && out_dtype != CK_OUT_FP32)
+    if (!args) return fail(CK_ERR_INVALID_ARG, "NULL args");
+    const ck_int4_args& p = *args;
+    if (p.dtype != CK_DT_BF16 && p.dtype != CK_DT_FP16) return fail(CK_ERR_INVALID_ARG, "bad dtype");
+    if (p.out_dtype != CK_OUT_BF16 && p.out_dtype != CK_OUT_FP16 && p.out_dtype != CK_OUT_FP32)
         return fail(CK_ERR_INVALID_ARG, "bad out_dtype");
-    if (m < 0) return fail(CK_ERR_INVALID_ARG, "negative size");
-    ck_status s = check_int4_sizes(n, k, group);
+    if (p.m < 0) return fail(CK_ERR_INVALID_ARG, "negative size");
+    ck_status s = check_int4_sizes(p.n, p.k, p.group);
     if (s != CK_OK) return s;
-    if (m == 0 || n == 0) return ok();
-    if (!out) return fail(CK_ERR_INVALID_ARG, "NULL out");
-    if (ldo < n) return fail(CK_ERR_INVALID_ARG, "ldo smaller than n");
-    if (k > 0) {
-        if (!x || !w || !w_scale) return fail(CK_ERR_INVALID_ARG, "NULL x, w or w_scale");
-        if (ldx < k) return fail(CK_ERR_INVALID_ARG, "ldx smaller than k");
-        if (ldx % 8 != 0 || !aligned(x, 16))
+    if (p.m == 0 || p.n == 0) return ok();
+    if (!p.out) return fail(CK_ERR_INVALID_ARG, "NULL out");
+    if (p.m > 1 && p.ldo < p.n) return fail(CK_ERR_INVALID_ARG, "ldo smaller than n");
+    if (p.k > 0) {
+        if (!p.x || !p.w || !p.w_scale) return fail(CK_ERR_INVALID_ARG, "NULL x, w or w_scale");
+        if (p.m > 1 && p.ldx < p.k) return fail(CK_ERR_INVALID_ARG, "ldx smaller than k");
+        if ((p.m > 1 && p.ldx % 8 != 0) || !aligned(p.x, 16))
             return fail(CK_ERR_UNSUPPORTED, "x rows must start 16 bytes apart (ldx %% 8 == 0)");
     }
-    const int esz = out_dtype == CK_OUT_FP32 ? 4 : 2;
-    if (!aligned(w, 16) || !aligned(w_scale, 16) || !aligned(w_zero, 16) || !aligned(out, esz) ||
-        (bias && !aligned(bias, esz)))
+    const int esz = p.out_dtype == CK_OUT_FP32 ? 4 : 2;
+    if (!aligned(p.w, 16) || !aligned(p.w_scale, 16) || !aligned(p.w_zero, 16) || !aligned(p.out, esz) ||
+        (p.bias && !aligned(p.bias, esz)))
         return fail(CK_ERR_UNSUPPORTED, "misaligned w, w_scale, w_zero, bias or out");
     // 32-bit offsets of a block's rows of x
-    if (64 * ldx >= (int64_t(1) << 31)) return fail(CK_ERR_UNSUPPORTED, "rows of x too long for 32-bit offsets");
-    if ((s = check_device()) != CK_OK) return s;
-    Int4Args a{(const uint16_t*)x, w, w_scale, w_zero, bias, out, ldx, ldo, m, n, k, cdiv(k, 128), cdiv(k, group),
-               out_dtype};
-    const Int4Plan p = int4_plan(dtype, m, n, group);
-    const int64_t bx = cdiv(cdiv(n, 16), p.tiles), by = cdiv(m, p.rows);
+    if (p.m > 1 && 64 * p.ldx >= (int64_t(1) << 31))
+        return fail(CK_ERR_UNSUPPORTED, "rows of x too long for 32-bit offsets");
+    const Int4Plan plan = int4_plan(p.dtype, p.m, p.n, p.group);
+    const int64_t bx = cdiv(cdiv(p.n, 16), plan.tiles), by = cdiv(p.m, plan.rows);
     if (by > 65535) return fail(CK_ERR_UNSUPPORTED, "too many rows");
+    if ((s = check_device()) != CK_OK) return s;
+    Int4Args a{(const uint16_t*)p.x, p.w, p.w_scale, p.w_zero, p.bias, p.out, p.ldx, p.ldo, p.m, p.n, p.k,
+               cdiv(p.k, 128), cdiv(p.k, p.group), p.out_dtype};
     void* kargs[] = {&a};
-    hipError_t e = hipLaunchKernel(p.fn, dim3((unsigned)bx, (unsigned)by), dim3(64 * p.waves), kargs, 0, stream);
+    hipError_t e = hipLaunchKernel(plan.fn, dim3((unsigned)bx, (unsigned)by), dim3(64 * plan.waves), kargs, 0, stream);
     if (e != hipSuccess) return fail(CK_ERR_HIP, "int4_linear launch: %s", hipGetErrorString(e));
     return ok();
 }

@@ -603,7 +603,8 @@ extern "C" ck_status ck_paged_attention(const ck_attention_args* args, const ck_
         return fail(CK_ERR_UNSUPPORTED, "too large a batch, table or number of heads");
     if (!p.q || !p.out || !p.lens || (!p.table && p.table_width > 0))
         return fail(CK_ERR_INVALID_ARG, "NULL q, out, table or lens");
-    if (!rows16(p.q, p.q_batch_stride, p.q_head_stride) || !rows16(p.out, p.out_batch_stride, p.out_head_stride))
+    if (!rows16(p.q, p.batch, p.q_batch_stride, p.hq, p.q_head_stride) ||
+        !rows16(p.out, p.batch, p.out_batch_stride, p.hq, p.out_head_stride))
         return fail(CK_ERR_UNSUPPORTED, "q and out rows must start 16 bytes apart");
     if (!aligned(p.table, 4) || !aligned(p.lens, 4)) return fail(CK_ERR_UNSUPPORTED, "misaligned table or lens");
     if (p.table_stride < p.table_width && p.batch > 1) return fail(CK_ERR_INVALID_ARG, "table_stride smaller than table_width");

@@ -234,9 +234,6 @@ const void* qk_fn(int lanes, bool i8, bool pairs)
     return pairs ? qk_fn_lanes<DT, false, true>(lanes) : qk_fn_lanes<DT, false, false>(lanes);
 }
 
-// 16-bit rows of [tokens, heads, head_dim] that start 16 bytes apart.
-bool rows16(const void* p, int64_t ts, int64_t hs) { return aligned(p, 16) && ts % 8 == 0 && hs % 8 == 0; }
-
 }  // namespace
 
 extern "C" ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipStream_t stream)
@@ -265,11 +262,11 @@ extern "C" ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* 
     if (p.rot > 0 && (!p.positions || (!p.cos_sin && p.table_rows > 0)))
         return fail(CK_ERR_INVALID_ARG, "NULL positions or cos_sin");
     if (p.rot > 0 && p.table_rows == 0) return fail(CK_ERR_INVALID_ARG, "empty cos_sin");
-    if ((p.hq > 0 && (!rows16(p.q, p.q_token_stride, p.q_head_stride) ||
-                      !rows16(p.q_out, p.q_out_token_stride, p.q_out_head_stride))) ||
-        (p.hk > 0 && (!rows16(p.k, p.k_token_stride, p.k_head_stride) ||
-                      (p.k_out && !rows16(p.k_out, p.k_out_token_stride, p.k_out_head_stride)))) ||
-        (cache && !rows16(p.v, p.v_token_stride, p.v_head_stride)))
+    if ((p.hq > 0 && (!rows16(p.q, p.tokens, p.q_token_stride, p.hq, p.q_head_stride) ||
+                      !rows16(p.q_out, p.tokens, p.q_out_token_stride, p.hq, p.q_out_head_stride))) ||
+        (p.hk > 0 && (!rows16(p.k, p.tokens, p.k_token_stride, p.hk, p.k_head_stride) ||
+                      (p.k_out && !rows16(p.k_out, p.tokens, p.k_out_token_stride, p.hk, p.k_out_head_stride)))) ||
+        (cache && !rows16(p.v, p.tokens, p.v_token_stride, p.hk, p.v_head_stride)))
         return fail(CK_ERR_UNSUPPORTED, "q, k, v and out rows must start 16 bytes apart");
     if (!aligned(p.cos_sin, 16) || !aligned(p.q_weight, 16) || !aligned(p.k_weight, 16) ||
         !aligned(p.positions, 8) || !aligned(p.slots, 8))

@@ -10,17 +10,43 @@ current stream; every step runs in the library's HIP kernels.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
+import struct
+
 import int8_weight_quantized_amd as _ck
+
+# A decode call lasts a few microseconds on the GPU, so these helpers keep the
+# host's part short: the checks are one condition over the arguments, and
+# only where it does not hold does the second, slower pass go through them one
+# by one to raise what is wrong.  The library's argument structures are packed
+# as bytes.  (torch is imported on first use, as everywhere in this package.)
+
+_QK = struct.Struct("10Q16qf3i4x")
+_ATTENTION = struct.Struct("5Q11qfi")
+_INT4 = struct.Struct("6Q6q2i")
+_torch = None
+_code16 = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _code16.update({torch.bfloat16: _ck.CK_DT_BF16, torch.float16: _ck.CK_DT_FP16})
+    _torch = torch
+    return torch
+
+
+def _stream(index):
+    """The current stream of CUDA device `index`."""
+    return _torch._C._cuda_getCurrentRawStream(index)
 
 
 def _dtype16(t, name):
     """CK_DT_* of a 16-bit floating tensor."""
-    import torch
-    if isinstance(t, torch.Tensor):
-        if t.dtype == torch.bfloat16:
-            return _ck.CK_DT_BF16
-        if t.dtype == torch.float16:
-            return _ck.CK_DT_FP16
+    torch = _torch or _load_torch()
+    if isinstance(t, torch.Tensor) and t.dtype in _code16:
+        return _code16[t.dtype]
     raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
 
 
@@ -78,6 +104,7 @@ class KVCache:
         self.struct = _ck.CkKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if int8 else 0,
                                     v_scale.data_ptr() if int8 else 0, pages, page_size, heads, d,
                                     *_strides(k)[:3], *ss, code, 0)
+        self.address = ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, pages, heads, page_size, head_dim, dtype="bf16", device="cuda"):
@@ -120,36 +147,79 @@ def qk_norm_rope(q, k, v, positions, cos_sin, q_weight=None, k_weight=None, eps:
     none); keys also go to k_out when it is given or there is no cache.
     q_out = q and k_out = k work in place.
     -> (q_out, k_out or None)."""
+    torch = _torch or _load_torch()
+    try:
+        tt, dev, (tokens, hq, d), qs = q.dtype, q.device, q.shape, q.stride()
+        good = q.is_cuda and tt in _code16 and qs[2] == 1
+        hk = kp = vp = pp = tp = sp = rot = rows = 0
+        ks = vs = (0, 0)
+        if k is not None:
+            hk, ks, kp = k.shape[1], k.stride(), k.data_ptr()
+            good = good and k.dtype is tt and k.device == dev and k.shape == (tokens, hk, d) and ks[2] == 1
+        if cos_sin is not None:
+            (rows, rot), pp, tp = cos_sin.shape, positions.data_ptr(), cos_sin.data_ptr()
+            good = (good and cos_sin.dtype is torch.float32 and cos_sin.device == dev and cos_sin.is_contiguous()
+                    and positions.dtype is torch.int64 and positions.device == dev and positions.shape == (tokens,)
+                    and positions.is_contiguous())
+        if cache is not None:
+            vs, vp, sp = v.stride(), v.data_ptr(), slots.data_ptr()
+            good = (good and kp and type(cache) is KVCache and cache.device == dev and v.dtype is tt and v.device == dev
+                    and v.shape == (tokens, hk, d) and vs[2] == 1 and slots.dtype is torch.int64
+                    and slots.device == dev and slots.shape == (tokens,) and slots.is_contiguous())
+        qw = kw = 0
+        if q_weight is not None:
+            qw = q_weight.data_ptr()
+            good = (good and q_weight.dtype is torch.float32 and q_weight.device == dev and q_weight.shape == (d,)
+                    and q_weight.is_contiguous())
+        if k_weight is not None:
+            kw = k_weight.data_ptr()
+            good = (good and k_weight.dtype is torch.float32 and k_weight.device == dev and k_weight.shape == (d,)
+                    and k_weight.is_contiguous())
+        good = good and q_out is None and k_out is None and (kp or (v is None and cache is None))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_qk(q, k, v, positions, cos_sin, q_weight, k_weight, cache, slots, q_out, k_out)
+        hk = 0 if k is None else k.shape[1]
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k_out is None and cache is None and k is not None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    os = q_out.stride()
+    kop, kos = (0, vs) if k_out is None else (k_out.data_ptr(), k_out.stride())
+    args = _QK.pack(q.data_ptr(), kp, vp, pp, tp, qw, kw, q_out.data_ptr(), kop, sp, qs[0], qs[1], ks[0], ks[1],
+                    vs[0], vs[1], os[0], os[1], kos[0], kos[1], tokens, hq, hk, d, rot, rows, eps, _code16[tt],
+                    1 if interleaved else 0, 0)
+    _ck.ck_qk_norm_rope(args, None if cache is None else cache.address, _stream(dev.index))
+    return q_out, k_out
+
+
+def _check_qk(q, k, v, positions, cos_sin, q_weight, k_weight, cache, slots, q_out, k_out):
+    """Every check of qk_norm_rope's arguments, one by one."""
     import torch
-    dt = _dtype16(q, "q")
+    _dtype16(q, "q")
     _ck._need(q, q.dtype, "q")
     if q.dim() != 3:
         raise ValueError("q must be 3-D [tokens, heads, head_dim]")
     dev, tt = q.device, q.dtype
     tokens, hq, d = q.shape
+    hk = 0
     if k is None:
         if v is not None or cache is not None or k_out is not None:
             raise ValueError("without k there is no v, cache or k_out")
-        hk = 0
     else:
         if not isinstance(k, torch.Tensor) or k.dim() != 3:
             raise ValueError("k must be 3-D [tokens, heads, head_dim]")
         hk = k.shape[1]
         _need_heads(k, tt, "k", tokens, hk, d, dev)
-    ws = []
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             _ck._need_vector(w, torch.float32, name, (d,), dev)
-        ws.append(0 if w is None else w.data_ptr())
-    rot = rows = pos_p = table_p = 0
     if cos_sin is not None:
         _ck._need(cos_sin, torch.float32, "cos_sin", dev)
         if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous [rows, rot] tensor")
-        rows, rot = cos_sin.shape
         _ck._need_vector(positions, torch.int64, "positions", (tokens,), dev)
-        pos_p, table_p = positions.data_ptr(), cos_sin.data_ptr()
-    vp = vt = vh = sp = 0
     if cache is not None:
         if not isinstance(cache, KVCache):
             raise TypeError("cache must be a KVCache")
@@ -159,37 +229,25 @@ def qk_norm_rope(q, k, v, positions, cos_sin, q_weight=None, k_weight=None, eps:
             raise ValueError("a cache needs v and slots")
         _need_heads(v, tt, "v", tokens, hk, d, dev)
         _ck._need_vector(slots, torch.int64, "slots", (tokens,), dev)
-        vp, sp = v.data_ptr(), slots.data_ptr()
-        vt, vh, _ = _strides(v)
-    if q_out is None:
-        q_out = torch.empty((tokens, hq, d), dtype=tt, device=dev)
-    else:
+    if q_out is not None:
         _need_heads(q_out, tt, "q_out", tokens, hq, d, dev)
-    kp = kt = kh = kop = kot = koh = 0
-    if k is not None:
-        kp, (kt, kh, _) = k.data_ptr(), _strides(k)
-        if k_out is not None:
-            _need_heads(k_out, tt, "k_out", tokens, hk, d, dev)
-        elif cache is None:
-            k_out = torch.empty((tokens, hk, d), dtype=tt, device=dev)
-        if k_out is not None:
-            kop, (kot, koh, _) = k_out.data_ptr(), _strides(k_out)
-    args = _ck.CkQkArgs(q.data_ptr(), kp, vp, pos_p, table_p, ws[0], ws[1], q_out.data_ptr(), kop, sp,
-                        *_strides(q)[:2], kt, kh, vt, vh, *_strides(q_out)[:2], kot, koh,
-                        tokens, hq, hk, d, rot, rows, eps, dt, 1 if interleaved else 0, 0)
-    _ck.ck_qk_norm_rope(args, None if cache is None else cache.struct, _ck._stream(q))
-    return q_out, k_out
+    if k_out is not None:
+        _need_heads(k_out, tt, "k_out", tokens, hk, d, dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(batch, hq, hk, d, width, page_size, window, sinks):
+    return _ck.ck_paged_attention_workspace(batch, hq, hk, d, width, page_size, window, sinks)
 
 
 def paged_attention_workspace(q, cache, table, window: int = 0, sinks: int = 0):
     """A workspace tensor for paged_attention calls of these shapes (or None
     if they need none): one per stream, kept for any number of calls."""
-    import torch
-    n = _ck.ck_paged_attention_workspace(q.shape[0], q.shape[1], cache.heads, cache.head_dim, table.shape[1],
-                                         cache.page_size, window, sinks)
+    n = _workspace_bytes(q.shape[0], q.shape[1], cache.heads, cache.head_dim, table.shape[1], cache.page_size,
+                         window, sinks)
     if n < 0:
         raise ValueError("sizes that paged_attention does not take")
-    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    return q.new_empty(n, dtype=(_torch or _load_torch()).uint8) if n else None
 
 
 def paged_attention(q, cache, table, lens, scale=None, window: int = 0, sinks: int = 0, out=None, workspace=None):
@@ -201,8 +259,36 @@ def paged_attention(q, cache, table, lens, scale=None, window: int = 0, sinks: i
     defaults to d ** -0.5.  With window > 0 only the last `window` and the
     first `sinks` tokens are visible.  workspace: from
     paged_attention_workspace; allocated here when None.  -> [batch, hq, d]."""
+    torch = _torch or _load_torch()
+    try:
+        tt, dev, (batch, hq, d), qs, (rows, width) = q.dtype, q.device, q.shape, q.stride(), table.shape
+        ts = table.stride()
+        good = (q.is_cuda and tt in _code16 and qs[2] == 1 and type(cache) is KVCache and cache.device == dev
+                and d == cache.head_dim and rows == batch and table.dtype is torch.int32 and table.device == dev
+                and (ts[1] == 1 or width <= 1) and lens.dtype is torch.int32 and lens.device == dev
+                and lens.shape == (batch,) and lens.is_contiguous() and out is None and workspace is None
+                and window >= 0 and sinks >= 0)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_attention(q, cache, table, lens, window, sinks, out, workspace)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if workspace is None:
+        workspace = paged_attention_workspace(q, cache, table, window, sinks)
+    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    os = out.stride()
+    args = _ATTENTION.pack(q.data_ptr(), out.data_ptr(), table.data_ptr(), lens.data_ptr(), wp, wn, qs[0], qs[1],
+                           os[0], os[1], ts[0], batch, hq, width, window, sinks,
+                           d ** -0.5 if scale is None else scale, _code16[tt])
+    _ck.ck_paged_attention(args, cache.address, _stream(dev.index))
+    return out
+
+
+def _check_attention(q, cache, table, lens, window, sinks, out, workspace):
+    """Every check of paged_attention's arguments, one by one."""
     import torch
-    dt = _dtype16(q, "q")
+    _dtype16(q, "q")
     _ck._need(q, q.dtype, "q")
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
@@ -218,20 +304,12 @@ def paged_attention(q, cache, table, lens, scale=None, window: int = 0, sinks: i
     _ck._need_vector(lens, torch.int32, "lens", (batch,), dev)
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
-    if out is None:
-        out = torch.empty((batch, hq, d), dtype=q.dtype, device=dev)
-    else:
+    if out is not None:
         _need_heads(out, q.dtype, "out", batch, hq, d, dev)
-    if workspace is None:
-        workspace = paged_attention_workspace(q, cache, table, window, sinks)
-    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-        raise TypeError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    args = _ck.CkAttentionArgs(q.data_ptr(), out.data_ptr(), table.data_ptr(), lens.data_ptr(), wp, wn,
-                               *_strides(q)[:2], *_strides(out)[:2], table.stride(0), batch, hq,
-                               table.shape[1], window, sinks, d ** -0.5 if scale is None else scale, dt)
-    _ck.ck_paged_attention(args, cache.struct, _ck._stream(q))
-    return out
+    if workspace is not None:
+        _ck._need(workspace, torch.uint8, "workspace", dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
 
 
 class Int4Weight:
@@ -241,6 +319,7 @@ class Int4Weight:
         self.w, self.scales, self.zeros = w, scales, zeros
         self.n, self.k, self.group, self.dtype = n, k, group, dtype
         self.device = w.device
+        self.w_ptr, self.s_ptr, self.z_ptr = w.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr()
 
 
 def int4_pack(codes, scales, zeros=None, group: int = 128):
@@ -280,7 +359,30 @@ def int4_linear(x, weight, bias=None, out=None, out_dtype=None):
     """bf16 or fp16 x [m, k] times the 4-bit weight [n, k] (of int4_pack,
     with scales of x's type) -> [m, n] of out_dtype ("bf16", "fp16" or "fp32";
     x's type when None).  bias [n] has the output's type."""
-    import torch
+    torch = _torch or _load_torch()
+    try:
+        tt, dev, (m, k), xs = x.dtype, x.device, x.shape, x.stride()
+        good = (x.is_cuda and type(weight) is Int4Weight and tt is weight.dtype and dev == weight.device
+                and k == weight.k and (xs[1] == 1 or k <= 1) and out is None and out_dtype is None)
+        n = weight.n
+        if bias is not None:
+            good = (good and bias.dtype is tt and bias.device == dev and bias.shape == (n,) and bias.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        code, odt = _check_int4(x, weight, bias, out, out_dtype)
+    else:
+        code, odt = _code16[tt], tt          # the out codes of the two types are the same
+    if out is None:
+        out = x.new_empty((m, n), dtype=odt)
+    args = _INT4.pack(x.data_ptr(), weight.w_ptr, weight.s_ptr, weight.z_ptr, 0 if bias is None else bias.data_ptr(),
+                      out.data_ptr(), xs[0], out.stride(0), m, n, k, weight.group, _code16[tt], code)
+    _ck.ck_int4_linear(args, _stream(dev.index))
+    return out
+
+
+def _check_int4(x, weight, bias, out, out_dtype):
+    """Every check of int4_linear's arguments, one by one; the output type."""
     if not isinstance(weight, Int4Weight):
         raise TypeError("weight must be an Int4Weight (see int4_pack)")
     dt = _dtype16(x, "x")
@@ -288,16 +390,8 @@ def int4_linear(x, weight, bias=None, out=None, out_dtype=None):
     code, tdt = _ck._out_dtype(("bf16", "fp16")[dt] if out_dtype is None else out_dtype)
     if x.dim() != 2 or x.shape[1] != weight.k:
         raise ValueError(f"x must be [m, {weight.k}]")
-    m, n, dev = x.shape[0], weight.n, x.device
     if bias is not None:
-        _ck._need_vector(bias, tdt, "bias", (n,), dev)
-    if out is None:
-        out = torch.empty((m, n), dtype=tdt, device=dev)
-    else:
-        _ck._need_matrix(out, tdt, "out", (m, n), dev)
-    # one row has no stride of its own
-    ldx, ldo = (x.stride(0), out.stride(0)) if m > 1 else ((weight.k + 7) // 8 * 8, n)
-    _ck.ck_int4_linear(x.data_ptr(), ldx, dt, weight.w.data_ptr(), weight.scales.data_ptr(),
-                       0 if weight.zeros is None else weight.zeros.data_ptr(), 0 if bias is None else bias.data_ptr(),
-                       out.data_ptr(), ldo, code, m, n, weight.k, weight.group, _ck._stream(x))
-    return out
+        _ck._need_vector(bias, tdt, "bias", (weight.n,), x.device)
+    if out is not None:
+        _ck._need_matrix(out, tdt, "out", (x.shape[0], weight.n), x.device)
+    return code, tdt

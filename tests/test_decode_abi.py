@@ -103,6 +103,7 @@ def test_rope_cache_validation(kw, status):
     (dict(positions=P + 4), UNS),
     (dict(q_weight=0, k_weight=0), HIP),
     (dict(tokens=1 << 42), UNS),
+    (dict(tokens=1, q_token_stride=3, k_token_stride=3, v_token_stride=3, q_out_token_stride=3), HIP),
 ])
 def test_rope_validation(kw, status):
     no_gpu(status)
@@ -236,28 +237,33 @@ def test_int4_pack_validation(kw, status):
     (dict(out=P + 2, out_dtype=2), UNS),
     (dict(bias=P + 1), UNS),
     (dict(k=0, x=0, w=0, w_scale=0), HIP),   # the bias alone
+    (dict(m=1, ldx=3, ldo=1), HIP),          # one row has no stride
 ])
 def test_int4_linear_validation(kw, status):
     no_gpu(status)
     a = dict(x=P, ldx=512, dtype=0, w=P, w_scale=P, w_zero=0, bias=0, out=P, ldo=64, out_dtype=0, m=3, n=64, k=512,
              group=128)
     a.update(kw)
-    assert ck.lib().ck_int4_linear(*a.values(), 0) == status
+    assert ck.lib().ck_int4_linear(ctypes.byref(ck.CkInt4Args(**a)), 0) == status
+    assert ck.lib().ck_int4_linear(None, 0) == BAD
 
 
 def test_struct_fields_follow_the_header():
     """The binding's structures have the header's fields, in its order."""
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
-    for name, cls in (("ck_kv_cache", ck.CkKvCache), ("ck_qk_args", ck.CkQkArgs), ("ck_attention_args", ck.CkAttentionArgs)):
+    for name, cls in (("ck_kv_cache", ck.CkKvCache), ("ck_qk_args", ck.CkQkArgs), ("ck_attention_args", ck.CkAttentionArgs),
+                      ("ck_int4_args", ck.CkInt4Args)):
         body = re.search(r"typedef struct \{([^}]*)\} %s;" % name, text).group(1)
         want = []
         for line in body.split(";"):
             if line.strip():
                 kind = "ptr" if "*" in line else re.search(r"\b(int64_t|int32_t|float)\b", line).group(1)
-                names = re.sub(r"\b(const|void|float|int64_t|int32_t)\b|\*", " ", line)
+                names = re.sub(r"\b(const|void|float|u?int[0-9]+_t)\b|\*", " ", line)
                 want += [(n.strip(), kind) for n in names.split(",")]
         kinds = {ctypes.c_void_p: "ptr", ctypes.c_int64: "int64_t", ctypes.c_int32: "int32_t", ctypes.c_float: "float"}
         assert [(n, kinds[t]) for n, t in cls._fields_] == want
+    for packed, cls in ((ck.decode._QK, ck.CkQkArgs), (ck.decode._ATTENTION, ck.CkAttentionArgs), (ck.decode._INT4, ck.CkInt4Args)):
+        assert packed.size == ctypes.sizeof(cls)
 
 
 # ------------------------------------------------------------- the binding
@@ -272,6 +278,7 @@ def host(monkeypatch):
 
     monkeypatch.setattr(ck, "_DEVICE_TYPE", "cpu")
     monkeypatch.setattr(ck, "_stream", lambda t: 0)
+    monkeypatch.setattr(ck.decode, "_stream", lambda index: 0)
     for f in ("ck_qk_norm_rope", "ck_paged_attention", "ck_int4_pack", "ck_int4_linear"):
         monkeypatch.setattr(ck, f, launched)
     return Launched
