@@ -22,7 +22,7 @@ import int8_weight_quantized_amd as _ck
 # by one to raise what is wrong.  The library's argument structures are packed
 # as bytes.  (torch is imported on first use, as everywhere in this package.)
 
-_QK = struct.Struct("10Q16qf3i4x")
+_QK = struct.Struct("10Q16qf3i")
 _ATTENTION = struct.Struct("5Q11qfi")
 _INT4 = struct.Struct("6Q6q2i")
 _torch = None
