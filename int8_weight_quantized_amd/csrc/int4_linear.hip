@@ -68,7 +68,7 @@ __device__ __forceinline__ void store_int4(const Int4Args& a, int64_t row, int64
     }
 }
 
-// Few rows of x (up to 32).  Mathematics: for each group g of columns,
+// Few rows of x (up to 16).  Mathematics: for each group g of columns,
 //   out[i, j] += s[j, g] (sum_t x[i, t] (16 + c[j, t]) - (16 + z[j, g]) X[i, g]),
 //   X[i, g] = sum_t x[i, t],
 // because 16 + c is one bit operation away from a code: the code's four bits
@@ -88,11 +88,16 @@ __device__ __forceinline__ void store_int4(const Int4Args& a, int64_t row, int64
 // operand row 4 (j % 4) + j / 4, which puts it into register j / 4 of lanes
 // G = j % 4: with up to 4 (8) rows only one (two) of the four accumulator
 // registers are in use, and only those get the scales (MR).
+// mask and base are int4_mask and int4_base in registers of the two kinds that
+// one and-or instruction takes (it has no room for constants).
 template <int DT>
-__device__ __forceinline__ v4i codes16(uint32_t w)
+constexpr uint32_t int4_mask = DT == CK_DT_FP16 ? 0x03c003c0u : 0x00780078u;
+template <int DT>
+constexpr uint32_t int4_base = DT == CK_DT_FP16 ? 0x4c004c00u : 0x41804180u;      // 16, twice
+
+template <int DT>
+__device__ __forceinline__ v4i codes16(uint32_t w, uint32_t mask, uint32_t base)
 {
-    constexpr uint32_t mask = DT == CK_DT_FP16 ? 0x03c003c0u : 0x00780078u;
-    constexpr uint32_t base = DT == CK_DT_FP16 ? 0x4c004c00u : 0x41804180u;       // 16, twice
     constexpr int up = DT == CK_DT_FP16 ? 6 : 3;                                  // bit of the code's place
     v4i r;
 #pragma unroll
@@ -112,17 +117,15 @@ struct Int4Few {
     static constexpr int xl = MB * MR;                       // 1 KiB loads of x: four rows of 128
     static constexpr int slot = (NT + xl + 1) * 1024;        // W, x, then scales and zeros
     static constexpr int loads = NT + xl + 1;
-    static constexpr int lds = 80 * 1024;                    // two blocks a CU
-    static constexpr int fit = lds / (KW * slot);
-    static constexpr int ahead = fit >= 6 ? 6 : fit >= 2 ? fit : 2;
+    static constexpr int ahead = 2;                          // more waves hide more than longer rings
     static constexpr int ring = KW * ahead * slot;
     static constexpr int regs = NT * MB * MR;
     static constexpr int sums = KW * regs * 256;
     static_assert(sums <= ring && ring <= 163840 && (ahead - 1) * loads < 64, "the ring, then the sums");
 };
 
-template <int DT, int GS, int MR, int MB, int NT, int KW>
-__global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
+template <int DT, int GS, bool Z, int MR, int MB, int NT, int KW>
+__global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 {
     using S = Int4Few<GS, MR, MB, NT, KW>;
     constexpr int AH = S::ahead, XL = S::xl, L = S::loads;
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
         x_at[j] = (uint32_t)((i16 ^ (row & 15)) * 16);
     }
     // Scales: two lanes a tile and group; zeros from lane 32 on, one lane.
-    const bool zl = a.wz != nullptr && lane >= 32;
+    const bool zl = Z && lane >= 32;
     const int su = zl ? lane - 32 : lane, per = zl ? 1 : 2;
     const int st = min(su / (GS * per), NT - 1), sg = su / per % GS;
     const int64_t stile = min(tile0 + st, tiles - 1);
@@ -179,6 +182,9 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
     }
     const uint32_t one2 = DT == CK_DT_FP16 ? 0x3c003c00u : 0x3f803f80u;
     const v4i one = {(int)one2, (int)one2, (int)one2, (int)one2};
+    uint32_t mask = int4_mask<DT>, base16 = int4_base<DT>;
+    asm volatile("" : "+v"(mask));
+    asm volatile("" : "+s"(base16));
     const f32x4v zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     float tot[NT][MB][MR];
 #pragma unroll
@@ -193,21 +199,18 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
         for (int i = 0; i < AH; ++i)
             if (i < nc) issue(i, i);
     }
-    int slot = 0;
-    for (int c = 0; c < nc; ++c) {
-        // the loads of up to AH - 1 later chunks may still be on their way
-        const int later = min(AH - 1, nc - 1 - c);
-        if (later >= AH - 1) wait_vmcnt<(AH - 1) * L>();
-        else if (AH > 5 && later == 4) wait_vmcnt<4 * L < 64 ? 4 * L : 63>();
-        else if (AH > 4 && later == 3) wait_vmcnt<3 * L < 64 ? 3 * L : 63>();
-        else if (AH > 3 && later == 2) wait_vmcnt<2 * L < 64 ? 2 * L : 63>();
-        else if (AH > 2 && later == 1) wait_vmcnt<L>();
-        else wait_vmcnt<0>();
-        const uint8_t* const base = my + slot * S::slot;
+    auto consume = [&](int slot, int c) {
+        uint8_t* const base = my + slot * S::slot;
+        const int kleft = (int)min<int64_t>(128, a.k - (int64_t)(cb + c) * 128);
+        if (kleft < 128) {                                   // x past k becomes zero
+#pragma unroll
+            for (int j = 0; j < XL; ++j)
+                if ((i16 ^ ((4 * j + G) & 15)) * 8 >= kleft)
+                    *reinterpret_cast<v4i*>(base + (NT + j) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
+        }
         v4i w[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const v4i*>(base + t * 1024 + lane * 16);
-        const int kleft = (int)min<int64_t>(128, a.k - (int64_t)(cb + c) * 128);
 #pragma unroll
         for (int g = 0; g < GS; ++g) {
             f32x4v acc[NT][MB], xs[MB];
@@ -223,12 +226,11 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
 #pragma unroll
                 for (int b = 0; b < MB; ++b) {
                     x[b] = *reinterpret_cast<const v4i*>(base + x_rd[b] + (((4 * s + G) ^ x_sw[b]) << 4));
-                    if (kleft < 128 && 32 * s + 8 * G >= kleft) x[b] = v4i{0, 0, 0, 0};
                     xs[b] = mfma16<DT>(x[b], one, xs[b]);
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const v4i wf = codes16<DT>((uint32_t)w[t][s]);
+                    const v4i wf = codes16<DT>((uint32_t)w[t][s], mask, base16);
 #pragma unroll
                     for (int b = 0; b < MB; ++b) acc[t][b] = mfma16<DT>(x[b], wf, acc[t][b]);
                 }
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
             for (int t = 0; t < NT; ++t) {
                 const uint8_t* const sp = base + (NT + XL) * 1024;
                 const float sc = widen1<DT>(*reinterpret_cast<const uint16_t*>(sp + (t * GS + g) * 32 + i16 * 2));
-                const float z = a.wz ? 16.0f + (float)sp[512 + (t * GS + g) * 16 + i16] : 24.0f;
+                const float z = Z ? 16.0f + (float)sp[512 + (t * GS + g) * 16 + i16] : 24.0f;
 #pragma unroll
                 for (int b = 0; b < MB; ++b)
 #pragma unroll
@@ -246,7 +248,22 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // the slot is read
+    };
+    int slot = 0, c = 0;
+    for (; c + AH <= nc; ++c) {                              // AH - 1 later chunks on their way
+        wait_vmcnt<(AH - 1) * L>();
+        consume(slot, c);
         if (c + AH < nc) issue(slot, c + AH);
+        slot = slot + 1 == AH ? 0 : slot + 1;
+    }
+    for (; c < nc; ++c) {
+        const int later = nc - 1 - c;
+        if (AH > 5 && later == 4) wait_vmcnt<AH * L < 64 ? 4 * L : 0>();
+        else if (AH > 4 && later == 3) wait_vmcnt<AH * L < 64 ? 3 * L : 0>();
+        else if (AH > 3 && later == 2) wait_vmcnt<AH * L < 64 ? 2 * L : 0>();
+        else if (AH > 2 && later == 1) wait_vmcnt<L>();
+        else wait_vmcnt<0>();
+        consume(slot, c);
         slot = slot + 1 == AH ? 0 : slot + 1;
     }
 
@@ -272,6 +289,286 @@ __global__ __launch_bounds__(64 * KW) void int4_few_kernel(Int4Args a)
     }
 }
 
+// More rows of x (blocks of 16 WM MB = 32, 64 or 128).  The same mathematics;
+// now the waves of a block share x and W.  A wave has MB row blocks of x times
+// NT row tiles of W; WM x WN waves make a team, and WK teams split K.  x comes
+// into LDS in stages of 64 columns for every team (one in use and one on its
+// way, one barrier a stage), W in chunks of 128 columns, two deep.  A wave
+// takes a chunk's words and scales into registers at once; the next barrier
+// frees the chunk's place.
+//
+// The sums X of x over a group are needed by every wave, but made by one:
+// each wave forms those of its share of the row blocks and leaves them in
+// LDS, and all waves take them off one stage later, after its barrier.
+//
+// Bound: the LDS reads of x (1 KiB for NT products), the matrix cores and the
+// vector unit within a factor of two of each other at 128 rows, HBM at 32.
+template <int GS, int MB, int NT, int WM, int WN, int WK>
+struct Int4Many {
+    static constexpr int waves = WM * WN * WK, team = WM * WN;
+    static constexpr int blocks = WM * MB;                   // 16-row blocks of x
+    static constexpr int part = blocks * 2048;               // a team's stage of x
+    static constexpr int stage = WK * part;
+    static constexpr int slot = (NT + 1) * 1024;             // W, then scales and zeros
+    static constexpr int wring = 2 * stage;
+    static constexpr int xsum = wring + WN * WK * 2 * slot;  // [team][stage parity][group][16 blocks]
+    static constexpr int hg = GS == 4 ? 2 : 1;               // groups per stage
+    static constexpr int spare = xsum + WK * 2 * hg * blocks * 64;   // where the lanes write that have no X
+    static constexpr int bytes = spare + 1024;
+    static constexpr int xl = blocks * 2 / team;             // 1 KiB loads of x per wave and stage
+    static constexpr int wl = NT / WM + 1;                   // and of W per wave and chunk
+    static constexpr int own = blocks / team;                // row blocks whose X a wave makes
+    static constexpr int regs = NT * MB * 4;
+    static constexpr int sums = waves * regs * 256;
+    static constexpr int total = bytes > sums ? bytes : sums;
+    static_assert(blocks % team == 0 && NT % WM == 0 && total <= 163840, "sizes");
+};
+
+template <int DT, int GS, bool Z, int MB, int NT, int WM, int WN, int WK>
+__global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Args a)
+{
+    using S = Int4Many<GS, MB, NT, WM, WN, WK>;
+    constexpr int XL = S::xl, WL = S::wl, HG = S::hg;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::total];
+    const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM % WN, wk = wave / S::team, member = wave % S::team;
+    const int64_t tiles = (a.n + 15) / 16, tile0 = ((int64_t)blockIdx.x * WN + wn) * NT;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * S::blocks);
+    const int rows = (int)min<int64_t>(a.m - m0, 16 * S::blocks);
+    const int cb = (int)(a.chunks * wk / WK), ce = (int)(a.chunks * (wk + 1) / WK), nc = ce - cb;
+    const int most = (int)((a.chunks + WK - 1) / WK);
+
+    // x: load j of a team's stage copies rows 8 j + lane / 8, 16-byte piece
+    // lane % 8, pieces exchanged by xor so that 16 rows' same piece lie apart
+    const uint8_t* const xb = reinterpret_cast<const uint8_t*>(a.x + m0 * a.ldx);
+    uint32_t x_off[XL], x_at[XL];
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+        const int row = 8 * (member + S::team * j) + (lane >> 3);
+        x_at[j] = (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+        x_off[j] = (uint32_t)(min(row, rows - 1) * a.ldx * 2) + x_at[j];
+    }
+    const uint32_t lds0 = lds_addr(lds);
+    auto issue_x = [&](int h, int o) {
+        const int64_t k0 = (int64_t)cb * 128 + h * 64;
+        const uint32_t dst = lds0 + o * S::stage + wk * S::part;
+        if (k0 + 64 <= a.k) {
+#pragma unroll
+            for (int j = 0; j < XL; ++j)
+                dma16(reinterpret_cast<const int8_t*>(xb + k0 * 2), x_off[j], dst + (member + S::team * j) * 1024);
+        } else {                                             // past k: the row's last piece again, zeroed before use
+            const int64_t base = k0 >= a.k ? (a.k - 8) * 2 : k0 * 2;
+            const uint32_t cap = (uint32_t)(a.k * 2 - base) - 16;
+#pragma unroll
+            for (int j = 0; j < XL; ++j)
+                dma16(reinterpret_cast<const int8_t*>(xb + base), x_off[j] - x_at[j] + min(x_at[j], cap), dst + (member + S::team * j) * 1024);
+        }
+    };
+    // W: the WM waves of the same tiles share the loads; scales (two lanes a
+    // tile and group) and zeros (one lane, from 32 on) come with each of them
+    const bool zl = Z && lane >= 32;
+    const int su = zl ? lane - 32 : lane, per = zl ? 1 : 2;
+    const int st = min(su / (GS * per), NT - 1), sg = su / per % GS;
+    const int64_t stile = min(tile0 + st, tiles - 1);
+    const uint8_t* const s_base = zl ? a.wz + stile * a.groups * 16
+                                     : reinterpret_cast<const uint8_t*>(a.ws) + stile * a.groups * 32 + (su & 1) * 16;
+    const uint32_t s_step = zl ? 16 : 32;
+    const uint8_t* w_base[NT / WM];
+#pragma unroll
+    for (int t = 0; t < NT / WM; ++t) w_base[t] = a.w + min(tile0 + wm + WM * t, tiles - 1) * a.chunks * 1024;
+    uint8_t* const my = lds + S::wring + (wk * WN + wn) * (2 * S::slot);
+    const uint32_t my_lds = lds_addr(my);
+    auto issue_w = [&](int c) {
+        const uint32_t dst = my_lds + (c & 1) * S::slot;
+        const int64_t kc = cb + c;
+#pragma unroll
+        for (int t = 0; t < NT / WM; ++t)
+            dma16(reinterpret_cast<const int8_t*>(w_base[t] + kc * 1024), lane * 16, dst + (wm + WM * t) * 1024);
+        const uint32_t g = (uint32_t)min<int64_t>(kc * GS + sg, a.groups - 1);
+        dma16_at(s_base + (uint64_t)g * s_step, dst + NT * 1024);
+    };
+
+    const uint32_t one2 = DT == CK_DT_FP16 ? 0x3c003c00u : 0x3f803f80u;
+    const v4i one = {(int)one2, (int)one2, (int)one2, (int)one2};
+    const f32x4v zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t mask = int4_mask<DT>, base16 = int4_base<DT>;
+    asm volatile("" : "+v"(mask));
+    asm volatile("" : "+s"(base16));
+    f32x4v tot[NT][MB], acc[NT][GS == 1 ? MB : 1], xacc[S::own];   // acc, xacc: a group longer than a stage
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int b = 0; b < MB; ++b) tot[t][b] = zero4;
+    v4i w[NT];                                               // the chunk's words
+    float sc[NT][GS], sz[NT][GS];                            // its scales, and scales times (16 + zero)
+    float sz_was[NT][HG];                                    // those of the X in LDS (none yet)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int g = 0; g < HG; ++g) sz_was[t][g] = 0.0f;
+    for (int i = threadIdx.x; i < WK * 2 * HG * S::blocks * 4; i += 64 * S::waves)
+        reinterpret_cast<f32x4v*>(lds + S::xsum)[i] = zero4;
+    f32x4v* const xsum = reinterpret_cast<f32x4v*>(lds + S::xsum) + wk * (2 * HG * S::blocks * 4);
+    const uint32_t x_wr = i16 == 0 ? S::xsum + (wk * 2 * HG * S::blocks * 4 + G) * 16 : S::spare + lane * 16;
+    auto take_off = [&](int o, bool now) {                   // the X of the stage before, of parity o
+        if (!now) return;
+#pragma unroll
+        for (int g = 0; g < HG; ++g)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                const f32x4v x = xsum[((o * HG + g) * S::blocks + wm * MB + b) * 4 + G];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) tot[t][b][r] = __builtin_fmaf(-sz_was[t][g], x[r], tot[t][b][r]);
+            }
+    };
+    // x's row in a 16-row block for this lane's operand row, and its two pieces
+    const int x_row = 4 * (i16 & 3) + (i16 >> 2), x_sw = (x_row >> 1) & 7;
+    const int x_rd[2] = {x_row * 128 + ((G ^ x_sw) << 4), x_row * 128 + (((4 + G) ^ x_sw) << 4)};
+    auto half = [&](int c, auto odd) {
+        constexpr int O = decltype(odd)::value ? 1 : 0;
+        const uint8_t* const xs = lds + O * S::stage + wk * S::part;
+        if (O == 0) {
+            const uint8_t* const base = my + (c & 1) * S::slot;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                w[t] = *reinterpret_cast<const v4i*>(base + t * 1024 + lane * 16);
+#pragma unroll
+                for (int g = 0; g < GS; ++g) {
+                    sc[t][g] = widen1<DT>(*reinterpret_cast<const uint16_t*>(base + NT * 1024 + (t * GS + g) * 32 + i16 * 2));
+                    const float z = Z ? 16.0f + (float)base[NT * 1024 + 512 + (t * GS + g) * 16 + i16] : 24.0f;
+                    sz[t][g] = sc[t][g] * z;
+                }
+            }
+        }
+        // x of the next stage goes where the stage before this one was, and
+        // after an even stage W of two chunks on where this chunk's was
+        if (O == 0 || c + 1 < nc) issue_x(2 * c + O + 1, 1 - O);
+        if (O == 1 && c + 2 < nc) issue_w(c + 2);
+        take_off(GS > 1 ? 1 - O : 0, GS > 1 || O == 0);
+        constexpr int SG = 2 / HG;                           // steps of 32 columns per group of this stage
+        // X of this wave's row blocks
+#pragma unroll
+        for (int i = 0; i < S::own; ++i) {
+            const int b = member + S::team * i;
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                f32x4v sum = GS == 1 && O == 1 ? xacc[i] : zero4;
+#pragma unroll
+                for (int s = g * SG; s < (g + 1) * SG; ++s)
+                    sum = mfma16<DT>(*reinterpret_cast<const v4i*>(xs + b * 2048 + x_rd[s]), one, sum);
+                if (GS == 1 && O == 0) xacc[i] = sum;
+                else *reinterpret_cast<f32x4v*>(lds + x_wr + (i16 == 0 ? (((GS > 1 ? O : 0) * HG + g) * S::blocks + b) * 64 : 0)) = sum;
+            }
+        }
+        v4i wf[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) wf[t][s] = codes16<DT>((uint32_t)w[t][2 * O + s], mask, base16);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+            v4i x[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) x[s] = *reinterpret_cast<const v4i*>(xs + x_rd[s] + (wm * MB + b) * 2048);
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    f32x4v sum = GS == 1 && O == 1 ? acc[t][GS == 1 ? b : 0] : zero4;
+#pragma unroll
+                    for (int s = g * SG; s < (g + 1) * SG; ++s) sum = mfma16<DT>(x[s], wf[t][s], sum);
+                    if (GS == 1 && O == 0) {
+                        acc[t][GS == 1 ? b : 0] = sum;
+                        continue;
+                    }
+                    const float scale = sc[t][GS == 4 ? 2 * O + g : GS == 2 ? O : 0];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) tot[t][b][r] = __builtin_fmaf(scale, sum[r], tot[t][b][r]);
+                }
+            }
+            // Left alone, the compiler moves the scaling of all products to
+            // where the sums are used next, past the stage's end, and runs
+            // out of registers on the way.
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (GS > 1 || O == 1) asm volatile("" : "+v"(tot[t][b]));
+                else asm volatile("" : "+v"(acc[t][GS == 1 ? b : 0]));
+            }
+        }
+        if (GS > 1 || O == 1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int g = 0; g < HG; ++g) sz_was[t][g] = sz[t][GS == 4 ? 2 * O + g : GS == 2 ? O : 0];
+        }
+    };
+    const bool tail = a.k % 128 != 0;
+    auto clear_tail = [&](int h, int o) {                    // x past k in a landed stage becomes zero
+        const int64_t left = a.k - ((int64_t)cb * 128 + h * 64);
+        if (left < 64) {
+#pragma unroll
+            for (int j = 0; j < XL; ++j)
+                if ((int)x_at[j] >= 2 * left)
+                    *reinterpret_cast<v4i*>(lds + o * S::stage + wk * S::part + (member + S::team * j) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
+        }
+    };
+    // The end of a stage: this wave's loads of x of the next one have landed,
+    // and after an odd stage those of the next chunk of W; only the W that was
+    // issued last, after that x, may be on its way.
+    auto close = [&](int c, auto odd) {
+        constexpr int O = decltype(odd)::value ? 1 : 0;
+        if (O == 1 && c + 2 < nc) wait_vmcnt<WL>();
+        else wait_vmcnt<0>();
+        if (tail) clear_tail(2 * c + O + 1, 1 - O);
+        __syncthreads();
+    };
+
+    if (nc > 0) {
+        issue_x(0, 0);
+        issue_w(0);
+        if (nc > 1) issue_w(1);
+    }
+    if (nc > 1) wait_vmcnt<WL>();                            // x of stage 0 and W of chunk 0
+    else wait_vmcnt<0>();
+    if (tail) clear_tail(0, 0);
+    __syncthreads();
+    for (int c = 0; c < nc; ++c) {
+        half(c, BoolTag<false>{});
+        close(c, BoolTag<false>{});
+        half(c, BoolTag<true>{});
+        close(c, BoolTag<true>{});
+    }
+    for (int c = nc; c < most; ++c) {                        // a team with a chunk less than another
+        __syncthreads();
+        __syncthreads();
+    }
+    if (nc > 0) take_off(GS > 1 ? 1 : 0, true);
+
+    // The teams' sums, over everything, then in their order.
+    __syncthreads();
+    float* const red = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[(wave * S::regs + (t * MB + b) * 4 + r) * 64 + lane] = tot[t][b][r];
+    __syncthreads();
+    for (int o = threadIdx.x; o < S::team * S::regs * 64; o += 64 * S::waves) {
+        const int l = o & 63, q = (o >> 6) % S::regs, wv = (o >> 6) / S::regs, r = q & 3, b = (q >> 2) % MB, t = (q >> 2) / MB;
+        const int64_t col = (((int64_t)blockIdx.x * WN + wv / WM) * NT + t) * 16 + (l & 15);
+        const int row = 16 * (wv % WM * MB + b) + 4 * r + (l >> 4);
+        if (col >= a.n || row >= rows) continue;
+        float v = red[o];
+#pragma unroll
+        for (int k = 1; k < WK; ++k) v = v + red[o + k * S::team * S::regs * 64];
+        store_int4(a, m0 + row, col, v);
+    }
+}
+
 namespace {
 
 ck_status check_int4_sizes(int64_t n, int64_t k, int64_t group)
@@ -289,26 +586,56 @@ struct Int4Plan {
     int tiles, rows, waves;
 };
 
-template <int DT, int GS>
-Int4Plan int4_plan_gs(int64_t m, int64_t n)
+template <int DT, int GS, bool Z>
+Int4Plan int4_plan_gs(int64_t m, int64_t n, int64_t chunks)
 {
 #define CK_INT4_FEW(MR, MB, NT, KW) \
-    Int4Plan{reinterpret_cast<const void*>(&int4_few_kernel<DT, GS, MR, MB, NT, KW>), NT, 16 * MB, KW}
-    const bool wide = n > 16 * 2 * kNumCUs;
-    if (m <= 4) return wide ? CK_INT4_FEW(1, 1, 2, 4) : CK_INT4_FEW(1, 1, 1, 8);
-    if (m <= 8) return wide ? CK_INT4_FEW(2, 1, 2, 4) : CK_INT4_FEW(2, 1, 1, 8);
-    if (m <= 16) return wide ? CK_INT4_FEW(4, 1, 2, 4) : CK_INT4_FEW(4, 1, 1, 8);
-    return wide ? CK_INT4_FEW(4, 2, 4, 4) : CK_INT4_FEW(4, 2, 2, 4);
+    Int4Plan{reinterpret_cast<const void*>(&int4_few_kernel<DT, GS, Z, MR, MB, NT, KW>), NT, 16 * MB, KW}
+#define CK_INT4_MANY(MB, NT, WM, WN, WK, COST)                                                       \
+    {{reinterpret_cast<const void*>(&int4_many_kernel<DT, GS, Z, MB, NT, WM, WN, WK>), NT * WN,        \
+      16 * MB * WM, WM * WN * WK}, WK, COST}
+    // Few rows: two row tiles per wave once that leaves a block or more per
+    // CU (1 row, 28672 x 5376: 20.4 against 24.9 us with one tile, 16384 x
+    // 4096: 10.2 against 9.8 us, 4096 x 4096: 5.5 against 4.6 us).
+    const bool wide = n > 20480;
+    if (m <= 4) return wide ? CK_INT4_FEW(1, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(1, 1, 1, 4) : CK_INT4_FEW(1, 1, 1, 8);
+    if (m <= 8) return wide ? CK_INT4_FEW(2, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(2, 1, 1, 4) : CK_INT4_FEW(2, 1, 1, 8);
+    if (m <= 16) return wide ? CK_INT4_FEW(4, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(4, 1, 1, 4) : CK_INT4_FEW(4, 1, 1, 8);
+    // More rows: a block holds most of a CU's LDS, so a launch runs in rounds
+    // of 256 blocks; a round takes about 3 us and COST / 100 us for each
+    // chunk of a team (fitted at 32 rows of 4096 x 4096, 16384 x 4096 and
+    // 21504 x 5376, 64 rows of 4096 x 4096 and 21504 x 5376, 128 rows of the
+    // latter).  The least product wins.
+    struct Choice { Int4Plan plan; int teams, cost; };
+    const Choice upto32[] = {CK_INT4_MANY(2, 2, 1, 1, 8, 110), CK_INT4_MANY(2, 2, 1, 2, 4, 110), CK_INT4_MANY(2, 4, 1, 2, 4, 190)};
+    const Choice more[] = {CK_INT4_MANY(4, 1, 1, 2, 4, 120), CK_INT4_MANY(4, 2, 1, 2, 4, 175), CK_INT4_MANY(4, 4, 1, 2, 4, 330),
+                           CK_INT4_MANY(4, 4, 2, 2, 2, 290)};
+    const Choice* const from = m <= 32 ? upto32 : more;
+    const int count = m <= 32 ? 3 : m <= 64 ? 3 : 4;
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < count; ++i) {
+        const int64_t blocks = cdiv(cdiv(n, 16), from[i].plan.tiles) * cdiv(m, from[i].plan.rows);
+        const int64_t time = cdiv(blocks, kNumCUs) * (300 + cdiv(chunks, from[i].teams) * from[i].cost);
+        if (time < least) least = time, best = i;
+    }
+    return from[best].plan;
+#undef CK_INT4_MANY
 #undef CK_INT4_FEW
 }
 
-Int4Plan int4_plan(int dtype, int64_t m, int64_t n, int64_t group)
+template <int DT, bool Z>
+Int4Plan int4_plan_z(int64_t m, int64_t n, int64_t chunks, int64_t group)
 {
-    if (dtype == CK_DT_FP16)
-        return group == 32 ? int4_plan_gs<CK_DT_FP16, 4>(m, n) : group == 64 ? int4_plan_gs<CK_DT_FP16, 2>(m, n)
-                                                                            : int4_plan_gs<CK_DT_FP16, 1>(m, n);
-    return group == 32 ? int4_plan_gs<CK_DT_BF16, 4>(m, n) : group == 64 ? int4_plan_gs<CK_DT_BF16, 2>(m, n)
-                                                                        : int4_plan_gs<CK_DT_BF16, 1>(m, n);
+    return group == 32   ? int4_plan_gs<DT, 4, Z>(m, n, chunks)
+           : group == 64 ? int4_plan_gs<DT, 2, Z>(m, n, chunks)
+                         : int4_plan_gs<DT, 1, Z>(m, n, chunks);
+}
+
+Int4Plan int4_plan(int dtype, bool zeros, int64_t m, int64_t n, int64_t chunks, int64_t group)
+{
+    if (dtype == CK_DT_FP16) return zeros ? int4_plan_z<CK_DT_FP16, true>(m, n, chunks, group) : int4_plan_z<CK_DT_FP16, false>(m, n, chunks, group);
+    return zeros ? int4_plan_z<CK_DT_BF16, true>(m, n, chunks, group) : int4_plan_z<CK_DT_BF16, false>(m, n, chunks, group);
 }
 
 }  // namespace
@@ -360,9 +687,9 @@ extern "C" ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream
         (p.bias && !aligned(p.bias, esz)))
         return fail(CK_ERR_UNSUPPORTED, "misaligned w, w_scale, w_zero, bias or out");
     // 32-bit offsets of a block's rows of x
-    if (p.m > 1 && 64 * p.ldx >= (int64_t(1) << 31))
+    if (p.m > 1 && 256 * p.ldx >= (int64_t(1) << 31))
         return fail(CK_ERR_UNSUPPORTED, "rows of x too long for 32-bit offsets");
-    const Int4Plan plan = int4_plan(p.dtype, p.m, p.n, p.group);
+    const Int4Plan plan = int4_plan(p.dtype, p.w_zero != nullptr, p.m, p.n, cdiv(p.k, 128), p.group);
     const int64_t bx = cdiv(cdiv(p.n, 16), plan.tiles), by = cdiv(p.m, plan.rows);
     if (by > 65535) return fail(CK_ERR_UNSUPPORTED, "too many rows");
     if ((s = check_device()) != CK_OK) return s;
