@@ -517,3 +517,47 @@ def test_int4_row_results_do_not_depend_on_the_batch_tile():
     w = ck.int4_pack(codes, scales, z, group=128)
     order = torch.randperm(16, generator=torch.Generator().manual_seed(1)).to(x.device)
     assert torch.equal(ck.int4_linear(x[order].contiguous(), w, b), ck.int4_linear(x, w, b)[order])
+
+
+# -------------------------------------------------------------- all together
+
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+def test_example_block_against_its_parts(cache):
+    """examples/decode_attention.py's block, prompt and two decode steps:
+    its output is that of plain 64-bit forms on the operators' own inputs."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from decode_attention import AttentionBlock
+    dev = cuda_device()
+    hidden, page, prompt = 512, 8, 43
+    block = AttentionBlock(hidden, 8, 2, 64, 20, page, cache, rows=256, device=dev)
+    table = torch.randperm(20, generator=torch.Generator().manual_seed(2)).int().view(2, 10).to(dev)
+    at = torch.arange(prompt, device=dev)
+    for b in range(2):
+        x = rand(prompt, hidden, dtype=torch.bfloat16, seed=b).to(dev)
+        assert block(x, at, table[b].long()[at // page] * page + at % page) is None
+    pos = torch.full((2,), prompt, device=dev)
+    for step in range(2):
+        x = rand(2, hidden, dtype=torch.bfloat16, seed=10 + step).to(dev)
+        slots = table.long().gather(1, (pos // page)[:, None])[:, 0] * page + pos % page
+        lens = (pos + 1).int()
+        y = block(x, pos, slots, table, lens)
+        qkv = ck.int8_linear(x, block.w_qkv, block.s_qkv)
+        q = ck.qk_norm_rope(qkv[:, :512].view(2, 8, 64), None, None, pos, block.table, block.q_norm)[0]
+        want_q, slack_q = ref.rope(qkv[:, :512].view(2, 8, 64), block.q_norm, block.table, pos, 64, False, 1e-6)
+        ref.assert_within(q, want_q, slack_q, "q")
+        c = block.cache
+        o = check_attention(q, c, table, lens)
+        w = block.w_out
+        got = ck.int4_linear(o.view(2, 512), w)
+        assert torch.equal(got, y)
+        # the newest row of the cache is this step's value
+        v = qkv[:, 640:].view(2, 2, 64).float()
+        row = c.v[slots // page, :, slots % page].float()
+        if cache == "int8":
+            row = row * c.v_scale[slots // page, :, slots % page][..., None]
+            assert ((row - v).abs() <= v.abs().amax(-1, keepdim=True) / 127).all()
+        else:
+            assert torch.equal(row, v)
+        pos += 1
