@@ -289,9 +289,9 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
     }
 }
 
-// More rows of x (blocks of 16 WM MB = 32, 64 or 128).  The same mathematics;
-// now the waves of a block share x and W.  A wave has MB row blocks of x times
-// NT row tiles of W; WM x WN waves make a team, and WK teams split K.  x comes
+// More rows of x (blocks of 16 MB = 32 or 64).  The same mathematics; now the
+// waves of a block share x.  A wave has MB row blocks of x times NT row tiles
+// of W; WN waves side by side make a team, and WK teams split K.  x comes
 // into LDS in stages of 64 columns for every team (one in use and one on its
 // way, one barrier a stage), W in chunks of 128 columns, two deep.  A wave
 // takes a chunk's words and scales into registers at once; the next barrier
@@ -301,41 +301,44 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 // each wave forms those of its share of the row blocks and leaves them in
 // LDS, and all waves take them off one stage later, after its barrier.
 //
-// Bound: the LDS reads of x (1 KiB for NT products), the matrix cores and the
-// vector unit within a factor of two of each other at 128 rows, HBM at 32.
-template <int GS, int MB, int NT, int WM, int WN, int WK>
+// Bound at 128 rows: the matrix cores (busy 35 % of the time), the vector unit
+// (31 %: two fused multiply-adds per output and group, two operations per two
+// codes) and the LDS reads of x (49 %, 1 KiB for NT products) take turns
+// rather than overlap, with two waves a SIMD: 128 x 21504 x 5376 52 us, 563
+// TFLOP/s.  Two blocks of four waves a CU overlap better than one of eight
+// waves (64 us).  At 32 rows HBM is as near: 32 x 21504 x 5376 23 us.
+template <int GS, int MB, int NT, int WN, int WK>
 struct Int4Many {
-    static constexpr int waves = WM * WN * WK, team = WM * WN;
-    static constexpr int blocks = WM * MB;                   // 16-row blocks of x
-    static constexpr int part = blocks * 2048;               // a team's stage of x
+    static constexpr int waves = WN * WK;
+    static constexpr int part = MB * 2048;                   // a team's stage of x
     static constexpr int stage = WK * part;
     static constexpr int slot = (NT + 1) * 1024;             // W, then scales and zeros
     static constexpr int wring = 2 * stage;
     static constexpr int xsum = wring + WN * WK * 2 * slot;  // [team][stage parity][group][16 blocks]
     static constexpr int hg = GS == 4 ? 2 : 1;               // groups per stage
-    static constexpr int spare = xsum + WK * 2 * hg * blocks * 64;   // where the lanes write that have no X
+    static constexpr int spare = xsum + WK * 2 * hg * MB * 64;   // where the lanes write that have no X
     static constexpr int bytes = spare + 1024;
-    static constexpr int xl = blocks * 2 / team;             // 1 KiB loads of x per wave and stage
-    static constexpr int wl = NT / WM + 1;                   // and of W per wave and chunk
-    static constexpr int own = blocks / team;                // row blocks whose X a wave makes
+    static constexpr int xl = MB * 2 / WN;                   // 1 KiB loads of x per wave and stage
+    static constexpr int wl = NT + 1;                        // and of W per wave and chunk
+    static constexpr int own = MB / WN;                      // row blocks whose X a wave makes
     static constexpr int regs = NT * MB * 4;
     static constexpr int sums = waves * regs * 256;
     static constexpr int total = bytes > sums ? bytes : sums;
-    static_assert(blocks % team == 0 && NT % WM == 0 && total <= 163840, "sizes");
+    static_assert(MB % WN == 0 && total <= 163840, "sizes");
 };
 
-template <int DT, int GS, bool Z, int MB, int NT, int WM, int WN, int WK>
-__global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Args a)
+template <int DT, int GS, bool Z, int MB, int NT, int WN, int WK>
+__global__ __launch_bounds__(64 * WN * WK, 2) void int4_many_kernel(Int4Args a)
 {
-    using S = Int4Many<GS, MB, NT, WM, WN, WK>;
+    using S = Int4Many<GS, MB, NT, WN, WK>;
     constexpr int XL = S::xl, WL = S::wl, HG = S::hg;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::total];
     const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % WM, wn = wave / WM % WN, wk = wave / S::team, member = wave % S::team;
+    const int wn = wave % WN, wk = wave / WN;
     const int64_t tiles = (a.n + 15) / 16, tile0 = ((int64_t)blockIdx.x * WN + wn) * NT;
-    const int64_t m0 = (int64_t)blockIdx.y * (16 * S::blocks);
-    const int rows = (int)min<int64_t>(a.m - m0, 16 * S::blocks);
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MB);
+    const int rows = (int)min<int64_t>(a.m - m0, 16 * MB);
     const int cb = (int)(a.chunks * wk / WK), ce = (int)(a.chunks * (wk + 1) / WK), nc = ce - cb;
     const int most = (int)((a.chunks + WK - 1) / WK);
 
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
     uint32_t x_off[XL], x_at[XL];
 #pragma unroll
     for (int j = 0; j < XL; ++j) {
-        const int row = 8 * (member + S::team * j) + (lane >> 3);
+        const int row = 8 * (wn + WN * j) + (lane >> 3);
         x_at[j] = (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
         x_off[j] = (uint32_t)(min(row, rows - 1) * a.ldx * 2) + x_at[j];
     }
@@ -356,17 +359,16 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
         if (k0 + 64 <= a.k) {
 #pragma unroll
             for (int j = 0; j < XL; ++j)
-                dma16(reinterpret_cast<const int8_t*>(xb + k0 * 2), x_off[j], dst + (member + S::team * j) * 1024);
+                dma16(reinterpret_cast<const int8_t*>(xb + k0 * 2), x_off[j], dst + (wn + WN * j) * 1024);
         } else {                                             // past k: the row's last piece again, zeroed before use
             const int64_t base = k0 >= a.k ? (a.k - 8) * 2 : k0 * 2;
             const uint32_t cap = (uint32_t)(a.k * 2 - base) - 16;
 #pragma unroll
             for (int j = 0; j < XL; ++j)
-                dma16(reinterpret_cast<const int8_t*>(xb + base), x_off[j] - x_at[j] + min(x_at[j], cap), dst + (member + S::team * j) * 1024);
+                dma16(reinterpret_cast<const int8_t*>(xb + base), x_off[j] - x_at[j] + min(x_at[j], cap), dst + (wn + WN * j) * 1024);
         }
     };
-    // W: the WM waves of the same tiles share the loads; scales (two lanes a
-    // tile and group) and zeros (one lane, from 32 on) come with each of them
+    // W, scales (two lanes a tile and group) and zeros (one lane, from 32 on)
     const bool zl = Z && lane >= 32;
     const int su = zl ? lane - 32 : lane, per = zl ? 1 : 2;
     const int st = min(su / (GS * per), NT - 1), sg = su / per % GS;
@@ -374,17 +376,17 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
     const uint8_t* const s_base = zl ? a.wz + stile * a.groups * 16
                                      : reinterpret_cast<const uint8_t*>(a.ws) + stile * a.groups * 32 + (su & 1) * 16;
     const uint32_t s_step = zl ? 16 : 32;
-    const uint8_t* w_base[NT / WM];
+    const uint8_t* w_base[NT];
 #pragma unroll
-    for (int t = 0; t < NT / WM; ++t) w_base[t] = a.w + min(tile0 + wm + WM * t, tiles - 1) * a.chunks * 1024;
+    for (int t = 0; t < NT; ++t) w_base[t] = a.w + min(tile0 + t, tiles - 1) * a.chunks * 1024;
     uint8_t* const my = lds + S::wring + (wk * WN + wn) * (2 * S::slot);
     const uint32_t my_lds = lds_addr(my);
     auto issue_w = [&](int c) {
         const uint32_t dst = my_lds + (c & 1) * S::slot;
         const int64_t kc = cb + c;
 #pragma unroll
-        for (int t = 0; t < NT / WM; ++t)
-            dma16(reinterpret_cast<const int8_t*>(w_base[t] + kc * 1024), lane * 16, dst + (wm + WM * t) * 1024);
+        for (int t = 0; t < NT; ++t)
+            dma16(reinterpret_cast<const int8_t*>(w_base[t] + kc * 1024), lane * 16, dst + t * 1024);
         const uint32_t g = (uint32_t)min<int64_t>(kc * GS + sg, a.groups - 1);
         dma16_at(s_base + (uint64_t)g * s_step, dst + NT * 1024);
     };
@@ -407,17 +409,17 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int g = 0; g < HG; ++g) sz_was[t][g] = 0.0f;
-    for (int i = threadIdx.x; i < WK * 2 * HG * S::blocks * 4; i += 64 * S::waves)
+    for (int i = threadIdx.x; i < WK * 2 * HG * MB * 4; i += 64 * S::waves)
         reinterpret_cast<f32x4v*>(lds + S::xsum)[i] = zero4;
-    f32x4v* const xsum = reinterpret_cast<f32x4v*>(lds + S::xsum) + wk * (2 * HG * S::blocks * 4);
-    const uint32_t x_wr = i16 == 0 ? S::xsum + (wk * 2 * HG * S::blocks * 4 + G) * 16 : S::spare + lane * 16;
+    f32x4v* const xsum = reinterpret_cast<f32x4v*>(lds + S::xsum) + wk * (2 * HG * MB * 4);
+    const uint32_t x_wr = i16 == 0 ? S::xsum + (wk * 2 * HG * MB * 4 + G) * 16 : S::spare + lane * 16;
     auto take_off = [&](int o, bool now) {                   // the X of the stage before, of parity o
         if (!now) return;
 #pragma unroll
         for (int g = 0; g < HG; ++g)
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
-                const f32x4v x = xsum[((o * HG + g) * S::blocks + wm * MB + b) * 4 + G];
+                const f32x4v x = xsum[((o * HG + g) * MB + b) * 4 + G];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -452,7 +454,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
         // X of this wave's row blocks
 #pragma unroll
         for (int i = 0; i < S::own; ++i) {
-            const int b = member + S::team * i;
+            const int b = wn + WN * i;
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 f32x4v sum = GS == 1 && O == 1 ? xacc[i] : zero4;
@@ -460,7 +462,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
                 for (int s = g * SG; s < (g + 1) * SG; ++s)
                     sum = mfma16<DT>(*reinterpret_cast<const v4i*>(xs + b * 2048 + x_rd[s]), one, sum);
                 if (GS == 1 && O == 0) xacc[i] = sum;
-                else *reinterpret_cast<f32x4v*>(lds + x_wr + (i16 == 0 ? (((GS > 1 ? O : 0) * HG + g) * S::blocks + b) * 64 : 0)) = sum;
+                else *reinterpret_cast<f32x4v*>(lds + x_wr + (i16 == 0 ? (((GS > 1 ? O : 0) * HG + g) * MB + b) * 64 : 0)) = sum;
             }
         }
         v4i wf[NT][2];
@@ -472,7 +474,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
         for (int b = 0; b < MB; ++b) {
             v4i x[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) x[s] = *reinterpret_cast<const v4i*>(xs + x_rd[s] + (wm * MB + b) * 2048);
+            for (int s = 0; s < 2; ++s) x[s] = *reinterpret_cast<const v4i*>(xs + x_rd[s] + b * 2048);
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
 #pragma unroll
@@ -512,7 +514,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
 #pragma unroll
             for (int j = 0; j < XL; ++j)
                 if ((int)x_at[j] >= 2 * left)
-                    *reinterpret_cast<v4i*>(lds + o * S::stage + wk * S::part + (member + S::team * j) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
+                    *reinterpret_cast<v4i*>(lds + o * S::stage + wk * S::part + (wn + WN * j) * 1024 + lane * 16) = v4i{0, 0, 0, 0};
         }
     };
     // The end of a stage: this wave's loads of x of the next one have landed,
@@ -557,14 +559,14 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void int4_many_kernel(Int4Arg
 #pragma unroll
             for (int r = 0; r < 4; ++r) red[(wave * S::regs + (t * MB + b) * 4 + r) * 64 + lane] = tot[t][b][r];
     __syncthreads();
-    for (int o = threadIdx.x; o < S::team * S::regs * 64; o += 64 * S::waves) {
+    for (int o = threadIdx.x; o < WN * S::regs * 64; o += 64 * S::waves) {
         const int l = o & 63, q = (o >> 6) % S::regs, wv = (o >> 6) / S::regs, r = q & 3, b = (q >> 2) % MB, t = (q >> 2) / MB;
-        const int64_t col = (((int64_t)blockIdx.x * WN + wv / WM) * NT + t) * 16 + (l & 15);
-        const int row = 16 * (wv % WM * MB + b) + 4 * r + (l >> 4);
+        const int64_t col = (((int64_t)blockIdx.x * WN + wv) * NT + t) * 16 + (l & 15);
+        const int row = 16 * b + 4 * r + (l >> 4);
         if (col >= a.n || row >= rows) continue;
         float v = red[o];
 #pragma unroll
-        for (int k = 1; k < WK; ++k) v = v + red[o + k * S::team * S::regs * 64];
+        for (int k = 1; k < WK; ++k) v = v + red[o + k * WN * S::regs * 64];
         store_int4(a, m0 + row, col, v);
     }
 }
@@ -591,9 +593,9 @@ Int4Plan int4_plan_gs(int64_t m, int64_t n, int64_t chunks)
 {
 #define CK_INT4_FEW(MR, MB, NT, KW) \
     Int4Plan{reinterpret_cast<const void*>(&int4_few_kernel<DT, GS, Z, MR, MB, NT, KW>), NT, 16 * MB, KW}
-#define CK_INT4_MANY(MB, NT, WM, WN, WK, COST)                                                       \
-    {{reinterpret_cast<const void*>(&int4_many_kernel<DT, GS, Z, MB, NT, WM, WN, WK>), NT * WN,        \
-      16 * MB * WM, WM * WN * WK}, WK, COST}
+#define CK_INT4_MANY(MB, NT, WN, WK, ONE, TWO)                                                    \
+    {{reinterpret_cast<const void*>(&int4_many_kernel<DT, GS, Z, MB, NT, WN, WK>), NT * WN, 16 * MB, \
+      WN * WK}, WK, ONE, TWO}
     // Few rows: two row tiles per wave once that leaves a block or more per
     // CU (1 row, 28672 x 5376: 20.4 against 24.9 us with one tile, 16384 x
     // 4096: 10.2 against 9.8 us, 4096 x 4096: 5.5 against 4.6 us).
@@ -601,22 +603,28 @@ Int4Plan int4_plan_gs(int64_t m, int64_t n, int64_t chunks)
     if (m <= 4) return wide ? CK_INT4_FEW(1, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(1, 1, 1, 4) : CK_INT4_FEW(1, 1, 1, 8);
     if (m <= 8) return wide ? CK_INT4_FEW(2, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(2, 1, 1, 4) : CK_INT4_FEW(2, 1, 1, 8);
     if (m <= 16) return wide ? CK_INT4_FEW(4, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(4, 1, 1, 4) : CK_INT4_FEW(4, 1, 1, 8);
-    // More rows: a block holds most of a CU's LDS, so a launch runs in rounds
-    // of 256 blocks; a round takes about 3 us and COST / 100 us for each
-    // chunk of a team (fitted at 32 rows of 4096 x 4096, 16384 x 4096 and
-    // 21504 x 5376, 64 rows of 4096 x 4096 and 21504 x 5376, 128 rows of the
-    // latter).  The least product wins.
-    struct Choice { Int4Plan plan; int teams, cost; };
-    const Choice upto32[] = {CK_INT4_MANY(2, 2, 1, 1, 8, 110), CK_INT4_MANY(2, 2, 1, 2, 4, 110), CK_INT4_MANY(2, 4, 1, 2, 4, 190)};
-    const Choice more[] = {CK_INT4_MANY(4, 1, 1, 2, 4, 120), CK_INT4_MANY(4, 2, 1, 2, 4, 175), CK_INT4_MANY(4, 4, 1, 2, 4, 330),
-                           CK_INT4_MANY(4, 4, 2, 2, 2, 290)};
+    // More rows: a round of 256 blocks, one a CU, takes about 2 us and ONE /
+    // 100 us for each chunk of a team; where two blocks fit a CU's LDS, a
+    // round of up to 512 takes TWO / 100 us a chunk.  (Fitted to group 128 at
+    // 17 to 128 rows of 4096 x 4096, 8192 x 4096, 16384 x 4096, 21504 x 5376 and
+    // 28672 x 5376; groups of 32 take 1.5 times as long in the same order.)
+    // The least sum wins: 128 rows of 21504 x 5376 take 66, 52, 62 and 70 us
+    // with blocks of 64, 96 and 128 columns of four waves and 128 columns of
+    // eight, of 16384 x 4096 34, 42, 36 and 30 us.
+    struct Choice { Int4Plan plan; int teams, one, two; };
+    const Choice upto32[] = {CK_INT4_MANY(2, 2, 1, 8, 110, 0), CK_INT4_MANY(2, 2, 2, 4, 110, 0), CK_INT4_MANY(2, 4, 2, 4, 190, 0)};
+    const Choice more[] = {CK_INT4_MANY(4, 1, 2, 4, 175, 0), CK_INT4_MANY(4, 2, 2, 2, 155, 190), CK_INT4_MANY(4, 3, 2, 2, 180, 240),
+                           CK_INT4_MANY(4, 4, 2, 2, 205, 290), CK_INT4_MANY(4, 2, 2, 4, 230, 0), CK_INT4_MANY(4, 4, 2, 4, 335, 0)};
     const Choice* const from = m <= 32 ? upto32 : more;
-    const int count = m <= 32 ? 3 : m <= 64 ? 3 : 4;
+    const int count = m <= 32 ? 3 : 6;
     int best = 0;
     int64_t least = INT64_MAX;
     for (int i = 0; i < count; ++i) {
-        const int64_t blocks = cdiv(cdiv(n, 16), from[i].plan.tiles) * cdiv(m, from[i].plan.rows);
-        const int64_t time = cdiv(blocks, kNumCUs) * (300 + cdiv(chunks, from[i].teams) * from[i].cost);
+        const Choice& c = from[i];
+        const int64_t blocks = cdiv(cdiv(n, 16), c.plan.tiles) * cdiv(m, c.plan.rows), each = cdiv(chunks, c.teams);
+        const int64_t round = c.two ? 2 * kNumCUs : kNumCUs, rest = blocks % round;
+        const int64_t full = 200 + each * (c.two ? c.two : c.one);
+        const int64_t time = blocks / round * full + (rest > kNumCUs ? full : rest > 0 ? 200 + each * c.one : 0);
         if (time < least) least = time, best = i;
     }
     return from[best].plan;
