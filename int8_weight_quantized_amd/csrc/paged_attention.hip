@@ -193,26 +193,50 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
 
     // Row offsets of the chunk's tokens, in 16-byte units; the last token's
     // again up to the end of the last tile, so that masked places hold
-    // values of a visible row.
+    // values of a visible row.  A thread's loads go out together, the pages
+    // of all its tokens and then the scales.
     if (tid == 0) bad_page = 0;
+    constexpr int PT = kAttnChunk / (64 * NW);               // tokens per thread
+    int32_t pages[PT], ats[PT];
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+        const int i = tid + j * 64 * NW;
+        if (i < tiles * kAttnTile) {
+            const int64_t tok = vis.token(first + min(i, n - 1));
+            pages[j] = a.table[b * a.table_stride + (tok >> a.page_shift)];
+            ats[j] = (int32_t)(tok & ((1 << a.page_shift) - 1));
+        }
+    }
     __syncthreads();
     float vmax = 0.0f;
-    for (int i = tid; i < tiles * kAttnTile; i += 64 * NW) {
-        const int64_t tok = vis.token(first + min(i, n - 1));
-        int64_t page = a.table[b * a.table_stride + (tok >> a.page_shift)];
-        const int64_t at = tok & ((1 << a.page_shift) - 1);
-        if (page < 0 || page >= a.pages) {
-            bad_page = 1;
-            page = 0;
+    if (a.pages > 0) {
+        float ks[PT], vs[PT];
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            const int i = tid + j * 64 * NW;
+            if (i < tiles * kAttnTile) {
+                int64_t page = pages[j];
+                if (page < 0 || page >= a.pages) {
+                    bad_page = 1;
+                    page = 0;
+                }
+                offs[i] = (uint32_t)((page * a.c_ps + kvh * a.c_hs + ats[j] * a.c_ts) * (I8 ? 1 : 2) / 16);
+                if constexpr (I8) {
+                    const int64_t so = page * a.s_ps + kvh * a.s_hs + ats[j] * a.s_ts;
+                    ks[j] = a.cks[so];
+                    vs[j] = a.cvs[so];
+                }
+            }
         }
-        if (a.pages > 0) {
-            offs[i] = (uint32_t)((page * a.c_ps + kvh * a.c_hs + at * a.c_ts) * (I8 ? 1 : 2) / 16);
-            if constexpr (I8) {
-                const int64_t so = page * a.s_ps + kvh * a.s_hs + at * a.s_ts;
-                kscale[i] = a.cks[so] * a.scale * 1.44269504f;
-                const float vs = a.cvs[so];
-                vscale[i] = vs;
-                vmax = fmaxf(vmax, __builtin_fabsf(vs));
+        if constexpr (I8) {
+#pragma unroll
+            for (int j = 0; j < PT; ++j) {
+                const int i = tid + j * 64 * NW;
+                if (i < tiles * kAttnTile) {
+                    kscale[i] = ks[j] * a.scale * 1.44269504f;
+                    vscale[i] = vs[j];
+                    vmax = fmaxf(vmax, __builtin_fabsf(vs[j]));
+                }
             }
         }
     }
@@ -442,55 +466,83 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
 }
 
 // Joins the chunks of one sequence and head: a lane has four elements of the
-// values, P groups of lanes each add every P-th chunk, and their sums are
-// added in LDS, all in an order that the sizes fix.
+// values, P groups of lanes each add every P-th chunk (four at a time, under
+// a running M as above), and their sums are added in LDS, all in an order that
+// the sizes fix.  Bound by latency: the first loads go out before the length
+// is known, within the workspace whatever it is.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a)
 {
     constexpr int C = D / 4;                                 // lanes that hold the values, four each
     constexpr int P = 256 / C;                               // chunks added side by side
+    constexpr int U = 4;
     __shared__ f32x4v sums[P][C];
-    __shared__ float tops[4], ls[P];
-    const int tid = threadIdx.x;
+    __shared__ float ms[P], ls[P];
+    const int tid = threadIdx.x, c = tid % C, g = tid / C;
     const int64_t bh = blockIdx.x;
     const int h = (int)(bh % a.hq);
     const int64_t b = bh / a.hq;
+    const float2* const ml = a.part_ml + bh * a.splits;
+    const float* const part = a.part + bh * a.splits * D + 4 * c;
+    float2 x[U];
+    f32x4v v[U];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + P * u;
+            if (g < P && s < a.splits) {
+                x[u] = ml[s];
+                v[u] = *reinterpret_cast<const f32x4v*>(part + (int64_t)s * D);
+            }
+        }
+    };
+    load(g);
     const Visible vis = visible(a, a.lens[b]);
     if (vis.count <= a.chunk) return;                        // written by its only block
     const int splits = (int)((vis.count + a.chunk - 1) / a.chunk);
-    const float2* ml = a.part_ml + bh * a.splits;
-    const float* part = a.part + bh * a.splits * D;
-    float m = -INFINITY;
-    for (int s = tid; s < splits; s += 256) m = fmaxf(m, ml[s].x);
+    float m = -INFINITY, l = 0.0f;
+    f32x4v o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = g; g < P && s0 < splits; s0 += P * U) {
+        if (s0 != g) load(s0);
+        float top = m;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    if ((tid & 63) == 0) tops[tid >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    const int c = tid % C, g = tid / C;
-    if (g < P) {
-        f32x4v o = {0.0f, 0.0f, 0.0f, 0.0f};
-        float l = 0.0f;
-#pragma unroll 4
-        for (int s = g; s < splits; s += P) {
-            const float2 x = ml[s];
-            const f32x4v v = *reinterpret_cast<const f32x4v*>(part + (int64_t)s * D + 4 * c);
-            const float f = __builtin_amdgcn_exp2f(x.x - m);
-            l = __builtin_fmaf(f, x.y, l);
+        for (int u = 0; u < U; ++u)
+            if (s0 + P * u < splits) top = fmaxf(top, x[u].x);
+        const float old = __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        l *= old;
+        o = o * old;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, v[r], o[r]);
+        for (int u = 0; u < U; ++u) {
+            if (s0 + P * u < splits) {
+                const float f = __builtin_amdgcn_exp2f(x[u].x - m);
+                l = __builtin_fmaf(f, x[u].y, l);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, v[u][r], o[r]);
+            }
         }
+    }
+    if (g < P) {
         sums[g][c] = o;
-        if (c == 0) ls[g] = l;
+        if (c == 0) {
+            ms[g] = m;
+            ls[g] = l;
+        }
     }
     __syncthreads();
     if (tid < C) {
-        f32x4v o = sums[0][tid];
-        float l = ls[0];
+        m = ms[0];
 #pragma unroll
-        for (int p = 1; p < P; ++p) {
-            o = o + sums[p][tid];
-            l = l + ls[p];
+        for (int p = 1; p < P; ++p) m = fmaxf(m, ms[p]);
+        o = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+        l = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const float f = __builtin_amdgcn_exp2f(ms[p] - m);   // a group without chunks: 0
+            l = __builtin_fmaf(f, ls[p], l);
+            const f32x4v q = sums[p][tid];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, q[r], o[r]);
         }
         const float inv = 1.0f / l;
         uint2 w;
