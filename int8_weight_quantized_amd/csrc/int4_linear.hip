@@ -88,6 +88,11 @@ __device__ __forceinline__ void store_int4(const Int4Args& a, int64_t row, int64
 // operand row 4 (j % 4) + j / 4, which puts it into register j / 4 of lanes
 // G = j % 4: with up to 4 (8) rows only one (two) of the four accumulator
 // registers are in use, and only those get the scales (MR).
+//
+// 1 x 28672 x 5376: groups of 128 17.3 us (4.6 TB/s), groups of 32 with zero
+// points 20.4 us (4.5 TB/s): HBM, and the start and end of 256 to 896 blocks.
+// 1 x 4096 x 4096: 4.0 us, where a launch of three blocks takes 3.1 us.
+//
 // mask and base are int4_mask and int4_base in registers of the two kinds that
 // one and-or instruction takes (it has no room for constants).
 template <int DT>
@@ -117,18 +122,17 @@ struct Int4Few {
     static constexpr int xl = MB * MR;                       // 1 KiB loads of x: four rows of 128
     static constexpr int slot = (NT + xl + 1) * 1024;        // W, x, then scales and zeros
     static constexpr int loads = NT + xl + 1;
-    static constexpr int ahead = 2;                          // more waves hide more than longer rings
-    static constexpr int ring = KW * ahead * slot;
+    static constexpr int ring = KW * 2 * slot;               // more waves hide more than longer rings
     static constexpr int regs = NT * MB * MR;
     static constexpr int sums = KW * regs * 256;
-    static_assert(sums <= ring && ring <= 163840 && (ahead - 1) * loads < 64, "the ring, then the sums");
+    static_assert(sums <= ring && ring <= 163840 && loads < 64, "the ring, then the sums");
 };
 
 template <int DT, int GS, bool Z, int MR, int MB, int NT, int KW>
 __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 {
     using S = Int4Few<GS, MR, MB, NT, KW>;
-    constexpr int AH = S::ahead, XL = S::xl, L = S::loads;
+    constexpr int XL = S::xl, L = S::loads;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S::ring];
     const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -157,7 +161,7 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) w_base[t] = a.w + min(tile0 + t, tiles - 1) * a.chunks * 1024;
 
-    uint8_t* const my = ring + wave * (AH * S::slot);
+    uint8_t* const my = ring + wave * (2 * S::slot);
     const uint32_t my_lds = lds_addr(my);
     auto issue = [&](int slot, int c) {
         const uint32_t dst = my_lds + slot * S::slot;
@@ -194,11 +198,8 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 #pragma unroll
             for (int r = 0; r < MR; ++r) tot[t][b][r] = 0.0f;
 
-    if (nc > 0) {
-#pragma unroll
-        for (int i = 0; i < AH; ++i)
-            if (i < nc) issue(i, i);
-    }
+    if (nc > 0) issue(0, 0);
+    if (nc > 1) issue(1, 1);
     auto consume = [&](int slot, int c) {
         uint8_t* const base = my + slot * S::slot;
         const int kleft = (int)min<int64_t>(128, a.k - (int64_t)(cb + c) * 128);
@@ -249,22 +250,11 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // the slot is read
     };
-    int slot = 0, c = 0;
-    for (; c + AH <= nc; ++c) {                              // AH - 1 later chunks on their way
-        wait_vmcnt<(AH - 1) * L>();
-        consume(slot, c);
-        if (c + AH < nc) issue(slot, c + AH);
-        slot = slot + 1 == AH ? 0 : slot + 1;
-    }
-    for (; c < nc; ++c) {
-        const int later = nc - 1 - c;
-        if (AH > 5 && later == 4) wait_vmcnt<AH * L < 64 ? 4 * L : 0>();
-        else if (AH > 4 && later == 3) wait_vmcnt<AH * L < 64 ? 3 * L : 0>();
-        else if (AH > 3 && later == 2) wait_vmcnt<AH * L < 64 ? 2 * L : 0>();
-        else if (AH > 2 && later == 1) wait_vmcnt<L>();
+    for (int c = 0; c < nc; ++c) {
+        if (c + 1 < nc) wait_vmcnt<L>();                     // the next chunk is on its way
         else wait_vmcnt<0>();
-        consume(slot, c);
-        slot = slot + 1 == AH ? 0 : slot + 1;
+        consume(c & 1, c);
+        if (c + 2 < nc) issue(c & 1, c + 2);
     }
 
     // The waves' sums, over the rings, then in their order.
@@ -304,7 +294,7 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 // Bound at 128 rows: the matrix cores (busy 35 % of the time), the vector unit
 // (31 %: two fused multiply-adds per output and group, two operations per two
 // codes) and the LDS reads of x (49 %, 1 KiB for NT products) take turns
-// rather than overlap, with two waves a SIMD: 128 x 21504 x 5376 52 us, 563
+// rather than overlap, with two waves a SIMD: 128 x 21504 x 5376 54 us, 548
 // TFLOP/s.  Two blocks of four waves a CU overlap better than one of eight
 // waves (64 us).  At 32 rows HBM is as near: 32 x 21504 x 5376 23 us.
 template <int GS, int MB, int NT, int WN, int WK>

@@ -288,6 +288,22 @@ def test_attention_lowest_finite_scores():
     ref.assert_within(out, want, slack, "mean")
 
 
+@pytest.mark.parametrize("hidden", [16, 32, 304])
+def test_attention_scores_of_minus_infinity(hidden):
+    """Leading tokens whose score is -inf have no weight, be they a tile, a wave's share or whole
+    chunks; a sequence of nothing else is 0 / 0."""
+    c = make_cache(80, 1, 16, 128, "bf16", "bf16")
+    table, n = tables([700, 500], 16, 80)
+    c.k[table[0, :hidden // 16].long(), :, :, 0] = -float("inf")
+    c.k[table[1, :32].long(), :, :, 0] = -float("inf")      # 500 tokens: the row's other entries are no pages
+    q = rand(2, 4, 128, dtype=torch.bfloat16).to(cuda_device())
+    q[:, :, 0] = 1
+    out = ck.paged_attention(q, c, table, n)
+    want, slack = ref.attention(q[:1], c.k, c.v, None, None, table[:1, hidden // 16:], n[:1] - hidden, 128 ** -0.5, 0, 0)
+    ref.assert_within(out[:1], want, slack, "visible scores")
+    assert out[1].isnan().all()
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
