@@ -475,6 +475,25 @@ def test_int4_exact_on_whole_numbers(m, group):
     assert torch.equal(got.cpu().double(), want)
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [
+    (1, 20501, 392), (7, 20501, 392), (16, 24001, 264), (3, 9007, 520), (6, 9007, 520), (16, 9007, 520),
+    (21, 8230, 392), (21, 17003, 264), (37, 9007, 136), (37, 8230, 392), (70, 9007, 136), (70, 8230, 648),
+    (70, 20501, 264), (130, 17003, 264),
+])
+def test_int4_exact_for_every_block_shape(m, n, k, group, zeros):
+    """Wide outputs, where blocks of each shape are chosen: whole numbers, as above."""
+    dev = cuda_device()
+    _, codes, scales, z, _ = int4_inputs(m, n, k, group, zeros, False, "fp16")
+    g = torch.Generator().manual_seed(m + n)
+    x = torch.randint(-3, 4, (m, k), generator=g).to(torch.float16).to(dev)
+    scales = (2.0 ** torch.randint(-2, 2, scales.shape, generator=g)).to(torch.float16).to(dev)
+    got = ck.int4_linear(x, ck.int4_pack(codes, scales, z, group=group), out_dtype="fp32")
+    want, _ = ref.int4(x, codes, scales, z, None, group)
+    assert torch.equal(got.cpu().double(), want)
+
+
 def test_int4_pack_layout():
     """The layout that include/ck_int8.h gives, word by word."""
     n, k, group = 37, 200, 64
