@@ -176,7 +176,8 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = lane >> 4, i16 = lane & 15;
-    // chunk fastest: a sequence's blocks run side by side
+    // chunk fastest: a sequence's blocks run side by side (4 x 131072 bf16 tokens
+    // 394 us, 48 ragged int8 sequences 53 us; chunk slowest 400 and 57 us)
     const int split = blockIdx.x % a.splits;
     const int64_t rest = blockIdx.x / a.splits;
     const int rb = (int)(rest % a.row_blocks);
