@@ -528,8 +528,9 @@ ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipS
  * m the largest score, over the visible tokens j of sequence b, of key head
  * h / (hq / hk).  Visible are j < lens[b], and with window > 0 of those only
  * the last `window` and the first `sinks`.  Scores, exponentials and sums are
- * fp32, the products on the matrix cores with p_j in two 16-bit parts (see
- * the kernel).  A sequence without visible tokens gives zeros.
+ * fp32, the products on the matrix cores with p_j in 16-bit parts that
+ * together hold it to 2^-22 or better.  A sequence without visible tokens
+ * gives zeros.
  *
  * q          [in]  16-bit [batch, hq, head_dim], rows at b * q_batch_stride +
  *                  h * q_head_stride.

@@ -33,9 +33,11 @@
 // next product's second operand (the order of the 32 tokens is free as long
 // as V's is the same), so the weights pass from one product to the other in
 // registers.  The first operand, V^T, comes out of row-major LDS by
-// transposing reads of the same tokens.  Weights enter as two 16-bit parts,
-// hi = round(p) and lo = round(p - hi): the products see p to 2^-16 or
-// better, and the matrix cores have the time.
+// transposing reads of the same tokens.  Weights enter as 16-bit parts, each
+// the rounded rest that those before it left: three of bf16, which hold p to
+// fp32's own 2^-24 (two would leave 2^-16, which shows where values cancel),
+// and two of fp16, to 2^-22.  The matrix cores have the time: 4 x 131072 bf16
+// tokens take 394 us with two parts and with three.
 //
 // An int8 cache is multiplied in fp16: codes are exact in it, and cost five
 // operations for four (byte | 0x6400 is 1024 + byte).  A head's query is
@@ -165,6 +167,7 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     using Sh = AttnShape<RB>;
     constexpr int NW = Sh::waves, NL = Sh::loads, KK = D / 32, DB = D / 16;
     constexpr int MT = I8 ? CK_DT_FP16 : DT;                 // the products' type
+    constexpr int WP = MT == CK_DT_FP16 ? 2 : 3;             // 16-bit parts of a weight
     // fp16 weights are kept 2^6 higher, away from its subnormals: at most 2^14
     constexpr float kLift = MT == CK_DT_FP16 ? 6.0f : 0.0f;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[NW * 2 * Sh::tile];
@@ -402,13 +405,18 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
                 p[4 * u] *= vs.x * vinv; p[4 * u + 1] *= vs.y * vinv; p[4 * u + 2] *= vs.z * vinv; p[4 * u + 3] *= vs.w * vinv;
             }
         }
-        v4i hi, lo;
+        v4i part[WP];                                        // the weights are their sum
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const uint32_t h = narrow2<MT>(p[2 * w], p[2 * w + 1]);
-            const float2 back = widen2<MT>(h);
-            hi[w] = (int)h;
-            lo[w] = (int)narrow2<MT>(p[2 * w] - back.x, p[2 * w + 1] - back.y);
+            float x = p[2 * w], y = p[2 * w + 1];
+#pragma unroll
+            for (int i = 0; i < WP; ++i) {
+                const uint32_t h = narrow2<MT>(x, y);
+                const float2 back = widen2<MT>(h);
+                part[i][w] = (int)h;
+                x -= back.x;
+                y -= back.y;
+            }
         }
         if (more) wait_vmcnt<NL>();                          // V of this tile; the next K came after it
         else wait_vmcnt<0>();
@@ -425,8 +433,8 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
                 const uint2 y = read_tr16(vring + (row + 16) * RB + ((c ^ Sh::swz2(row + 16)) << 4) + (i16 & 1) * 8);
                 vf = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
             }
-            acc[d] = mfma16<MT>(vf, hi, acc[d]);
-            acc[d] = mfma16<MT>(vf, lo, acc[d]);
+#pragma unroll
+            for (int i = 0; i < WP; ++i) acc[d] = mfma16<MT>(vf, part[i], acc[d]);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // V is read
         if (more) issue_v();

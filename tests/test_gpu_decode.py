@@ -304,6 +304,47 @@ def test_attention_scores_of_minus_infinity(hidden):
     assert out[1].isnan().all()
 
 
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("fp16", "fp16"), ("int8", "bf16"), ("int8", "fp16")])
+def test_attention_weights_to_32_bits(cache, dtype):
+    """Values that almost cancel, so that the output shows the weights' own precision.
+
+    Tokens 0 and 2 have score 0 and the values -hi and -lo, token 1 the value 1 and the weight
+    e = exp(score) with hi + lo = e to 14 bits or more: out = (e - hi - lo) / (2 + e).
+    Allowed, in units of 2^-24 of (e + hi + |lo|) / (2 + e): 12 for the weight (three roundings of the
+    score's change to base 2, at most 1 in magnitude, one of its offset from M, at most 8 in
+    magnitude, the exponential's 2, a value scale's 3, its own to 32 bits), 8 for the products and
+    sums, 4 for the division."""
+    dev = cuda_device()
+    hq, d, n = 16, 64, 8
+    t = DT[dtype]
+    score = -torch.linspace(0.02, 0.69, n * hq).to(t).view(n, hq)
+    e = torch.exp(score.double())
+    k, v = torch.zeros((n, 1, 4, d)), torch.zeros((n, 1, 4, d))
+    k[:, 0, 1, 0] = 1
+    ks = vs = None
+    if cache == "int8":
+        v[:, 0, 1], v[:, 0, 0, :hq] = 64, -torch.round(e * 128)
+        v[:, 0, 2, :hq] = -torch.round((e + v[:, 0, 0, :hq].double() / 128) * 2 ** 14).float()
+        vs = torch.tensor([2.0 ** -7, 2.0 ** -6, 2.0 ** -14, 0.0]).expand(n, 1, 4).contiguous()
+        ks = torch.ones((n, 1, 4))
+        parts = v[:, 0, :3].double() * vs[:, 0, :3, None].double()
+        k, v = k.to(torch.int8), v.to(torch.int8)
+    else:
+        v[:, 0, 1], v[:, 0, 0, :hq] = 1, -e.to(t).float()
+        v[:, 0, 2, :hq] = -(e - e.to(t).double()).to(t).float()
+        parts = v[:, 0, :3].to(t).double()
+        k, v = k.to(t), v.to(t)
+    c = ck.KVCache(*(None if x is None else x.to(dev) for x in (k, v, ks, vs)))
+    q = torch.zeros((n, hq, d), dtype=t)
+    q[:, :, 0] = score
+    table = torch.arange(n, dtype=torch.int32, device=dev)[:, None]
+    lens = torch.full((n,), 3, dtype=torch.int32, device=dev)
+    out = ck.paged_attention(q.to(dev), c, table, lens, 1.0)
+    weight = torch.stack([torch.ones_like(e), e, torch.ones_like(e)], -1)
+    want = weight @ parts / (2 + e[..., None])
+    ref.assert_within(out, want, 24 * ref.U32 * (weight @ parts.abs()) / (2 + e[..., None]), "almost nothing")
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
