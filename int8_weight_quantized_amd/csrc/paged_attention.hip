@@ -43,8 +43,8 @@
 // operations for four (byte | 0x6400 is 1024 + byte).  A head's query is
 // scaled by a power of two to the range of fp16 (exact but for elements
 // below 2^-38 of its largest), the scale of a key row is applied to its
-// score, and that of a value row to its weight, relative to the chunk's
-// largest so that it cannot overflow.
+// score, and that of a value row to its weight, relative to a power of two
+// near the chunk's largest so that it cannot overflow.
 
 struct AttnArgs {
     const uint16_t* q;
@@ -294,12 +294,15 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         }
         return;
     }
-    float vinv = 1.0f;
+    // Value scales are taken relative to 2^ve, which the largest of the chunk is
+    // just below: exact, and right for subnormal scales too, whose reciprocal
+    // would be infinite.
+    int ve = 0;
     if constexpr (I8) {
         vmax = wave_v[0];
 #pragma unroll
         for (int w = 1; w < NW; ++w) vmax = fmaxf(vmax, wave_v[w]);
-        vinv = vmax > 0.0f ? 1.0f / vmax : 0.0f;
+        ve = vmax > 0.0f ? __builtin_amdgcn_frexp_expf(vmax) : 0;
     }
 
     uint8_t* const kring = ring + wave * (2 * Sh::tile);
@@ -402,7 +405,9 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float4 vs = *reinterpret_cast<const float4*>(&vscale[tok0 + 16 * u]);
-                p[4 * u] *= vs.x * vinv; p[4 * u + 1] *= vs.y * vinv; p[4 * u + 2] *= vs.z * vinv; p[4 * u + 3] *= vs.w * vinv;
+                const float v[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[4 * u + r] *= __builtin_amdgcn_ldexpf(v[r], -ve);
             }
         }
         v4i part[WP];                                        // the weights are their sum
@@ -469,7 +474,10 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, v[r], o[r]);
         }
-        if constexpr (I8) o = o * vmax;
+        if constexpr (I8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = __builtin_amdgcn_ldexpf(o[r], ve);
+        }
         if (last) {
             const float inv = 1.0f / l;
             uint2 w;

@@ -345,6 +345,21 @@ def test_attention_weights_to_32_bits(cache, dtype):
     ref.assert_within(out, want, 24 * ref.U32 * (weight @ parts.abs()) / (2 + e[..., None]), "almost nothing")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("exponent", [-149, -140, -130, -127, -100, 0, 90])
+def test_attention_value_scales_of_any_size(exponent, dtype):
+    """An int8 cache whose value scales are subnormal, small or large, all of them finite."""
+    c = make_cache(40, 2, 16, 128, "int8", dtype)
+    c.v_scale.fill_(2.0 ** exponent)
+    c.v.abs_()
+    table, n = tables([500, 20], 16, 40)
+    q = rand(2, 8, 128, dtype=DT[dtype]).to(cuda_device())
+    if dtype == "fp16" and exponent > 9:
+        assert ck.paged_attention(q, c, table, n).isinf().any()
+    else:
+        check_attention(q, c, table, n)
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
