@@ -39,12 +39,18 @@
 // and two of fp16, to 2^-22.  The matrix cores have the time: 4 x 131072 bf16
 // tokens take 394 us with two parts and with three.
 //
-// An int8 cache is multiplied in fp16: codes are exact in it, and cost five
-// operations for four (byte | 0x6400 is 1024 + byte).  A head's query is
-// scaled by a power of two to the range of fp16 (exact but for elements
-// below 2^-38 of its largest), the scale of a key row is applied to its
-// score, and that of a value row to its weight, relative to a power of two
-// near the chunk's largest so that it cannot overflow.
+// The keys of an int8 cache are multiplied in fp16: codes are exact in it,
+// and cost five operations for four (byte | 0x6400 is 1024 + byte).  A head's
+// query is scaled by a power of two to the range of fp16 (exact for bf16
+// elements down to 2^-31 of its largest and fp16 ones down to 2^-28; lost below
+// 2^-38), and the scale of a key row is applied to its score.  Values are multiplied in bf16 (six operations for
+// four codes): a row's scale is applied to its weight, and the product has to
+// hold what a light token's row or a row of a small scale contributes beside a
+// heavy one or one of a large scale.  (In fp16, whose parts end at 2^-24, the
+// rows whose product lay 2^26 below the largest were 4 % off and those 2^32
+// below were lost; 48 ragged sequences took 53.3 us so, 55.1 in bf16.)  Scales are
+// taken relative to a power of two near the chunk's largest, so that the
+// product neither overflows nor is subnormal.
 
 struct AttnArgs {
     const uint16_t* q;
@@ -133,6 +139,24 @@ __device__ __forceinline__ v4i codes8_f16(uint2 w)
     return v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
 }
 
+// Four int8 codes to bf16, exactly: the upper halves of their fp32 values.
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i));
+    lo = __builtin_amdgcn_perm(__float_as_uint(f[1]), __float_as_uint(f[0]), 0x07060302u);
+    hi = __builtin_amdgcn_perm(__float_as_uint(f[3]), __float_as_uint(f[2]), 0x07060302u);
+}
+
+__device__ __forceinline__ v4i codes8_bf16(uint2 w)
+{
+    uint32_t o[4];
+    codes_bf16(w.x, o[0], o[1]);
+    codes_bf16(w.y, o[2], o[3]);
+    return v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+}
+
 template <int DT>
 __device__ __forceinline__ f32x4v mfma16(const v4i& a, const v4i& b, const f32x4v& c)
 {
@@ -166,10 +190,11 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     constexpr int RB = D * (I8 ? 1 : 2);
     using Sh = AttnShape<RB>;
     constexpr int NW = Sh::waves, NL = Sh::loads, KK = D / 32, DB = D / 16;
-    constexpr int MT = I8 ? CK_DT_FP16 : DT;                 // the products' type
-    constexpr int WP = MT == CK_DT_FP16 ? 2 : 3;             // 16-bit parts of a weight
+    constexpr int KT = I8 ? CK_DT_FP16 : DT;                 // the products' types
+    constexpr int VT = I8 ? CK_DT_BF16 : DT;
+    constexpr int WP = VT == CK_DT_FP16 ? 2 : 3;             // 16-bit parts of a weight
     // fp16 weights are kept 2^6 higher, away from its subnormals: at most 2^14
-    constexpr float kLift = MT == CK_DT_FP16 ? 6.0f : 0.0f;
+    constexpr float kLift = VT == CK_DT_FP16 ? 6.0f : 0.0f;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[NW * 2 * Sh::tile];
     __shared__ __attribute__((aligned(16))) uint32_t offs[kAttnChunk];
     __shared__ __attribute__((aligned(16))) float kscale[I8 ? kAttnChunk : 4], vscale[I8 ? kAttnChunk : 4];
@@ -358,7 +383,7 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
                 } else {
                     kf = *reinterpret_cast<const v4i*>(kr + (((4 * kk + G) ^ Sh::swz(row)) << 4));
                 }
-                s[u] = mfma16<MT>(kf, qf[kk], s[u]);
+                s[u] = mfma16<KT>(kf, qf[kk], s[u]);
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // K is read: its place is free
@@ -416,8 +441,8 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
             float x = p[2 * w], y = p[2 * w + 1];
 #pragma unroll
             for (int i = 0; i < WP; ++i) {
-                const uint32_t h = narrow2<MT>(x, y);
-                const float2 back = widen2<MT>(h);
+                const uint32_t h = narrow2<VT>(x, y);
+                const float2 back = widen2<VT>(h);
                 part[i][w] = (int)h;
                 x -= back.x;
                 y -= back.y;
@@ -431,7 +456,7 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
             if constexpr (I8) {
                 // row r of the eight: token 4 G + r of the first tile or 4 G + r - 4 of the second
                 const int r = i16 >> 1, row = 4 * G + (r & 3) + 16 * (r >> 2);
-                vf = codes8_f16(read_tr8(vring + row * RB + ((d ^ Sh::swz(row)) << 4) + (i16 & 1) * 8));
+                vf = codes8_bf16(read_tr8(vring + row * RB + ((d ^ Sh::swz(row)) << 4) + (i16 & 1) * 8));
             } else {
                 const int row = 4 * G + (i16 >> 2), c = 2 * d + ((i16 >> 1) & 1);
                 const uint2 x = read_tr16(vring + row * RB + ((c ^ Sh::swz2(row)) << 4) + (i16 & 1) * 8);
@@ -439,7 +464,7 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
                 vf = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
             }
 #pragma unroll
-            for (int i = 0; i < WP; ++i) acc[d] = mfma16<MT>(vf, part[i], acc[d]);
+            for (int i = 0; i < WP; ++i) acc[d] = mfma16<VT>(vf, part[i], acc[d]);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // V is read
         if (more) issue_v();

@@ -360,6 +360,51 @@ def test_attention_value_scales_of_any_size(exponent, dtype):
         check_attention(q, c, table, n)
 
 
+def check_light_tokens(cache, dtype):
+    """600 tokens in several chunks.  Head h gives the first one a score `nats[h]` above all others',
+    and its values are zero.  The others' values are large enough for what is left to be normal
+    numbers of the output's type."""
+    nats = torch.tensor([4.0, 8.0, 11.0, 14.0, 16.0, 16.75, 18.0, 18.5, 20.0, 22.0, 23.5, 24.0, 26.0, 28.0, 31.0, 35.0])
+    dev = cuda_device()
+    c = make_cache(40, 1, 16, 64, cache, dtype)
+    table, n = tables([600, 30], 16, 40)
+    for i in range(2):
+        at = table[i, :-(-int(n[i]) // 16)].long()
+        c.k[at, 0], c.k[at[0], 0, 0, 0] = 0, 1
+        if cache == "int8":
+            c.k_scale[at, 0] = 1.0
+            c.v_scale[at, 0] *= 2.0 ** 12
+        else:
+            c.v[at, 0] *= 2.0 ** 12
+        c.v[at, 0] = c.v[at, 0].abs()
+        c.v[at[0], 0, 0] = 0
+    q = torch.zeros((2, 16, 64), dtype=DT[dtype], device=dev)
+    q[:, :, 0] = nats.to(dev)
+    check_attention(q, c, table, n, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_int8_light_tokens_beside_a_heavy_one_without_value(dtype):
+    """The first token outweighs all others and its values are zero: the output is the others', of
+    weights down to 2^-51."""
+    check_light_tokens("int8", dtype)
+
+
+@pytest.mark.parametrize("spread", [16, 22, 26, 30, 40])
+def test_attention_int8_value_scales_far_apart(spread):
+    """One row's value scale is 2^spread (in the second sequence 2^(2 spread)) times the others' and
+    its weight e^-40 or less: the others' mean is as exact as without it."""
+    c = make_cache(40, 2, 16, 128, "int8", "fp16")
+    table, n = tables([500, 100], 16, 40)
+    heads = torch.arange(2, device=cuda_device())
+    for i in range(2):
+        page = table[i, 0].long()
+        c.k[page, heads, 3], c.v[page, heads, 3] = 127, 127
+        c.k_scale[page, heads, 3], c.v_scale[page, heads, 3] = 0.05, 2.0 ** spread * float(c.v_scale.max())
+    q = rand(2, 8, 128, dtype=torch.float16).abs().to(cuda_device())
+    check_attention(-q, c, table, n)
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
