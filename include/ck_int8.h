@@ -529,7 +529,8 @@ ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipS
  * h / (hq / hk).  Visible are j < lens[b], and with window > 0 of those only
  * the last `window` and the first `sinks`.  Scores, exponentials and sums are
  * fp32, the products on the matrix cores with p_j in 16-bit parts that
- * together hold it to 2^-22 or better.  A sequence without visible tokens
+ * together hold it to 2^-22 (bf16 and int8 caches: 2^-24) of itself, or in an
+ * fp16 cache to 2^-54 of the largest.  A sequence without visible tokens
  * gives zeros.
  *
  * q          [in]  16-bit [batch, hq, head_dim], rows at b * q_batch_stride +

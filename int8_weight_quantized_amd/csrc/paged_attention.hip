@@ -36,8 +36,12 @@
 // transposing reads of the same tokens.  Weights enter as 16-bit parts, each
 // the rounded rest that those before it left: three of bf16, which hold p to
 // fp32's own 2^-24 (two would leave 2^-16, which shows where values cancel),
-// and two of fp16, to 2^-22.  The matrix cores have the time: 4 x 131072 bf16
-// tokens take 394 us with two parts and with three.
+// and four of fp16.  fp16 ends at 2^-24, so its last two parts are 2^23 times
+// finer and have sums of their own: a weight is held to 2^-22 of itself or
+// 2^-54 of the largest one.  (With the first two alone, light tokens beside a
+// heavy one of little value were 0.2 % off at 2^-24 of it and lost at 2^-32.)
+// The matrix cores have the time: 4 x 131072 bf16 tokens take 394 us with two
+// parts and with three, 8 x 32768 fp16 ones 194 us with two and with four.
 //
 // The keys of an int8 cache are multiplied in fp16: codes are exact in it,
 // and cost five operations for four (byte | 0x6400 is 1024 + byte).  A head's
@@ -192,9 +196,12 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     constexpr int NW = Sh::waves, NL = Sh::loads, KK = D / 32, DB = D / 16;
     constexpr int KT = I8 ? CK_DT_FP16 : DT;                 // the products' types
     constexpr int VT = I8 ? CK_DT_BF16 : DT;
-    constexpr int WP = VT == CK_DT_FP16 ? 2 : 3;             // 16-bit parts of a weight
-    // fp16 weights are kept 2^6 higher, away from its subnormals: at most 2^14
+    constexpr int WP = VT == CK_DT_FP16 ? 4 : 3;             // 16-bit parts of a weight
+    // fp16 weights are kept 2^6 higher, at most 2^14; the last two parts hold
+    // 2^23 times what the first two left, at most 2^14 too, in sums of their own
+    constexpr int NA = VT == CK_DT_FP16 ? 2 : 1;
     constexpr float kLift = VT == CK_DT_FP16 ? 6.0f : 0.0f;
+    constexpr float kFine = 8388608.0f;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[NW * 2 * Sh::tile];
     __shared__ __attribute__((aligned(16))) uint32_t offs[kAttnChunk];
     __shared__ __attribute__((aligned(16))) float kscale[I8 ? kAttnChunk : 4], vscale[I8 ? kAttnChunk : 4];
@@ -354,9 +361,11 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         }
     };
 
-    f32x4v acc[DB];
+    f32x4v acc[NA][DB];
 #pragma unroll
-    for (int d = 0; d < DB; ++d) acc[d] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[i][d] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
     float M = kAttnLow, L = 0.0f;
     const float sc = I8 ? qscale : a.scale * 1.44269504f;
 
@@ -415,8 +424,12 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
             const float f = __builtin_amdgcn_exp2f(M - m);
             M = m;
             L *= f;
+            if (t != wave) {                                 // the first tile's sums are still zero
 #pragma unroll
-            for (int d = 0; d < DB; ++d) acc[d] = acc[d] * f;
+                for (int i = 0; i < NA; ++i)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) acc[i][d] = acc[i][d] * f;
+            }
         }
         const float ref = M - kLift;
         float sum = 0.0f;
@@ -446,6 +459,10 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
                 part[i][w] = (int)h;
                 x -= back.x;
                 y -= back.y;
+                if (NA == 2 && i == 1) {
+                    x *= kFine;
+                    y *= kFine;
+                }
             }
         }
         if (more) wait_vmcnt<NL>();                          // V of this tile; the next K came after it
@@ -464,7 +481,10 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
                 vf = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
             }
 #pragma unroll
-            for (int i = 0; i < WP; ++i) acc[d] = mfma16<VT>(vf, part[i], acc[d]);
+            for (int i = 0; i < WP; ++i) {
+                f32x4v& sum = acc[NA == 2 ? i / 2 : 0][d];
+                sum = mfma16<VT>(vf, part[i], sum);
+            }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // V is read
         if (more) issue_v();
@@ -476,8 +496,11 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     L += __shfl_xor(L, 32);
     float* const own = reinterpret_cast<float*>(kring);
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-        *reinterpret_cast<f32x4v*>(own + i16 * D + (((4 * d + G) ^ (i16 & 7)) << 2)) = acc[d];
+    for (int d = 0; d < DB; ++d) {
+        f32x4v sum = acc[0][d];
+        if constexpr (NA == 2) sum = sum + acc[1][d] * (1.0f / kFine);
+        *reinterpret_cast<f32x4v*>(own + i16 * D + (((4 * d + G) ^ (i16 & 7)) << 2)) = sum;
+    }
     if (lane < 16) {
         wave_m[wave][lane] = M;
         wave_l[wave][lane] = L;

@@ -405,6 +405,12 @@ def test_attention_int8_value_scales_far_apart(spread):
     check_attention(-q, c, table, n)
 
 
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("fp16", "fp16")])
+def test_attention_light_tokens_beside_a_heavy_one_without_value(cache, dtype):
+    """As for the int8 cache above."""
+    check_light_tokens(cache, dtype)
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
