@@ -348,8 +348,9 @@ def int4_pack(codes, scales, zeros=None, group: int = 128):
     w = torch.empty(tiles * chunks * 1024, dtype=torch.uint8, device=dev)
     s = torch.empty((tiles, groups, 16), dtype=scales.dtype, device=dev)
     z = None if zeros is None else torch.empty((tiles, groups, 16), dtype=torch.uint8, device=dev)
-    ldc, lds, ldz = (t.stride(0) if t is not None and n > 1 else groups for t in (codes, scales, zeros))
-    _ck.ck_int4_pack(codes.data_ptr(), max(ldc, k // 2), scales.data_ptr(), lds,
+    ldc, lds, ldz = (t.stride(0) if t is not None and n > 1 else row
+                     for t, row in ((codes, k // 2), (scales, groups), (zeros, groups)))
+    _ck.ck_int4_pack(codes.data_ptr(), ldc, scales.data_ptr(), lds,
                      0 if z is None else zeros.data_ptr(), ldz, w.data_ptr(), s.data_ptr(),
                      0 if z is None else z.data_ptr(), n, k, group, _ck._stream(codes))
     return Int4Weight(w, s, z, n, k, group, scales.dtype)

@@ -420,6 +420,20 @@ def test_binding_int4(host):
             ck.int4_linear(**{**dict(x=bf(3, 256), weight=w), **kw})
 
 
+@pytest.mark.parametrize("stride", [0, 1, 64, 127])
+def test_binding_int4_pack_passes_the_codes_stride(host, monkeypatch, stride):
+    """Rows of codes that overlap (an expanded row among them) reach the library with the stride that
+    they have, which it refuses; the stride of a single row is not looked at."""
+    seen = []
+    monkeypatch.setattr(ck, "ck_int4_pack", lambda codes, ldc, *a: seen.append(ldc))
+    codes = torch.zeros(31 * stride + 128, dtype=torch.uint8).as_strided((32, 128), (stride, 1))
+    ck.int4_pack(codes, bf(32, 2))
+    assert seen == [stride]
+    assert ck.lib().ck_int4_pack(P, stride, P, 2, 0, 0, P, P, 0, 32, 256, 128, 0) == BAD
+    ck.int4_pack(codes[:1], bf(1, 2))
+    assert seen[1] >= 128
+
+
 def test_rope_table():
     t = ck.rope_table(1000, 64, 500000.0, device="cpu")
     assert t.shape == (1000, 64) and t.dtype == torch.float32
