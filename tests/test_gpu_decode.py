@@ -411,6 +411,39 @@ def test_attention_light_tokens_beside_a_heavy_one_without_value(cache, dtype):
     check_light_tokens(cache, dtype)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+def test_attention_bad_pages_of_a_split_sequence(cache):
+    """A bad page in the first, a middle or the last chunk of a sequence in several chunks makes that
+    sequence NaN whatever the workspace held, and no other."""
+    lens = [3000, 3000, 3000, 3000, 40]
+    pages = sum(-(-n // 16) for n in lens)
+    c = make_cache(pages, 2, 16, 128, cache, "bf16")
+    table, n = tables(lens, 16, pages)
+    q = rand(5, 8, 128, dtype=torch.bfloat16).to(cuda_device())
+    good = check_attention(q, c, table, n)
+    bad = table.clone()
+    bad[0, 0], bad[1, 90], bad[2, 187] = -1, pages, 1 << 30
+    ws = ck.paged_attention_workspace(q, c, table)
+    assert ws is not None
+    for byte in (0, 127, 255):
+        ws.fill_(byte)
+        out = ck.paged_attention(q, c, bad, n, workspace=ws)
+        assert out[:3].isnan().all()
+        assert torch.equal(out[3:], good[3:])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("width", [1, 300])
+def test_attention_cache_without_pages(cache, width):
+    """No page is inside a cache of none: NaN where a token is visible, zeros where none is."""
+    dev = cuda_device()
+    c = ck.KVCache.empty(0, 2, 16, 128, cache, dev)
+    table = torch.zeros((3, width), dtype=torch.int32, device=dev)
+    n = torch.tensor([5, 0, 16 * width], dtype=torch.int32, device=dev)
+    out = ck.paged_attention(rand(3, 4, 128, dtype=torch.bfloat16).to(dev), c, table, n)
+    assert out[0].isnan().all() and out[2].isnan().all() and (out[1] == 0).all()
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
