@@ -541,6 +541,8 @@ ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipS
  *                  table[b, j / page_size].
  * lens       [in]  int32 [batch], on the device; values past
  *                  table_width * page_size count as that, negative ones as 0.
+ * The cache's k and v each span at most 64 GiB from their first to their last
+ * element (CK_ERR_UNSUPPORTED otherwise).
  * A visible token whose page is outside [0, pages) is an error of its
  * sequence, and its output rows are NaN; nothing outside the cache is read.
  * Cache rows that are not visible are never used, whatever they hold.

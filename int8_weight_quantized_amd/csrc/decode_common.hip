@@ -42,6 +42,21 @@ bool rows16(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t hs
     return aligned(p, 16) && (tokens <= 1 || ts % 8 == 0) && (heads <= 1 || hs % 8 == 0);
 }
 
+// How far a [pages, heads, page_size] tensor reaches, in elements past its
+// start (as a double: the products may pass 64 bits); negative if a stride
+// that counts is.  The stride of a dimension with one element does not.
+double cache_reach(const ck_kv_cache* c, int64_t ps, int64_t hs, int64_t ts, int64_t row)
+{
+    const int64_t n[3] = {c->pages, c->heads, c->page_size}, stride[3] = {ps, hs, ts};
+    double reach = (double)row;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (stride[i] < 0) return -1.0;
+        reach += (double)(n[i] - 1) * (double)stride[i];
+    }
+    return reach;
+}
+
 // A paged cache for activations of type dtype; `align` bytes between rows.
 ck_status check_cache(const ck_kv_cache* c, int dtype, int64_t head_dim, int align)
 {
@@ -53,9 +68,11 @@ ck_status check_cache(const ck_kv_cache* c, int dtype, int64_t head_dim, int ali
     if (c->pages > (int64_t(1) << 31) - 1) return fail(CK_ERR_UNSUPPORTED, "too many pages");
     if (c->head_dim != head_dim) return fail(CK_ERR_INVALID_ARG, "cache and heads disagree on head_dim");
     if (c->pages > 0 && (!c->k || !c->v)) return fail(CK_ERR_INVALID_ARG, "NULL cache");
-    if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0 || c->scale_page_stride < 0 ||
-        c->scale_head_stride < 0 || c->scale_token_stride < 0)
-        return fail(CK_ERR_INVALID_ARG, "negative cache stride");
+    const double reach = cache_reach(c, c->page_stride, c->head_stride, c->token_stride, head_dim);
+    const double scale_reach = c->dtype == CK_DT_INT8
+        ? cache_reach(c, c->scale_page_stride, c->scale_head_stride, c->scale_token_stride, 1) : 0.0;
+    if (reach < 0.0 || scale_reach < 0.0) return fail(CK_ERR_INVALID_ARG, "negative cache stride");
+    if (reach > 0x1p60 || scale_reach > 0x1p60) return fail(CK_ERR_UNSUPPORTED, "cache strides too large");
     if (c->page_size > 1 && c->token_stride < head_dim)
         return fail(CK_ERR_INVALID_ARG, "token_stride smaller than head_dim");
     const int esz = c->dtype == CK_DT_INT8 ? 1 : 2;

@@ -741,9 +741,8 @@ extern "C" ck_status ck_paged_attention(const ck_attention_args* args, const ck_
     const bool i8 = cache->dtype == CK_DT_INT8, f16 = p.dtype == CK_DT_FP16;
     const int64_t d = cache->head_dim, row_bytes = d * (i8 ? 1 : 2);
     // row offsets are 32 bits of 16-byte units
-    const int64_t reach = cache->pages * cache->page_stride + cache->heads * cache->head_stride +
-                          cache->page_size * cache->token_stride;
-    if (reach * (row_bytes / d) >= (int64_t(1) << 36)) return fail(CK_ERR_UNSUPPORTED, "the cache spans 64 GiB or more");
+    if (cache_reach(cache, cache->page_stride, cache->head_stride, cache->token_stride, d) * (row_bytes / d) > 0x1p36)
+        return fail(CK_ERR_UNSUPPORTED, "the cache spans more than 64 GiB");
     AttnArgs a{};
     const int64_t most = most_visible(p.table_width, cache->page_size, p.window, p.sinks);
     a.chunk = (int)attn_chunk(p.batch, p.hq, cache->heads, row_bytes, most);

@@ -185,6 +185,40 @@ def test_attention_workspace():
         assert ck.ck_paged_attention_workspace(*bad) == -1
 
 
+FAR = 1 << 62
+
+
+@pytest.mark.parametrize("kw,status", [
+    # the stride of a dimension with one element is not looked at
+    (dict(pages=1, page_stride=FAR), HIP),
+    (dict(pages=1, page_stride=-4096), HIP),
+    (dict(heads=1, head_stride=-8), HIP),
+    (dict(page_size=1, token_stride=-1), HIP),
+    (dict(pages=1, page_stride=-8, dtype=ck.CK_DT_INT8, k_scale=P, v_scale=P, scale_page_stride=-1), HIP),
+    # others may not leave 64 bits
+    (dict(pages=3, page_stride=FAR), UNS),
+    (dict(heads=2, head_stride=FAR), UNS),
+    (dict(pages=(1 << 31) - 1, page_stride=1 << 40), UNS),
+    (dict(dtype=ck.CK_DT_INT8, k_scale=P, v_scale=P, scale_page_stride=FAR), UNS),
+    (dict(page_stride=-4096), BAD),
+    (dict(head_stride=-2048), BAD),
+    (dict(dtype=ck.CK_DT_INT8, k_scale=P, v_scale=P, scale_token_stride=-1), BAD),
+])
+def test_cache_strides(kw, status):
+    no_gpu(status)
+    c, hk = cache(**kw), kw.get("heads", 2)
+    assert call_qk(qk_args(hk=hk, hq=8), c) == status
+    assert ck.lib().ck_paged_attention(ctypes.byref(attn_args()), ctypes.byref(c), 0) == status
+
+
+def test_cache_of_64_gib():
+    """Attention's row offsets are 32 bits of 16-byte units: a cache up to 64 GiB, to the byte."""
+    no_gpu(HIP)
+    pages = (1 << 36) // (2 * 4096)
+    for n, status in ((pages, HIP), (pages + 1, UNS)):
+        assert ck.lib().ck_paged_attention(ctypes.byref(attn_args()), ctypes.byref(cache(pages=n)), 0) == status
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(), HIP),
     (dict(n=0, codes=0, w=0), OK),
