@@ -655,7 +655,8 @@ int attn_waves(int64_t row_bytes)
 // - / 67, 1024 394 / 54, 2048 380 / 61.
 int64_t attn_chunk(int64_t batch, int64_t hq, int64_t hk, int64_t row_bytes, int64_t most)
 {
-    const int64_t pairs = batch * hk * cdiv(hq / hk, 16), tiles = cdiv(most, kAttnTile);
+    const int64_t pairs = batch * hk * cdiv(hq / hk, 16);
+    const int64_t tiles = std::min<int64_t>(cdiv(most, kAttnTile), 1 << 20);   // past the cap below, far from 64 bits
     const int64_t waves = attn_waves(row_bytes);
     const int64_t want = cdiv(cdiv(tiles * pairs, 2 * kNumCUs), waves) * waves;
     return std::min<int64_t>(std::max(want, waves) * kAttnTile, kAttnChunk);
@@ -667,9 +668,20 @@ bool attention_sizes_ok(int64_t batch, int64_t hq, int64_t hk, int64_t table_wid
            table_width * page_size <= (int64_t(1) << 40);
 }
 
-int64_t attn_workspace(int64_t batch, int64_t hq, int64_t head_dim, int64_t splits)
+struct AttnPlan {
+    int64_t chunk, splits, blocks, bytes;                    // tokens a block, blocks a row block, the grid, the workspace
+};
+
+// False for more blocks, or rows of the output, than a launch takes.
+bool attn_plan(AttnPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_dim, int64_t row_bytes, int64_t most)
 {
-    return splits > 1 ? batch * hq * splits * (head_dim + 2) * 4 : 0;
+    const int64_t limit = 0x7fffffff, pairs = batch * hk * cdiv(hq / hk, 16);
+    p.chunk = attn_chunk(batch, hq, hk, row_bytes, most);
+    p.splits = std::max<int64_t>(1, cdiv(most, p.chunk));
+    if (batch * hq > limit || pairs > limit / p.splits) return false;
+    p.blocks = pairs * p.splits;
+    p.bytes = p.splits > 1 ? batch * hq * p.splits * (head_dim + 2) * 4 : 0;
+    return true;
 }
 
 template <int DT, bool I8>
@@ -710,8 +722,11 @@ extern "C" int64_t ck_paged_attention_workspace(int64_t batch, int64_t hq, int64
         return -1;
     const int64_t most = most_visible(table_width, page_size, window, sinks);
     int64_t bytes = 0;
-    for (int esz = 1; esz <= 2; ++esz)
-        bytes = std::max(bytes, attn_workspace(batch, hq, head_dim, cdiv(most, attn_chunk(batch, hq, hk, esz * head_dim, most))));
+    for (int esz = 1; esz <= 2; ++esz) {
+        AttnPlan plan;
+        if (!attn_plan(plan, batch, hq, hk, head_dim, esz * head_dim, most)) return -1;
+        bytes = std::max(bytes, plan.bytes);
+    }
     return bytes;
 }
 
@@ -745,21 +760,19 @@ extern "C" ck_status ck_paged_attention(const ck_attention_args* args, const ck_
         return fail(CK_ERR_UNSUPPORTED, "the cache spans more than 64 GiB");
     AttnArgs a{};
     const int64_t most = most_visible(p.table_width, cache->page_size, p.window, p.sinks);
-    a.chunk = (int)attn_chunk(p.batch, p.hq, cache->heads, row_bytes, most);
-    const int64_t splits = std::max<int64_t>(1, cdiv(most, a.chunk));
-    const int64_t need = attn_workspace(p.batch, p.hq, d, splits);
-    if (need > 0 && (!p.workspace || p.workspace_bytes < need))
-        return fail(CK_ERR_INVALID_ARG, "the workspace needs %lld bytes", (long long)need);
+    AttnPlan plan;
+    if (!attn_plan(plan, p.batch, p.hq, cache->heads, d, row_bytes, most)) return fail(CK_ERR_UNSUPPORTED, "too many blocks");
+    if (plan.bytes > 0 && (!p.workspace || p.workspace_bytes < plan.bytes))
+        return fail(CK_ERR_INVALID_ARG, "the workspace needs %lld bytes", (long long)plan.bytes);
     if (!aligned(p.workspace, 256)) return fail(CK_ERR_UNSUPPORTED, "misaligned workspace");
     a.hq = (int)p.hq; a.hk = (int)cache->heads; a.group = (int)(p.hq / cache->heads);
     a.row_blocks = (int)cdiv(a.group, 16);
-    const int64_t blocks = p.batch * a.hk * a.row_blocks * splits;
-    if (blocks > 0x7fffffffLL || p.batch * p.hq > 0x7fffffffLL) return fail(CK_ERR_UNSUPPORTED, "too many blocks");
-    a.splits = (int)splits;
+    a.chunk = (int)plan.chunk;
+    a.splits = (int)plan.splits;
     if ((s = check_device()) != CK_OK) return s;
     a.q = (const uint16_t*)p.q; a.out = (uint16_t*)p.out; a.table = p.table; a.lens = p.lens;
     a.part = (float*)p.workspace;
-    a.part_ml = (float2*)(a.part + p.batch * p.hq * splits * d);
+    a.part_ml = (float2*)(a.part + p.batch * p.hq * plan.splits * d);
     a.ck = (const uint8_t*)cache->k; a.cv = (const uint8_t*)cache->v; a.cks = cache->k_scale; a.cvs = cache->v_scale;
     a.q_bs = p.q_batch_stride; a.q_hs = p.q_head_stride; a.o_bs = p.out_batch_stride; a.o_hs = p.out_head_stride;
     a.table_stride = p.table_stride;
@@ -771,8 +784,8 @@ extern "C" ck_status ck_paged_attention(const ck_attention_args* args, const ck_
     const void* fn = f16 ? (i8 ? attention_fn<CK_DT_FP16, true>(d) : attention_fn<CK_DT_FP16, false>(d))
                          : (i8 ? attention_fn<CK_DT_BF16, true>(d) : attention_fn<CK_DT_BF16, false>(d));
     void* kargs[] = {&a};
-    if ((s = launch(fn, (unsigned)blocks, 64u * attn_waves(row_bytes), kargs, stream, "paged_attention")) != CK_OK) return s;
-    if (splits > 1) {
+    if ((s = launch(fn, (unsigned)plan.blocks, 64u * attn_waves(row_bytes), kargs, stream, "paged_attention")) != CK_OK) return s;
+    if (plan.splits > 1) {
         const void* join = f16 ? attention_join_fn<CK_DT_FP16>(d) : attention_join_fn<CK_DT_BF16>(d);
         if ((s = launch(join, (unsigned)(p.batch * p.hq), 256, kargs, stream, "paged_attention_join")) != CK_OK) return s;
     }

@@ -219,6 +219,19 @@ def test_cache_of_64_gib():
         assert ck.lib().ck_paged_attention(ctypes.byref(attn_args()), ctypes.byref(cache(pages=n)), 0) == status
 
 
+@pytest.mark.parametrize("batch,hq,hk,width,page", [
+    (1 << 20, 65536, 65536, 1 << 25, 32768),     # the workspace's bytes and the blocks pass 64 bits
+    (1 << 20, 65536, 1, 1 << 25, 32768),
+    (1 << 16, 1024, 1024, 1 << 12, 1024),        # 2^38 blocks
+    (1 << 20, 4096, 1, 1, 16),                   # 2^32 rows of the output
+])
+def test_attention_refuses_what_no_launch_holds(batch, hq, hk, width, page):
+    assert ck.ck_paged_attention_workspace(batch, hq, hk, 128, width, page, 0, 0) == -1
+    a = attn_args(batch=batch, hq=hq, table_width=width, table_stride=width, workspace=0, workspace_bytes=0)
+    c = cache(heads=hk, page_size=page, head_stride=128, token_stride=128, page_stride=128)
+    assert ck.lib().ck_paged_attention(ctypes.byref(a), ctypes.byref(c), 0) == UNS
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(), HIP),
     (dict(n=0, codes=0, w=0), OK),
