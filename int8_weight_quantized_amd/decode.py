@@ -62,14 +62,26 @@ def _need_heads(t, dtype, name, tokens, heads, d, device):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, d)}")
 
 
-class KVCache:
+class _Fixed:
+    """An object that holds tensors and their addresses, made once: its
+    attributes do not change, and copies are made from copies of the tensors."""
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a {type(self).__name__} does not change: make another")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+
+class KVCache(_Fixed):
     """A paged key/value cache of one layer.
 
     k, v: [pages, heads, page_size, head_dim], bfloat16, float16 or int8; any
     strides with the last dimension contiguous (the same for both), so a view
     of [pages, page_size, heads, head_dim] storage is fine.  An int8 cache has
     fp32 k_scale and v_scale [pages, heads, page_size]: a row is its codes
-    times its scale.  The tensors stay the caller's; the object holds them.
+    times its scale.  The tensors stay the caller's; the object holds them
+    and their addresses, so their storage must stay (no resize_ or set_).
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
@@ -96,15 +108,16 @@ class KVCache:
         pages, heads, page_size, d = k.shape
         if page_size < 1 or page_size & (page_size - 1) or page_size > 32768:
             raise ValueError("page_size must be a power of two up to 32768")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, d
-        self.device, self.dtype = k.device, k.dtype
         code = {torch.bfloat16: _ck.CK_DT_BF16, torch.float16: _ck.CK_DT_FP16, torch.int8: _ck.CK_DT_INT8}[k.dtype]
         ss = _strides(k_scale) if int8 else (0, 0, 0)
-        self.struct = _ck.CkKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if int8 else 0,
-                                    v_scale.data_ptr() if int8 else 0, pages, page_size, heads, d,
-                                    *_strides(k)[:3], *ss, code, 0)
-        self.address = ctypes.addressof(self.struct)
+        struct_ = _ck.CkKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if int8 else 0,
+                                v_scale.data_ptr() if int8 else 0, pages, page_size, heads, d,
+                                *_strides(k)[:3], *ss, code, 0)
+        vars(self).update(k=k, v=v, k_scale=k_scale, v_scale=v_scale, pages=pages, heads=heads, page_size=page_size,
+                          head_dim=d, device=k.device, dtype=k.dtype, struct=struct_, address=ctypes.addressof(struct_))
+
+    def __reduce__(self):
+        return type(self), (self.k, self.v, self.k_scale, self.v_scale)
 
     @classmethod
     def empty(cls, pages, heads, page_size, head_dim, dtype="bf16", device="cuda"):
@@ -312,14 +325,15 @@ def _check_attention(q, cache, table, lens, window, sinks, out, workspace):
             raise ValueError("workspace must be contiguous")
 
 
-class Int4Weight:
+class Int4Weight(_Fixed):
     """4-bit weights laid out for int4_linear (see int4_pack)."""
 
     def __init__(self, w, scales, zeros, n, k, group, dtype):
-        self.w, self.scales, self.zeros = w, scales, zeros
-        self.n, self.k, self.group, self.dtype = n, k, group, dtype
-        self.device = w.device
-        self.w_ptr, self.s_ptr, self.z_ptr = w.data_ptr(), scales.data_ptr(), 0 if zeros is None else zeros.data_ptr()
+        vars(self).update(w=w, scales=scales, zeros=zeros, n=n, k=k, group=group, dtype=dtype, device=w.device,
+                          w_ptr=w.data_ptr(), s_ptr=scales.data_ptr(), z_ptr=0 if zeros is None else zeros.data_ptr())
+
+    def __reduce__(self):
+        return type(self), (self.w, self.scales, self.zeros, self.n, self.k, self.group, self.dtype)
 
 
 def int4_pack(codes, scales, zeros=None, group: int = 128):

@@ -481,6 +481,43 @@ def test_binding_int4_pack_passes_the_codes_stride(host, monkeypatch, stride):
     assert seen[1] >= 128
 
 
+def test_weights_and_caches_are_copied_with_their_pointers(host):
+    """A copy of a weight or a cache points at its own tensors, however it was made."""
+    import copy
+    import pickle
+
+    def weight(w):
+        return [w.w_ptr, w.s_ptr, w.z_ptr], [t.data_ptr() for t in (w.w, w.scales, w.zeros)]
+
+    def cache_(c):
+        s = ctypes.cast(c.address, ctypes.POINTER(ck.CkKvCache)).contents
+        return [s.k, s.v, s.k_scale, s.v_scale], [t.data_ptr() for t in (c.k, c.v, c.k_scale, c.v_scale)]
+
+    w = ck.Int4Weight(torch.zeros(4096, dtype=torch.uint8), bf(2, 2, 16), torch.zeros((2, 2, 16), dtype=torch.uint8),
+                      32, 256, 128, torch.bfloat16)
+    c = ck.KVCache.empty(3, 2, 16, 64, "int8", "cpu")
+    for x, pointers in ((w, weight), (c, cache_)):
+        had = pointers(x)
+        assert had[0] == had[1]
+        for copied in (copy.copy(x), copy.deepcopy(x), pickle.loads(pickle.dumps(x))):
+            got = pointers(copied)
+            assert got[0] == got[1] and type(copied) is type(x)
+        assert pointers(x) == had
+        assert got[1] != had[1]
+
+
+def test_weights_and_caches_are_fixed(host):
+    """Another tensor in place of one of theirs would not be used: it is an error."""
+    w = ck.Int4Weight(torch.zeros(4096, dtype=torch.uint8), bf(2, 2, 16), None, 32, 256, 128, torch.bfloat16)
+    c = ck.KVCache.empty(3, 2, 16, 64, "bf16", "cpu")
+    for x, names in ((w, ("w", "scales", "zeros", "n", "group")), (c, ("k", "v", "k_scale", "page_size", "struct"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(x, name, getattr(x, name))
+            with pytest.raises(AttributeError):
+                delattr(x, name)
+
+
 def test_rope_table():
     t = ck.rope_table(1000, 64, 500000.0, device="cpu")
     assert t.shape == (1000, 64) and t.dtype == torch.float32
