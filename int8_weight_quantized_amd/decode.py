@@ -326,9 +326,24 @@ def _check_attention(q, cache, table, lens, window, sinks, out, workspace):
 
 
 class Int4Weight(_Fixed):
-    """4-bit weights laid out for int4_linear (see int4_pack)."""
+    """4-bit weights laid out for int4_linear, as int4_pack returns them: w
+    uint8 [ceil(n / 16) * ceil(k / 128) * 1024], scales (of `dtype`) and zeros
+    (uint8, or None) [ceil(n / 16), ceil(k / group), 16], all contiguous."""
 
     def __init__(self, w, scales, zeros, n, k, group, dtype):
+        import torch
+        if n < 0 or k < 0 or k % 8 or group not in (32, 64, 128):
+            raise ValueError("n must not be negative, k a multiple of 8, group 32, 64 or 128")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("dtype must be bfloat16 or float16")
+        tiles, chunks, groups = -(-n // 16), -(-k // 128), -(-k // group)
+        _ck._need_vector(w, torch.uint8, "w", (tiles * chunks * 1024,))
+        for name, t, tt in (("scales", scales, dtype), ("zeros", zeros, torch.uint8)):
+            if t is None and name == "zeros":
+                continue
+            _ck._need(t, tt, name, w.device)
+            if tuple(t.shape) != (tiles, groups, 16) or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {(tiles, groups, 16)} tensor")
         vars(self).update(w=w, scales=scales, zeros=zeros, n=n, k=k, group=group, dtype=dtype, device=w.device,
                           w_ptr=w.data_ptr(), s_ptr=scales.data_ptr(), z_ptr=0 if zeros is None else zeros.data_ptr())
 

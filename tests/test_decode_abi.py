@@ -518,6 +518,34 @@ def test_weights_and_caches_are_fixed(host):
                 delattr(x, name)
 
 
+def test_int4_weight_checks_its_tensors(host):
+    """A weight made of tensors that were laid out before (a checkpoint's, say) has their sizes checked:
+    the kernels read as much as n, k and group say."""
+    good = dict(w=torch.zeros(6144, dtype=torch.uint8), scales=bf(3, 4, 16), zeros=torch.zeros((3, 4, 16), dtype=torch.uint8),
+                n=33, k=232, group=64, dtype=torch.bfloat16)
+    ck.Int4Weight(**good)
+    for exc, kw in [
+        (ValueError, dict(w=torch.zeros(6143, dtype=torch.uint8))),
+        (ValueError, dict(w=torch.zeros(12288, dtype=torch.uint8)[::2])),
+        (TypeError, dict(w=torch.zeros(6144, dtype=torch.int8))),
+        (ValueError, dict(scales=bf(3, 3, 16))),
+        (ValueError, dict(scales=bf(3, 16, 4).transpose(1, 2))),
+        (TypeError, dict(scales=bf(3, 4, 16).half())),
+        (ValueError, dict(zeros=torch.zeros((2, 4, 16), dtype=torch.uint8))),
+        (TypeError, dict(zeros=bf(3, 4, 16))),
+        (ValueError, dict(n=49)),
+        (ValueError, dict(n=-1)),
+        (ValueError, dict(k=264)),
+        (ValueError, dict(k=228)),
+        (ValueError, dict(group=48)),
+        (ValueError, dict(group=32)),
+        (TypeError, dict(dtype=torch.float16)),
+        (TypeError, dict(dtype=torch.float32, scales=bf(3, 4, 16).float())),
+    ]:
+        with pytest.raises(exc):
+            ck.Int4Weight(**{**good, **kw})
+
+
 def test_rope_table():
     t = ck.rope_table(1000, 64, 500000.0, device="cpu")
     assert t.shape == (1000, 64) and t.dtype == torch.float32
