@@ -429,7 +429,8 @@ ck_status ck_mfma_ceiling(int64_t iters, int mode, int32_t* out, uint32_t seed, 
  * cache, ck_paged_attention over it, and an output projection
  * (ck_int8_layer, or ck_int4_linear with 4-bit weights).  Their many
  * arguments come in structures, which are read before the call returns.  The
- * stride of a dimension with one element is not looked at.
+ * stride of a dimension with one element is not looked at.  Rows that a call
+ * writes must lie apart (CK_ERR_INVALID_ARG otherwise).
  */
 
 /* Element type of activations (16-bit) and of a paged cache. */

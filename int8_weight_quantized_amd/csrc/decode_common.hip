@@ -42,6 +42,26 @@ bool rows16(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t hs
     return aligned(p, 16) && (tokens <= 1 || ts % 8 == 0) && (heads <= 1 || hs % 8 == 0);
 }
 
+struct Dim {
+    int64_t count, stride;
+};
+
+// Whether the rows (`row` elements) of a tensor of these dimensions lie apart,
+// in any order of the dimensions.
+bool rows_apart(int64_t row, Dim a, Dim b, Dim c = {1, 0})
+{
+    if (a.stride > b.stride) std::swap(a, b);
+    if (b.stride > c.stride) std::swap(b, c);
+    if (a.stride > b.stride) std::swap(a, b);
+    double span = (double)row;                               // of the dimensions so far
+    for (const Dim& d : {a, b, c}) {
+        if (d.count <= 1) continue;
+        if ((double)d.stride < span) return false;
+        span += (double)(d.count - 1) * (double)d.stride;
+    }
+    return true;
+}
+
 // How far a [pages, heads, page_size] tensor reaches, in elements past its
 // start (as a double: the products may pass 64 bits); negative if a stride
 // that counts is.  The stride of a dimension with one element does not.

@@ -764,6 +764,8 @@ extern "C" ck_status ck_paged_attention(const ck_attention_args* args, const ck_
     if (!attn_plan(plan, p.batch, p.hq, cache->heads, d, row_bytes, most)) return fail(CK_ERR_UNSUPPORTED, "too many blocks");
     if (plan.bytes > 0 && (!p.workspace || p.workspace_bytes < plan.bytes))
         return fail(CK_ERR_INVALID_ARG, "the workspace needs %lld bytes", (long long)plan.bytes);
+    if (!rows_apart(d, {p.batch, p.out_batch_stride}, {p.hq, p.out_head_stride}))
+        return fail(CK_ERR_INVALID_ARG, "rows of out overlap");
     if (!aligned(p.workspace, 256)) return fail(CK_ERR_UNSUPPORTED, "misaligned workspace");
     a.hq = (int)p.hq; a.hk = (int)cache->heads; a.group = (int)(p.hq / cache->heads);
     a.row_blocks = (int)cdiv(a.group, 16);

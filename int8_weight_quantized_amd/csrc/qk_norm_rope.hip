@@ -316,6 +316,12 @@ extern "C" ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* 
                       (p.k_out && !rows16(p.k_out, p.tokens, p.k_out_token_stride, p.hk, p.k_out_head_stride)))) ||
         (cache && !rows16(p.v, p.tokens, p.v_token_stride, p.hk, p.v_head_stride)))
         return fail(CK_ERR_UNSUPPORTED, "q, k, v and out rows must start 16 bytes apart");
+    if ((p.hq > 0 && !rows_apart(p.head_dim, {p.tokens, p.q_out_token_stride}, {p.hq, p.q_out_head_stride})) ||
+        (p.hk > 0 && p.k_out && !rows_apart(p.head_dim, {p.tokens, p.k_out_token_stride}, {p.hk, p.k_out_head_stride})))
+        return fail(CK_ERR_INVALID_ARG, "rows of q_out or k_out overlap");
+    if (cache && !rows_apart(p.head_dim, {cache->pages, cache->page_stride}, {cache->heads, cache->head_stride},
+                             {cache->page_size, cache->token_stride}))
+        return fail(CK_ERR_INVALID_ARG, "rows of the cache overlap");
     if (!aligned(p.cos_sin, 16) || !aligned(p.q_weight, 16) || !aligned(p.k_weight, 16) ||
         !aligned(p.positions, 8) || !aligned(p.slots, 8))
         return fail(CK_ERR_UNSUPPORTED, "misaligned positions, slots, cos_sin or weight");

@@ -232,6 +232,36 @@ def test_attention_refuses_what_no_launch_holds(batch, hq, hk, width, page):
     assert ck.lib().ck_paged_attention(ctypes.byref(a), ctypes.byref(c), 0) == UNS
 
 
+def test_rows_that_are_written_lie_apart():
+    """Outputs and caches whose rows overlap (expanded tensors) are refused where they are written;
+    heads before tokens is fine, and so is an expanded input, or a cache that is only read."""
+    no_gpu(HIP)
+    for kw, ckw, status in [
+        (dict(q_out_token_stride=128, q_out_head_stride=512), {}, HIP),
+        (dict(q_out_token_stride=0), {}, BAD),
+        (dict(q_out_head_stride=0), {}, BAD),
+        (dict(q_out_head_stride=64), {}, BAD),
+        (dict(q_out_token_stride=1016), {}, BAD),
+        (dict(tokens=1, q_out_token_stride=0), {}, HIP),
+        (dict(k_out=P, k_out_head_stride=0), {}, BAD),
+        (dict(k_out=P), {}, HIP),
+        (dict(q_token_stride=0, k_head_stride=0, v_head_stride=0), {}, HIP),
+        (dict(), dict(head_stride=0), BAD),
+        (dict(), dict(page_stride=4088), BAD),
+        (dict(), dict(head_stride=128, token_stride=256), HIP),
+    ]:
+        assert call_qk(qk_args(**kw), cache(**ckw)) == status, (kw, ckw)
+    for kw, ckw, status in [
+        (dict(out_batch_stride=0), {}, BAD),
+        (dict(out_head_stride=120), {}, BAD),
+        (dict(out_batch_stride=128, out_head_stride=384), {}, HIP),
+        (dict(batch=1, out_batch_stride=0), {}, HIP),
+        (dict(q_batch_stride=0, q_head_stride=0), {}, HIP),
+        (dict(), dict(head_stride=0), HIP),
+    ]:
+        assert ck.lib().ck_paged_attention(ctypes.byref(attn_args(**kw)), ctypes.byref(cache(**ckw)), 0) == status, (kw, ckw)
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(), HIP),
     (dict(n=0, codes=0, w=0), OK),
