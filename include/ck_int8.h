@@ -542,6 +542,7 @@ ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipS
  *                  table[b, j / page_size].
  * lens       [in]  int32 [batch], on the device; values past
  *                  table_width * page_size count as that, negative ones as 0.
+ * Queries and visible cache rows must be finite (an infinite value gives NaN).
  * The cache's k and v each span at most 64 GiB from their first to their last
  * element (CK_ERR_UNSUPPORTED otherwise).
  * A visible token whose page is outside [0, pages) is an error of its
@@ -552,7 +553,8 @@ ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* cache, hipS
  *                  time; its contents do not matter.  NULL if that is 0.
  * The work of a sequence is split over its length by a rule on the sizes
  * above (not on lens) and joined in a fixed order: results do not vary from
- * call to call.
+ * call to call.  The rule goes by table_width, so a table much wider than its
+ * sequences costs time: blocks that find nothing to do leave at about 100 a us.
  */
 typedef struct {
     const void* q;
@@ -604,7 +606,10 @@ ck_status ck_int4_pack(const uint8_t* codes, int64_t ldc, const uint16_t* scales
  * out[i, j] = round_out( sum_t x[i, t] (c[j, t] - z[j, g]) s[j, g] + bias[j] ),
  * g = t / group, on the packed weights of ck_int4_pack: W4A16, x not
  * quantised.  Codes and zero points are exact in the products; a group's sum
- * is formed in fp32 before its scale is applied, also in fp32.
+ * is formed in fp32 before its scale is applied, also in fp32, from 16 + c and
+ * 16 + z: it keeps up to 3 bits less than a sum of (c - z) x would, which only
+ * an fp32 output shows.  x must be finite and below 2^112: a row of x with an
+ * infinity gives NaN in every column (the formula: infinities too).
  *
  * x        [in]  16-bit (dtype) [m, ldx]; ldx >= k, ldx % 8 == 0, 16-B aligned.
  * w, w_scale, w_zero  from ck_int4_pack, scales of x's type.

@@ -74,8 +74,9 @@ __device__ __forceinline__ void store_int4(const Int4Args& a, int64_t row, int64
 // because 16 + c is one bit operation away from a code: the code's four bits
 // are the upper mantissa bits of 16 in bf16 and in fp16 alike.  The products
 // are exact in fp32, X comes from the same matrix cores (a product with
-// ones), and the group's sum keeps about 3 bits less than one of c - z would,
-// far below the output's rounding.
+// ones), and the group's sum keeps about 3 bits less than one of c - z would:
+// far below a 16-bit output's rounding, up to twice the error of a plain fp32
+// product in an fp32 output.
 //
 // Bound: HBM; the weights are read once, 1 KiB at a time, in the order that
 // ck_int4_pack laid them out in.  Each wave streams its part of K for NT row
@@ -89,8 +90,9 @@ __device__ __forceinline__ void store_int4(const Int4Args& a, int64_t row, int64
 // G = j % 4: with up to 4 (8) rows only one (two) of the four accumulator
 // registers are in use, and only those get the scales (MR).
 //
-// 1 x 28672 x 5376: groups of 128 17.3 us (4.6 TB/s), groups of 32 with zero
-// points 20.4 us (4.5 TB/s): HBM, and the start and end of 256 to 896 blocks.
+// 1 x 28672 x 5376: groups of 128 16.2 us (4.9 TB/s), groups of 32 with zero
+// points 20.0 us (4.6 TB/s): HBM, and the start and end of 256 to 896 blocks.
+// 16384 x 4096, groups of 64 with zeros: 1 row 9.1 us, 4 9.6, 8 10.3, 16 12.9.
 // 1 x 4096 x 4096: 4.0 us, where a launch of three blocks takes 3.1 us.
 //
 // mask and base are int4_mask and int4_base in registers of the two kinds that
@@ -291,12 +293,15 @@ __global__ __launch_bounds__(64 * KW, 2) void int4_few_kernel(Int4Args a)
 // each wave forms those of its share of the row blocks and leaves them in
 // LDS, and all waves take them off one stage later, after its barrier.
 //
-// Bound at 128 rows: the matrix cores (busy 35 % of the time), the vector unit
+// Bound at 128 rows: the matrix cores (busy 22 % of the time), the vector unit
 // (31 %: two fused multiply-adds per output and group, two operations per two
-// codes) and the LDS reads of x (49 %, 1 KiB for NT products) take turns
-// rather than overlap, with two waves a SIMD: 128 x 21504 x 5376 54 us, 548
-// TFLOP/s.  Two blocks of four waves a CU overlap better than one of eight
-// waves (64 us).  At 32 rows HBM is as near: 32 x 21504 x 5376 23 us.
+// codes) and the LDS reads of x (26 %, 1 KiB for NT products; two fifths of it
+// bank conflicts) take turns rather than overlap, with two waves a SIMD that
+// wait for a third of their time: 128 x 21504 x 5376 53 to 55 us, 550 TFLOP/s.
+// Two blocks of four waves a CU overlap better than one of eight waves (64
+// us).  At 32 rows HBM is as near: 32 x 21504 x 5376 23 us.  Rows past 128
+// repeat the unpacking of W in every block of 64: 512 rows 175 us, 8192 rows
+// 2.57 ms (740 TFLOP/s).
 template <int GS, int MB, int NT, int WN, int WK>
 struct Int4Many {
     static constexpr int waves = WN * WK;
@@ -586,9 +591,16 @@ Int4Plan int4_plan_gs(int64_t m, int64_t n, int64_t chunks)
 #define CK_INT4_MANY(MB, NT, WN, WK, ONE, TWO)                                                    \
     {{reinterpret_cast<const void*>(&int4_many_kernel<DT, GS, Z, MB, NT, WN, WK>), NT * WN, 16 * MB, \
       WN * WK}, WK, ONE, TWO}
-    // Few rows: two row tiles per wave once that leaves a block or more per
-    // CU (1 row, 28672 x 5376: 20.4 against 24.9 us with one tile, 16384 x
-    // 4096: 10.2 against 9.8 us, 4096 x 4096: 5.5 against 4.6 us).
+    // Few rows: eight waves, four from 8193 columns on, and above 20480 columns
+    // eight waves of two row tiles, by the number of blocks (16 columns a row
+    // tile).  1 row, groups of 128, eight waves / four / eight of two tiles, us:
+    //   4096 x 4096   4.4  5.6  5.2      20480 x 4096  11.0  10.4  12.5
+    //   8192 x 4096   6.0  6.7  6.6      21504 x 5376  14.9  15.1  14.1
+    //   10240 x 4096  7.4  7.4  8.2      24576 x 5376  15.4  15.4  14.7
+    //   16384 x 4096 10.1  8.9  10.1     28672 x 5376  18.0  18.4  17.6
+    // Groups of 32 follow them, but for equal times of the last two columns at
+    // 28672.  k does not enter: with 1024 columns two tiles are up to 8 % slower
+    // there than four waves would be (28672: 6.6 against 6.1).
     const bool wide = n > 20480;
     if (m <= 4) return wide ? CK_INT4_FEW(1, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(1, 1, 1, 4) : CK_INT4_FEW(1, 1, 1, 8);
     if (m <= 8) return wide ? CK_INT4_FEW(2, 1, 2, 8) : n > 8192 ? CK_INT4_FEW(2, 1, 1, 4) : CK_INT4_FEW(2, 1, 1, 8);

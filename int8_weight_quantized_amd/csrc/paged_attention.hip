@@ -12,11 +12,11 @@
 // one multiply-add per query head of the group, far below the matrix cores'
 // rate.  Eight sequences of 32768 tokens, 8 key heads, both launches: bf16
 // heads of 128 194 us (5.5 TB/s; heads of 64 5.3, of 192 5.1, of 256 5.7),
-// int8 heads of 128 110 us (5.0; of 256 4.9).  48 sequences of up to 9001
-// tokens, 100000 in all, int8: 54 us (3.9 TB/s): the blocks that find nothing
-// to do leave at about 100 a us, and the last ones run alone.  A short
+// int8 heads of 128 111 us (5.0; of 256 4.9).  48 sequences of up to 9001
+// tokens, 100000 in all, int8: 53 to 55 us (3.9 TB/s): the blocks that find
+// nothing to do leave at about 100 a us, and the last ones run alone.  A short
 // sequence is bound by latency, the chain lens -> table -> K -> V and the
-// join: one of 1000 tokens 6.7 us.
+// join: one of 1000 tokens 6.6 us.
 //
 // A block takes one sequence, one key head (up to 16 of its query heads,
 // one matrix tile) and a chunk of the visible tokens.  Its threads first
@@ -648,11 +648,19 @@ int attn_waves(int64_t row_bytes)
 // Tokens per block: as many as give every CU two blocks, if all sequences
 // were as long as they can be, but a tile per wave at least and kAttnChunk
 // at most: short sequences are spread over the chip, and long ones in parts
-// small enough to even out sequences of different lengths (a part's sums,
-// (d + 2) * 4 bytes a head, written and read, are under 2 % of the traffic of
-// its rows for groups of up to 8 heads).  Measured, 4 sequences of 131072
-// bf16 tokens / 48 of up to 9001 int8 ones: 512 a block 420 us / 54 us, 768
-// - / 67, 1024 394 / 54, 2048 380 / 61.
+// small enough to even out sequences of different lengths.  A part's sums,
+// (d + 2) * 4 bytes a head, are written and read: for a group of 8 heads of 128
+// 1.6 % of the traffic of its rows with 1024 bf16 tokens, 3.1 % with int8 ones,
+// and more in smaller chunks (1 x 1000 bf16 tokens in groups of 4, 128 a
+// block: 6.3 %; one sequence of 4096 with 16 / 2 heads of 256, 64 a block: 25 %),
+// which are taken where the chip would stand idle otherwise.  Measured, 4
+// sequences of 131072 bf16 tokens / 48 of up to 9001 int8 ones: 512 a block 420
+// us / 54 us, 768 - / 67, 1024 394 / 54, 2048 380 / 61.
+//
+// The rule goes by what a row of the table can name, not by the lengths, which
+// the host does not know: a table wider than its sequences costs empty blocks
+// and smaller shares (one of 1000 tokens in a table for 131072 17 us, 64 of
+// them 579 us in place of 48).
 int64_t attn_chunk(int64_t batch, int64_t hq, int64_t hk, int64_t row_bytes, int64_t most)
 {
     const int64_t pairs = batch * hk * cdiv(hq / hk, 16);

@@ -8,11 +8,13 @@
 // Squares, sums, the rotation and the int8 row's amax are fp32.
 //
 // Bound: HBM (each value is read and written once: 2 + 2 bytes, or 2 + 1):
-// 8192 tokens of 32 / 8 / 8 heads of 128, 201 MB, 49.5 us or 4.1 TB/s.  515
-// tokens into an int8 cache take 7.7 us; a decode call of one token is a
-// launch, 3.1 us.  One group of L lanes (a power of
-// two, 8 values a lane) holds a head, so the norm is a reduction over the
-// group and nothing passes through LDS.  With halves rotated, a lane has four
+// 8192 tokens of 32 / 8 / 8 heads of 128, 201 MB, 48.2 us or 4.2 TB/s.  Into an
+// int8 cache they take 65 us (2.9 TB/s): normed heads, queries too, pay for the
+// ordered sum and the 64-bit root and division below, and with rotated halves
+// for a second load of the row.  515 tokens of 24 / 8 / 8 heads of 96 take 5.2
+// us, into an int8 cache 7.0; a decode call of one token is a launch, 3.2 us.
+// One group of L lanes (a power of two, 8 values a lane) holds a head, so the
+// norm is a reduction over the group and nothing passes through LDS.  With halves rotated, a lane has four
 // elements of the first half and their four partners of the second, so the
 // rotation stays inside the lane.  A group takes several heads of one token,
 // HB at a time: the angles and weights are read once for all of them, and HB
@@ -55,10 +57,12 @@ __device__ __forceinline__ float group_sum(float v)
 // The sum of a row's d terms, eight a lane, in one particular order.  Below
 // 128 terms: those 64 apart, then neighbours, pairs of neighbours and so on.
 // From 128 on: those 128 (256 from d = 256 on) apart, then each four in
-// sequence, then neighbouring fours and so on.  It is the order in which
-// torch sums such rows on this device; with the root rounded from 64 bits, as
-// torch's is, the key codes of an int8 cache, which jump where a value lies
-// between two of them, are those of the same formula in torch operations.
+// sequence, then neighbouring fours and so on.  Any order is as right; this is
+// the one in which the torch this was compared with (2.10) sums such rows on
+// this device.  With the root rounded from 64 bits, as torch's is, the key
+// codes of an int8 cache, which jump where a value lies between two of them,
+// are then those of the same formula in torch operations (tested at widths of
+// 64, 96, 128, 192 and 256; another torch may sum in another order).
 template <int L>
 __device__ __forceinline__ float group_sum_ordered(const float (&x)[8], int d)
 {
