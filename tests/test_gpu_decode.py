@@ -444,6 +444,18 @@ def test_attention_cache_without_pages(cache, width):
     assert out[0].isnan().all() and out[2].isnan().all() and (out[1] == 0).all()
 
 
+@pytest.mark.parametrize("d", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("fp16", "fp16"), ("int8", "bf16"), ("int8", "fp16")])
+def test_attention_every_head_dim(d, cache, dtype):
+    """Each head_dim with each type of cache: a sequence of several chunks, one of a few tiles, one token."""
+    lens = [3000, 70, 1]
+    pages = sum(-(-n // 16) for n in lens)
+    c = make_cache(pages, 2, 16, d, cache, dtype)
+    table, n = tables(lens, 16, pages)
+    poison(c, table, n)
+    check_attention(rand(3, 10, d, dtype=DT[dtype], scale=2.0).to(cuda_device()), c, table, n)
+
+
 def test_attention_bad_pages():
     """A visible page outside the cache makes that sequence NaN, and no other."""
     lens = [100, 100, 100, 100]
