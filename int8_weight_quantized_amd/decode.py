@@ -42,6 +42,17 @@ def _stream(index):
     return _torch._C._cuda_getCurrentRawStream(index)
 
 
+def _launch(call, index, *args):
+    """call(*args, stream) on CUDA device `index` and its current stream (every
+    device's default stream is the null stream, which launches on the current
+    device).  Host tensors, of no index, have no device to change to."""
+    if index is None or index == _torch._C._cuda_getDevice():
+        call(*args, _stream(index))
+    else:
+        with _torch.cuda.device(index):
+            call(*args, _stream(index))
+
+
 def _dtype16(t, name):
     """CK_DT_* of a 16-bit floating tensor."""
     torch = _torch or _load_torch()
@@ -203,7 +214,7 @@ def qk_norm_rope(q, k, v, positions, cos_sin, q_weight=None, k_weight=None, eps:
     args = _QK.pack(q.data_ptr(), kp, vp, pp, tp, qw, kw, q_out.data_ptr(), kop, sp, qs[0], qs[1], ks[0], ks[1],
                     vs[0], vs[1], os[0], os[1], kos[0], kos[1], tokens, hq, hk, d, rot, rows, eps, _code16[tt],
                     1 if interleaved else 0, 0)
-    _ck.ck_qk_norm_rope(args, None if cache is None else cache.address, _stream(dev.index))
+    _launch(_ck.ck_qk_norm_rope, dev.index, args, None if cache is None else cache.address)
     return q_out, k_out
 
 
@@ -297,7 +308,7 @@ def paged_attention(q, cache, table, lens, scale=None, window: int = 0, sinks: i
     args = _ATTENTION.pack(q.data_ptr(), out.data_ptr(), table.data_ptr(), lens.data_ptr(), wp, wn, qs[0], qs[1],
                            os[0], os[1], ts[0], batch, hq, width, window, sinks,
                            d ** -0.5 if scale is None else scale, _code16[tt])
-    _ck.ck_paged_attention(args, cache.address, _stream(dev.index))
+    _launch(_ck.ck_paged_attention, dev.index, args, cache.address)
     return out
 
 
@@ -382,9 +393,9 @@ def int4_pack(codes, scales, zeros=None, group: int = 128):
     z = None if zeros is None else torch.empty((tiles, groups, 16), dtype=torch.uint8, device=dev)
     ldc, lds, ldz = (t.stride(0) if t is not None and n > 1 else row
                      for t, row in ((codes, k // 2), (scales, groups), (zeros, groups)))
-    _ck.ck_int4_pack(codes.data_ptr(), ldc, scales.data_ptr(), lds,
-                     0 if z is None else zeros.data_ptr(), ldz, w.data_ptr(), s.data_ptr(),
-                     0 if z is None else z.data_ptr(), n, k, group, _ck._stream(codes))
+    _launch(_ck.ck_int4_pack, dev.index, codes.data_ptr(), ldc, scales.data_ptr(), lds,
+            0 if z is None else zeros.data_ptr(), ldz, w.data_ptr(), s.data_ptr(),
+            0 if z is None else z.data_ptr(), n, k, group)
     return Int4Weight(w, s, z, n, k, group, scales.dtype)
 
 
@@ -411,7 +422,7 @@ def int4_linear(x, weight, bias=None, out=None, out_dtype=None):
         out = x.new_empty((m, n), dtype=odt)
     args = _INT4.pack(x.data_ptr(), weight.w_ptr, weight.s_ptr, weight.z_ptr, 0 if bias is None else bias.data_ptr(),
                       out.data_ptr(), xs[0], out.stride(0), m, n, k, weight.group, _code16[tt], code)
-    _ck.ck_int4_linear(args, _stream(dev.index))
+    _launch(_ck.ck_int4_linear, dev.index, args)
     return out
 
 

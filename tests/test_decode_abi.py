@@ -576,6 +576,39 @@ def test_int4_weight_checks_its_tensors(host):
             ck.Int4Weight(**{**good, **kw})
 
 
+def test_launches_go_to_the_tensors_device(host, monkeypatch):
+    """The default stream of every device is the null stream, which launches on the current device:
+    a call on another device's tensors makes that one current for its time."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.index
+
+        def __exit__(self, *a):
+            current[0] = self.was
+
+    ck.decode._load_torch()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ck.decode, "_stream", lambda index: 100 + index)
+    for index in (0, 3):
+        ck.decode._launch(lambda *a: seen.append((current[0], a)), index, "args", None)
+        assert current[0] == 0
+    assert seen == [(0, ("args", None, 100)), (3, ("args", None, 103))]
+    calls = []
+    monkeypatch.setattr(ck.decode, "_launch", lambda f, index, *a: calls.append(index))
+    c = ck.KVCache.empty(9, 2, 16, 128, "bf16", "cpu")
+    ck.qk_norm_rope(bf(4, 8, 128), bf(4, 2, 128), None, None, None)
+    ck.paged_attention(bf(3, 8, 128), c, torch.zeros((3, 4), dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+    w = ck.int4_pack(torch.zeros((32, 128), dtype=torch.uint8), bf(32, 2))
+    ck.int4_linear(bf(3, 256), w)
+    assert len(calls) == 4
+
+
 def test_rope_table():
     t = ck.rope_table(1000, 64, 500000.0, device="cpu")
     assert t.shape == (1000, 64) and t.dtype == torch.float32
