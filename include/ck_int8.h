@@ -499,7 +499,7 @@ typedef struct {
  * head_dim     a multiple of 8 up to 512; rot a multiple of 16 up to
  *              head_dim, or 0 (no rotation; positions and cos_sin unused).
  * Every row must start 16 bytes apart (CK_ERR_UNSUPPORTED otherwise).
- * Inputs must be finite.
+ * Inputs must be finite, and a normed head's sum of squares in fp32's range.
  */
 typedef struct {
     const void* q;
