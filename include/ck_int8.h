@@ -631,6 +631,151 @@ typedef struct {
 
 ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
 
+/*
+ * Operators of a server's batch: what a step of many requests at once needs
+ * beside the operators above.  The conventions are those of the decode-step
+ * operators.
+ */
+
+/*
+ * Attention of one new token per sequence over a paged cache, where groups of
+ * sequences begin with the same tokens (a prefix), whose keys and values stand
+ * in the cache once and are read once for the group:
+ *   out[b, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b, h] . k_j - m),
+ * m the largest score, over the tokens j of sequence b: those of its prefix,
+ * if it has one, then its own.  Scores, exponentials and sums are fp32, the
+ * products on the matrix cores with p_j in 16-bit parts (ck_paged_attention).
+ * A sequence without any token gives zeros.
+ *
+ * q, cache, out     as in ck_paged_attention.
+ * prefix_table [in] int32 [prefixes, prefix_width], rows prefix_table_stride
+ *                   apart: token j of prefix p is token j % page_size of page
+ *                   prefix_table[p, j / page_size].
+ * prefix_lens  [in] int32 [prefixes]: the tokens of each, any number.
+ * starts       [in] int32 [prefixes + 1]: the sequences starts[p] to
+ *                   starts[p + 1] - 1 begin with prefix p; those before the
+ *                   first and from the last entry on have none.  The entries
+ *                   must not decrease and lie in 0 .. batch: where they do
+ *                   not, every output is NaN.
+ * table, lens  [in] int32 [batch, table_width] and [batch]: the pages and the
+ *                   number of each sequence's own tokens, those after the
+ *                   prefix, the new one included.
+ * Lengths past what a table's row can name count as that, negative ones as 0.
+ * A page outside [0, pages) is an error of the sequences that see it: their
+ * outputs are NaN.  Queries and visible rows must be finite, the cache's k and
+ * v span at most 64 GiB each, and rows that are not visible are never used.
+ * workspace  [tmp] as in ck_paged_attention, of
+ *                  ck_shared_prefix_attention_workspace bytes.
+ * prefixes == 0 is ck_paged_attention without a window (the prefix pointers
+ * may be NULL).
+ */
+typedef struct {
+    const void* q;
+    void* out;
+    const int32_t* prefix_table;
+    const int32_t* prefix_lens;
+    const int32_t* starts;
+    const int32_t* table;
+    const int32_t* lens;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t q_batch_stride, q_head_stride, out_batch_stride, out_head_stride, prefix_table_stride, table_stride;
+    int64_t batch, hq, prefixes, prefix_width, table_width;
+    float scale;
+    int32_t dtype;          /* of q and out */
+} ck_prefix_args;
+
+ck_status ck_shared_prefix_attention(const ck_prefix_args* args, const ck_kv_cache* cache,
+                                     hipStream_t stream);
+
+/* Bytes of workspace that ck_shared_prefix_attention needs for these sizes
+ * (host only); -1 for sizes that it refuses. */
+int64_t ck_shared_prefix_attention_workspace(int64_t batch, int64_t hq, int64_t hk, int64_t head_dim,
+                                             int64_t prefixes, int64_t prefix_width,
+                                             int64_t table_width, int64_t page_size);
+
+/*
+ * Low-rank adapters beside a projection that all rows share:
+ *   out[i, j] = round_out( y[i, j] + scale[t] sum_r v[r] b[t, j, r] ),
+ *   v[r] = sum_c x[i, c] a[t, r, c],  t = ids[i];
+ * out[i] = y[i], bit for bit, for an id outside [0, adapters) (-1, say).
+ * v and all sums are fp32 (v enters the product in 16-bit parts that hold it
+ * to 2^-22 of itself (fp16) or better; see below for fp16's range).
+ *
+ * x        [in]  16-bit (dtype) [m, ldx]; ldx >= k, ldx % 8 == 0, 16-B aligned.
+ * a        [in]  16-bit (dtype) [adapters][rank][k], adapters a_stride apart.
+ * b        [in]  16-bit (dtype) [adapters][n][rank], adapters b_stride apart.
+ *                Strides are multiples of 8, a and b 16-B aligned.
+ * scale    [in]  fp32 [adapters], or NULL for 1.
+ * ids      [in]  int32 [m], in any order; rows of one adapter that stand
+ *                together are cheaper.
+ * y        [in]  [m, ldy] of out_dtype.
+ * out      [out] [m, ldo] of out_dtype; may be y itself (same ld), and must
+ *                not overlap it or x otherwise.
+ * rank a multiple of 8 from 8 to 256 (adapters of smaller rank: zeros), k a
+ * multiple of 8.  m == 0 or n == 0 is a no-op.
+ * workspace  [tmp] device memory of ck_lora_add_workspace bytes, 256-B
+ *                  aligned, used by one call at a time.  NULL if that is 0.
+ */
+typedef struct {
+    const void* x;
+    const void* a;
+    const void* b;
+    const float* scale;
+    const int32_t* ids;
+    const void* y;
+    void* out;
+    void* workspace;
+    int64_t workspace_bytes, ldx, ldy, ldo, a_stride, b_stride, m, n, k, rank, adapters;
+    int32_t dtype;          /* of x, a and b: CK_DT_BF16 or CK_DT_FP16 */
+    int32_t out_dtype;      /* ck_out_dtype, of y and out */
+} ck_lora_args;
+
+ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream);
+
+/* Bytes of workspace that ck_lora_add needs for these sizes (host only); -1
+ * for sizes that it refuses. */
+int64_t ck_lora_add_workspace(int64_t m, int64_t n, int64_t k, int64_t rank);
+
+/*
+ * Log probabilities of given tokens, with the entropy and the most likely
+ * alternatives of each row of logits x (natural logarithms):
+ *   L = log sum_j exp(x[j]),  logprob = x[token] - L,
+ *   entropy = -sum_j p_j log p_j,  p_j = exp(x[j] - L)  (0 for p_j = 0),
+ *   top: the `top` largest x[j] in descending order, of equal ones the lowest
+ *   index first (+0 and -0 are equal, NaN is larger than all), and x[j] - L.
+ * Logits of -inf (masked) have probability 0.  A row of nothing else, with
+ * +inf or with NaN gives NaN for all but the indices.
+ *
+ * logits   [in]  dtype [rows, ld], ld >= vocab; rows may start anywhere.
+ * tokens   [in]  int64 [rows]; one outside [0, vocab) gives NaN.  May be NULL
+ *                together with logprob.
+ * logprob, entropy  [out] fp32 [rows]; entropy may be NULL.
+ * top_ids, top_logprobs  [out] int64 and fp32 [rows, top], contiguous; NULL
+ *                allowed for top == 0.
+ * top from 0 to 64 (and vocab), vocab from 1 to 2^31 - 1.
+ * workspace  [tmp] device memory of ck_token_logprobs_workspace bytes, 256-B
+ *                  aligned, used by one call at a time.  NULL if that is 0.
+ */
+typedef struct {
+    const void* logits;
+    const int64_t* tokens;
+    float* logprob;
+    float* entropy;
+    int64_t* top_ids;
+    float* top_logprobs;
+    void* workspace;
+    int64_t workspace_bytes, ld, rows, vocab, top;
+    int32_t dtype;          /* ck_out_dtype, of the logits */
+    int32_t reserved;       /* 0 */
+} ck_logprob_args;
+
+ck_status ck_token_logprobs(const ck_logprob_args* args, hipStream_t stream);
+
+/* Bytes of workspace that ck_token_logprobs needs for these sizes (host
+ * only); -1 for sizes that it refuses. */
+int64_t ck_token_logprobs_workspace(int64_t rows, int64_t vocab, int64_t top);
+
 /* Name of a status code (static string). */
 const char* ck_status_string(ck_status s);
 
@@ -640,7 +785,7 @@ const char* ck_last_error(void);
 /* ABI version of this header: bumped when a signature changes. */
 int ck_abi_version(void);
 
-#define CK_ABI_VERSION 12
+#define CK_ABI_VERSION 13
 
 #ifdef __cplusplus
 }

@@ -31,7 +31,7 @@ CK_OUT_FP32 = 2
 
 CK_MAX_K = 132104
 CK_NUM_TILES = 14
-CK_ABI_VERSION = 12
+CK_ABI_VERSION = 13
 
 CK_DT_BF16 = 0
 CK_DT_FP16 = 1
@@ -44,6 +44,8 @@ EXPORTED = (
     "ck_int8_table_set", "ck_int8_table_clear", "ck_int8_table_size",
     "ck_int8_set_forced_tile", "ck_int8_forced_tile", "ck_int8_set_path_log",
     "ck_qk_norm_rope", "ck_paged_attention", "ck_paged_attention_workspace", "ck_int4_pack", "ck_int4_linear",
+    "ck_shared_prefix_attention", "ck_shared_prefix_attention_workspace", "ck_lora_add", "ck_lora_add_workspace",
+    "ck_token_logprobs", "ck_token_logprobs_workspace",
 )
 
 
@@ -83,6 +85,29 @@ class CkAttentionArgs(ctypes.Structure):
                                         "out_head_stride table_stride batch hq table_width window sinks"),
                        (ctypes.c_float, "scale"),
                        (ctypes.c_int32, "dtype"))
+
+
+class CkPrefixArgs(ctypes.Structure):
+    """ck_prefix_args of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "q out prefix_table prefix_lens starts table lens workspace"),
+                       (ctypes.c_int64, "workspace_bytes q_batch_stride q_head_stride out_batch_stride out_head_stride "
+                                        "prefix_table_stride table_stride batch hq prefixes prefix_width table_width"),
+                       (ctypes.c_float, "scale"),
+                       (ctypes.c_int32, "dtype"))
+
+
+class CkLoraArgs(ctypes.Structure):
+    """ck_lora_args of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "x a b scale ids y out workspace"),
+                       (ctypes.c_int64, "workspace_bytes ldx ldy ldo a_stride b_stride m n k rank adapters"),
+                       (ctypes.c_int32, "dtype out_dtype"))
+
+
+class CkLogprobArgs(ctypes.Structure):
+    """ck_logprob_args of include/ck_int8.h."""
+    _fields_ = _fields((ctypes.c_void_p, "logits tokens logprob entropy top_ids top_logprobs workspace"),
+                       (ctypes.c_int64, "workspace_bytes ld rows vocab top"),
+                       (ctypes.c_int32, "dtype reserved"))
 
 
 class CKError(RuntimeError):
@@ -156,6 +181,18 @@ def lib():
     L.ck_int4_pack.restype = ci
     L.ck_int4_linear.argtypes = [p, p]
     L.ck_int4_linear.restype = ci
+    L.ck_shared_prefix_attention.argtypes = [p, p, p]
+    L.ck_shared_prefix_attention.restype = ci
+    L.ck_shared_prefix_attention_workspace.argtypes = [i64] * 8
+    L.ck_shared_prefix_attention_workspace.restype = i64
+    L.ck_lora_add.argtypes = [p, p]
+    L.ck_lora_add.restype = ci
+    L.ck_lora_add_workspace.argtypes = [i64] * 4
+    L.ck_lora_add_workspace.restype = i64
+    L.ck_token_logprobs.argtypes = [p, p]
+    L.ck_token_logprobs.restype = ci
+    L.ck_token_logprobs_workspace.argtypes = [i64] * 3
+    L.ck_token_logprobs_workspace.restype = i64
     L.ck_status_string.argtypes = [ci]
     L.ck_status_string.restype = ctypes.c_char_p
     L.ck_last_error.argtypes = []
@@ -229,7 +266,7 @@ def ck_int8_gemm_i32(q, ldq, w, ldw, acc, ldacc, m, n, k, tile=-1, stream=0):
            "ck_int8_gemm_i32")
 
 
-# The structures of the next three (ck_*_args and ck_kv_cache) come as ctypes
+# The structures of the calls below (ck_*_args and ck_kv_cache) come as ctypes
 # structures by reference or as the bytes of one; a cache also as its address.
 
 def ck_qk_norm_rope(args, cache=None, stream=0):
@@ -250,8 +287,39 @@ def ck_int4_linear(args, stream=0):
         _check(s, "ck_int4_linear")
 
 
+def ck_shared_prefix_attention(args, cache, stream=0):
+    s = (_lib or lib()).ck_shared_prefix_attention(args, cache, stream)
+    if s:
+        _check(s, "ck_shared_prefix_attention")
+
+
+def ck_lora_add(args, stream=0):
+    s = (_lib or lib()).ck_lora_add(args, stream)
+    if s:
+        _check(s, "ck_lora_add")
+
+
+def ck_token_logprobs(args, stream=0):
+    s = (_lib or lib()).ck_token_logprobs(args, stream)
+    if s:
+        _check(s, "ck_token_logprobs")
+
+
 def ck_paged_attention_workspace(batch, hq, hk, head_dim, table_width, page_size, window=0, sinks=0) -> int:
     return int(lib().ck_paged_attention_workspace(batch, hq, hk, head_dim, table_width, page_size, window, sinks))
+
+
+def ck_shared_prefix_attention_workspace(batch, hq, hk, head_dim, prefixes, prefix_width, table_width, page_size) -> int:
+    return int(lib().ck_shared_prefix_attention_workspace(batch, hq, hk, head_dim, prefixes, prefix_width, table_width,
+                                                          page_size))
+
+
+def ck_lora_add_workspace(m, n, k, rank) -> int:
+    return int(lib().ck_lora_add_workspace(m, n, k, rank))
+
+
+def ck_token_logprobs_workspace(rows, vocab, top) -> int:
+    return int(lib().ck_token_logprobs_workspace(rows, vocab, top))
 
 
 def ck_int4_pack(codes, ldc, scales, lds, zeros, ldz, w, w_scale, w_zero, n, k, group, stream=0):
@@ -584,3 +652,9 @@ def int8_gemm_i32(q, w, tile: int = -1, out=None):
 
 from .decode import (Int4Weight, KVCache, int4_linear, int4_pack, paged_attention,  # noqa: E402
                      paged_attention_workspace, qk_norm_rope, rope_table)
+
+# ------------------------------------------------ operators of a server's batch
+
+from .serving import (LoraWeight, TokenLogprobs, lora_add, lora_add_workspace,  # noqa: E402
+                      shared_prefix_attention, shared_prefix_attention_workspace, token_logprobs,
+                      token_logprobs_workspace)
