@@ -187,6 +187,151 @@ __device__ __forceinline__ uint2 read_tr8(const uint8_t* p)
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(p)));
 }
 
+// The types of the products and how a weight enters the second one: PARTS
+// parts of 16 bits, in NA sums.  The parts of fp16 are kept 2^6 higher, at most
+// 2^14, and those of the second sum hold `fine` times what the first ones left,
+// at most 2^14 too.
+template <int DT, bool I8, int PARTS>
+struct AttnKind {
+    static constexpr int KT = I8 ? CK_DT_FP16 : DT;
+    static constexpr int VT = I8 ? CK_DT_BF16 : DT;
+    static constexpr int NA = VT == CK_DT_FP16 ? 2 : 1;
+    static constexpr int each = PARTS / NA;                  // parts of a sum
+    static constexpr float lift = VT == CK_DT_FP16 ? 6.0f : 0.0f;
+    static constexpr float fine = each == 2 ? 8388608.0f : 2048.0f;
+};
+
+// One tile of 32 tokens for MB blocks of 16 rows of queries: kr and vr are its
+// K and V rows in LDS, kscale and vscale (int8) the tokens' scales there, and
+// `limit` the number of its tokens that count.  M, L and acc are the rows'
+// running reference, sums of weights and weighted values; `empty`: the sums
+// are still zero.  k_read(), v_ready() and v_read() are called when K has been
+// read, before V is read and after.
+template <int DT, bool I8, int D, int MB, int PARTS, class KRead, class VReady, class VRead>
+__device__ __forceinline__ void attn_tile(const uint8_t* kr, const uint8_t* vr, const v4i (&qf)[MB][D / 32],
+                                          const float (&sc)[MB], const float* kscale, const float* vscale, int ve,
+                                          int limit, bool empty, float (&M)[MB], float (&L)[MB],
+                                          f32x4v (&acc)[MB][AttnKind<DT, I8, PARTS>::NA][D / 16], KRead k_read,
+                                          VReady v_ready, VRead v_read)
+{
+    constexpr int RB = D * (I8 ? 1 : 2), KK = D / 32, DB = D / 16;
+    using Sh = AttnShape<RB>;
+    using Kind = AttnKind<DT, I8, PARTS>;
+    constexpr int KT = Kind::KT, VT = Kind::VT, NA = Kind::NA;
+    const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
+    f32x4v s[MB][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int b = 0; b < MB; ++b) s[b][u] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+        const int row = 16 * u + i16;
+        const uint8_t* const at = kr + row * RB;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            v4i kf;
+            if constexpr (I8) {
+                const int piece = 4 * kk + G;
+                kf = codes8_f16(*reinterpret_cast<const uint2*>(at + (((piece >> 1) ^ Sh::swz(row)) << 4) + (piece & 1) * 8));
+            } else {
+                kf = *reinterpret_cast<const v4i*>(at + (((4 * kk + G) ^ Sh::swz(row)) << 4));
+            }
+#pragma unroll
+            for (int b = 0; b < MB; ++b) s[b][u] = mfma16<KT>(kf, qf[b][kk], s[b][u]);
+        }
+    }
+    k_read();
+    v4i part[MB][PARTS];                                     // the weights are their sum
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = s[b][e >> 2][e & 3] * sc[b];
+        if constexpr (I8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float4 ks = *reinterpret_cast<const float4*>(&kscale[4 * G + 16 * u]);
+                p[4 * u] *= ks.x; p[4 * u + 1] *= ks.y; p[4 * u + 2] *= ks.z; p[4 * u + 3] *= ks.w;
+            }
+        }
+        if (limit < kAttnTile) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (4 * G + 16 * (e >> 2) + (e & 3) >= limit) p[e] = -INFINITY;
+        }
+        float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+        if (__any(top > M[b] + kAttnSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m = fmaxf(M[b], top);
+            const float f = __builtin_amdgcn_exp2f(M[b] - m);
+            M[b] = m;
+            L[b] *= f;
+            if (!empty) {
+#pragma unroll
+                for (int i = 0; i < NA; ++i)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) acc[b][i][d] = acc[b][i][d] * f;
+            }
+        }
+        const float ref = M[b] - Kind::lift;
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(p[e] - ref);
+            sum += p[e];
+        }
+        L[b] += sum;
+        if constexpr (I8) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float4 vs = *reinterpret_cast<const float4*>(&vscale[4 * G + 16 * u]);
+                const float v[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[4 * u + r] *= __builtin_amdgcn_ldexpf(v[r], -ve);
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float x = p[2 * w], y = p[2 * w + 1];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                const uint32_t h = narrow2<VT>(x, y);
+                const float2 back = widen2<VT>(h);
+                part[b][i][w] = (int)h;
+                x -= back.x;
+                y -= back.y;
+                if (NA == 2 && i == Kind::each - 1) {
+                    x *= Kind::fine;
+                    y *= Kind::fine;
+                }
+            }
+        }
+    }
+    v_ready();
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+        v4i vf;
+        if constexpr (I8) {
+            // row r of the eight: token 4 G + r of the first tile or 4 G + r - 4 of the second
+            const int r = i16 >> 1, row = 4 * G + (r & 3) + 16 * (r >> 2);
+            vf = codes8_bf16(read_tr8(vr + row * RB + ((d ^ Sh::swz(row)) << 4) + (i16 & 1) * 8));
+        } else {
+            const int row = 4 * G + (i16 >> 2), c = 2 * d + ((i16 >> 1) & 1);
+            const uint2 x = read_tr16(vr + row * RB + ((c ^ Sh::swz2(row)) << 4) + (i16 & 1) * 8);
+            const uint2 y = read_tr16(vr + (row + 16) * RB + ((c ^ Sh::swz2(row + 16)) << 4) + (i16 & 1) * 8);
+            vf = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                f32x4v& sum = acc[b][i / Kind::each < NA ? i / Kind::each : NA - 1][d];
+                sum = mfma16<VT>(vf, part[b][i], sum);
+            }
+    }
+    v_read();
+}
+
 // DT: type of q and out, and of a 16-bit cache; I8: int8 cache.
 template <int DT, bool I8, int D>
 __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void paged_attention_kernel(AttnArgs a)
@@ -194,14 +339,8 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     constexpr int RB = D * (I8 ? 1 : 2);
     using Sh = AttnShape<RB>;
     constexpr int NW = Sh::waves, NL = Sh::loads, KK = D / 32, DB = D / 16;
-    constexpr int KT = I8 ? CK_DT_FP16 : DT;                 // the products' types
-    constexpr int VT = I8 ? CK_DT_BF16 : DT;
-    constexpr int WP = VT == CK_DT_FP16 ? 4 : 3;             // 16-bit parts of a weight
-    // fp16 weights are kept 2^6 higher, at most 2^14; the last two parts hold
-    // 2^23 times what the first two left, at most 2^14 too, in sums of their own
-    constexpr int NA = VT == CK_DT_FP16 ? 2 : 1;
-    constexpr float kLift = VT == CK_DT_FP16 ? 6.0f : 0.0f;
-    constexpr float kFine = 8388608.0f;
+    constexpr int WP = I8 || DT != CK_DT_FP16 ? 3 : 4;       // 16-bit parts of a weight
+    constexpr int NA = AttnKind<DT, I8, WP>::NA;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[NW * 2 * Sh::tile];
     __shared__ __attribute__((aligned(16))) uint32_t offs[kAttnChunk];
     __shared__ __attribute__((aligned(16))) float kscale[I8 ? kAttnChunk : 4], vscale[I8 ? kAttnChunk : 4];
@@ -232,10 +371,10 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     const int tiles = (n + kAttnTile - 1) / kAttnTile;
 
     // Queries: lane 16 G + i holds elements 32 kk + 8 G + 0 .. 7 of head i.
-    v4i qf[KK];
+    v4i qf[1][KK];
     const uint16_t* qp = a.q + b * a.q_bs + (h0 + min(i16, heads - 1)) * a.q_hs + 8 * G;
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) qf[kk] = *reinterpret_cast<const v4i*>(qp + 32 * kk);
+    for (int kk = 0; kk < KK; ++kk) qf[0][kk] = *reinterpret_cast<const v4i*>(qp + 32 * kk);
 
     // Row offsets of the chunk's tokens, in 16-byte units; the last token's
     // again up to the end of the last tile, so that masked places hold
@@ -296,13 +435,13 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         // Take q now: a wait for it inside the main loop would also wait for
         // the direct-to-LDS loads, which the compiler does not count.
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) asm volatile("" : "+v"(qf[kk]));
+        for (int kk = 0; kk < KK; ++kk) asm volatile("" : "+v"(qf[0][kk]));
     } else {
         // to fp16, the largest element in [2^13, 2^14)
         float f[KK][8], m = 0.0f;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            widen8<DT>(qf[kk], f[kk]);
+            widen8<DT>(qf[0][kk], f[kk]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(f[kk][e]));
         }
@@ -313,7 +452,7 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
             for (int w = 0; w < 4; ++w)
-                qf[kk][w] = (int)f16x2_rne_bits(__builtin_amdgcn_ldexpf(f[kk][2 * w], e), __builtin_amdgcn_ldexpf(f[kk][2 * w + 1], e));
+                qf[0][kk][w] = (int)f16x2_rne_bits(__builtin_amdgcn_ldexpf(f[kk][2 * w], e), __builtin_amdgcn_ldexpf(f[kk][2 * w + 1], e));
         qscale = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
     __syncthreads();
@@ -361,13 +500,13 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         }
     };
 
-    f32x4v acc[NA][DB];
+    f32x4v acc[1][NA][DB];
 #pragma unroll
     for (int i = 0; i < NA; ++i)
 #pragma unroll
-        for (int d = 0; d < DB; ++d) acc[i][d] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-    float M = kAttnLow, L = 0.0f;
-    const float sc = I8 ? qscale : a.scale * 1.44269504f;
+        for (int d = 0; d < DB; ++d) acc[0][i][d] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    float Ms[1] = {kAttnLow}, Ls[1] = {0.0f};
+    const float sc[1] = {I8 ? qscale : a.scale * 1.44269504f};
 
     if (wave < tiles) {
         read_offs(wave);
@@ -377,118 +516,27 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     for (int t = wave; t < tiles; t += NW) {
         const bool more = t + NW < tiles;
         wait_vmcnt<NL>();                                    // K of this tile; V came after it
-        f32x4v s[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-            const int row = 16 * u + i16;
-            const uint8_t* const kr = kring + row * RB;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                v4i kf;
-                if constexpr (I8) {
-                    const int piece = 4 * kk + G;
-                    kf = codes8_f16(*reinterpret_cast<const uint2*>(kr + (((piece >> 1) ^ Sh::swz(row)) << 4) + (piece & 1) * 8));
-                } else {
-                    kf = *reinterpret_cast<const v4i*>(kr + (((4 * kk + G) ^ Sh::swz(row)) << 4));
+        attn_tile<DT, I8, D, 1, WP>(
+            kring, vring, qf, sc, &kscale[I8 ? t * kAttnTile : 0], &vscale[I8 ? t * kAttnTile : 0], ve,
+            n - t * kAttnTile, t == wave, Ms, Ls, acc,
+            [&] {
+                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // K is read: its place is free
+                if (more) {
+                    read_offs(t + NW);
+                    issue_k();
                 }
-                s[u] = mfma16<KT>(kf, qf[kk], s[u]);
-            }
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // K is read: its place is free
-        if (more) {
-            read_offs(t + NW);
-            issue_k();
-        }
-        float p[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = s[e >> 2][e & 3] * sc;
-        const int tok0 = t * kAttnTile + 4 * G;
-        if constexpr (I8) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float4 ks = *reinterpret_cast<const float4*>(&kscale[tok0 + 16 * u]);
-                p[4 * u] *= ks.x; p[4 * u + 1] *= ks.y; p[4 * u + 2] *= ks.z; p[4 * u + 3] *= ks.w;
-            }
-        }
-        if ((t + 1) * kAttnTile > n) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (tok0 + 16 * (e >> 2) + (e & 3) >= n) p[e] = -INFINITY;
-        }
-        float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-        if (__any(top > M + kAttnSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = fmaxf(M, top);
-            const float f = __builtin_amdgcn_exp2f(M - m);
-            M = m;
-            L *= f;
-            if (t != wave) {                                 // the first tile's sums are still zero
-#pragma unroll
-                for (int i = 0; i < NA; ++i)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) acc[i][d] = acc[i][d] * f;
-            }
-        }
-        const float ref = M - kLift;
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(p[e] - ref);
-            sum += p[e];
-        }
-        L += sum;
-        if constexpr (I8) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float4 vs = *reinterpret_cast<const float4*>(&vscale[tok0 + 16 * u]);
-                const float v[4] = {vs.x, vs.y, vs.z, vs.w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) p[4 * u + r] *= __builtin_amdgcn_ldexpf(v[r], -ve);
-            }
-        }
-        v4i part[WP];                                        // the weights are their sum
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float x = p[2 * w], y = p[2 * w + 1];
-#pragma unroll
-            for (int i = 0; i < WP; ++i) {
-                const uint32_t h = narrow2<VT>(x, y);
-                const float2 back = widen2<VT>(h);
-                part[i][w] = (int)h;
-                x -= back.x;
-                y -= back.y;
-                if (NA == 2 && i == 1) {
-                    x *= kFine;
-                    y *= kFine;
-                }
-            }
-        }
-        if (more) wait_vmcnt<NL>();                          // V of this tile; the next K came after it
-        else wait_vmcnt<0>();
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-            v4i vf;
-            if constexpr (I8) {
-                // row r of the eight: token 4 G + r of the first tile or 4 G + r - 4 of the second
-                const int r = i16 >> 1, row = 4 * G + (r & 3) + 16 * (r >> 2);
-                vf = codes8_bf16(read_tr8(vring + row * RB + ((d ^ Sh::swz(row)) << 4) + (i16 & 1) * 8));
-            } else {
-                const int row = 4 * G + (i16 >> 2), c = 2 * d + ((i16 >> 1) & 1);
-                const uint2 x = read_tr16(vring + row * RB + ((c ^ Sh::swz2(row)) << 4) + (i16 & 1) * 8);
-                const uint2 y = read_tr16(vring + (row + 16) * RB + ((c ^ Sh::swz2(row + 16)) << 4) + (i16 & 1) * 8);
-                vf = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
-            }
-#pragma unroll
-            for (int i = 0; i < WP; ++i) {
-                f32x4v& sum = acc[NA == 2 ? i / 2 : 0][d];
-                sum = mfma16<VT>(vf, part[i], sum);
-            }
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // V is read
-        if (more) issue_v();
+            },
+            [&] {
+                if (more) wait_vmcnt<NL>();                  // V of this tile; the next K came after it
+                else wait_vmcnt<0>();
+            },
+            [&] {
+                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // V is read
+                if (more) issue_v();
+            });
     }
+    const float M = Ms[0];
+    float L = Ls[0];
 
     // The waves' sums meet in LDS: each in its own ring, [head][d], 16-byte
     // pieces exchanged by xor.
@@ -497,8 +545,8 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
     float* const own = reinterpret_cast<float*>(kring);
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
-        f32x4v sum = acc[0][d];
-        if constexpr (NA == 2) sum = sum + acc[1][d] * (1.0f / kFine);
+        f32x4v sum = acc[0][0][d];
+        if constexpr (NA == 2) sum = sum + acc[0][1][d] * (1.0f / AttnKind<DT, I8, WP>::fine);
         *reinterpret_cast<f32x4v*>(own + i16 * D + (((4 * d + G) ^ (i16 & 7)) << 2)) = sum;
     }
     if (lane < 16) {
