@@ -1,5 +1,22 @@
 // shared_prefix.hip -- attention of one new token per sequence over a paged
 // cache, where the sequences of a group begin with the same tokens.
+//
+// Mathematics: that of paged_attention.hip.  The tokens that a sequence sees
+// are those of its prefix and its own; both are cut into chunks, each chunk's
+// sums kept relative to a reference of their own, and joined.
+//
+// A chunk of a prefix is read once for all query rows of its group: sequence
+// by sequence the heads of one key head, R = members x (hq / hk) rows.  Per
+// byte of a 16-bit cache there are R multiply-adds, so HBM bounds a small group
+// and the matrix cores a large one.  Two forms of a block:
+//   - up to 16 rows (a small group, or a sequence's own tokens): the waves
+//     split the tokens, each with tiles of its own, as in paged_attention.hip;
+//   - more rows: the waves split the rows, up to MB blocks of 16 each, and
+//     share tiles of K and V in LDS, one in use and one on its way, one barrier
+//     a tile.
+// A weight enters the value product in two 16-bit parts.  Of bf16 they hold it
+// to 2^-17 of itself.  The second part of fp16 is the rest that the first left,
+// 2^11 times finer, in sums of its own: 2^-23 of a weight or 2^-50 of the largest.
 
 struct PrefixArgs {
     const uint16_t* q;
@@ -9,87 +26,653 @@ struct PrefixArgs {
     const int32_t* starts;
     const int32_t* table;
     const int32_t* lens;
+    float* part;                         // [batch * hq][slots][d] weighted values
+    float2* part_ml;                     // [batch * hq][slots] (M, sum)
     const uint8_t* ck;
     const uint8_t* cv;
     const float* cks;
     const float* cvs;
     int64_t q_bs, q_hs, o_bs, o_hs, pt_stride, table_stride, c_ps, c_hs, c_ts, s_ps, s_hs, s_ts;
-    int64_t pages, pcap, cap;                                // pcap, cap: tokens that a row of ptable, table can name
+    int64_t pages, pcap, cap;            // pcap, cap: tokens that a row of ptable, table can name
+    int64_t pblocks;                     // blocks of prefixes; those of sequences follow
     float scale;
-    int batch, hq, hk, prefixes, page_shift, d, i8, f16;
+    int batch, hq, hk, group, prefixes, page_shift;
+    int prows, psplits, pchunk;          // row blocks and chunks of prefixes
+    int row_blocks, splits, chunk;       // and of sequences
 };
 
-// One block per sequence and query head, 256 threads over the tokens: scores,
-// then the weights' sum, then the values.
-__global__ __launch_bounds__(256) void shared_prefix_kernel(PrefixArgs a)
+constexpr int kPrefixParts = 2;          // 16-bit parts of a weight
+constexpr int kPrefixSeg = 512;          // tokens whose row offsets are made at a time
+
+// Sizes for rows of RB bytes: four waves, 64 KiB of K and V in LDS, so that two
+// blocks share a CU.
+template <int RB>
+struct PrefixShape {
+    static constexpr int tile = RB <= 256 ? 64 : 32;         // tokens of a shared tile
+    static constexpr int walkers = RB <= 256 ? 4 : 2;        // waves with tiles of their own
+    static constexpr int shared = 4 * tile * RB, walked = walkers * 2 * kAttnTile * RB;
+    static constexpr int ring = shared > walked ? shared : walked;
+};
+
+__host__ __device__ constexpr int prefix_rows(int d) { return d <= 128 ? 128 : 64; }
+
+// What a block works on: rows row0 .. row0 + rows - 1 of the group that begins
+// at sequence seq0 (row r: sequence seq0 + r / group, head r % group of the key
+// head), and tokens first .. first + n - 1 of the list that `table` names.
+struct PrefixWork {
+    const int32_t* table;
+    int64_t first;
+    int n, rows, row0, seq0, kvh, slot;
+};
+
+// False if there is nothing to do.
+template <int ROWS>
+__device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
 {
-    __shared__ float red[256], qs[256], acc[256];
-    __shared__ int bad;
-    const int tid = threadIdx.x, h = blockIdx.x % a.hq;
-    const int64_t b = blockIdx.x / a.hq;
-    const int kvh = h / (a.hq / a.hk);
-    int p = -1, wrong = 0;
-    for (int i = 0; i <= a.prefixes && a.prefixes > 0; ++i) {
-        const int s = a.starts[i];
-        wrong |= s < 0 || s > a.batch || (i > 0 && s < a.starts[i - 1]);
-        p += s <= b;
+    const int lane = threadIdx.x & 63;
+    if ((int64_t)blockIdx.x >= a.pblocks) {                  // a sequence's own tokens
+        const int64_t id = (int64_t)blockIdx.x - a.pblocks, rest = id / a.splits, bk = rest / a.row_blocks;
+        const int split = (int)(id % a.splits), rb = (int)(rest % a.row_blocks);
+        w.kvh = (int)(bk % a.hk);
+        w.seq0 = (int)(bk / a.hk);
+        w.row0 = 16 * rb;
+        w.rows = min(16, a.group - w.row0);
+        w.table = a.table + w.seq0 * a.table_stride;
+        w.first = (int64_t)split * a.chunk;
+        w.n = (int)min<int64_t>(a.chunk, min((int64_t)a.lens[w.seq0], a.cap) - w.first);
+        w.slot = a.psplits + split;
+        return w.n > 0;
     }
-    if (p >= a.prefixes) p = -1;
-    const int64_t np = p < 0 ? 0 : min(max((int64_t)a.plens[p], (int64_t)0), a.pcap);
-    const int64_t n = np + min(max((int64_t)a.lens[b], (int64_t)0), a.cap);
-    auto at16 = [&](const uint8_t* base, int64_t i) {
-        const uint32_t w = reinterpret_cast<const uint16_t*>(base)[i];
-        return a.f16 ? widen2<CK_DT_FP16>(w).x : widen2<CK_DT_BF16>(w).x;
-    };
-    auto place = [&](int64_t j, int64_t& row, int64_t& srow) {
-        const int64_t t = j < np ? j : j - np;
-        const int32_t* const tab = j < np ? a.ptable + p * a.pt_stride : a.table + b * a.table_stride;
-        const int64_t page = tab[t >> a.page_shift], in = t & ((1 << a.page_shift) - 1);
-        row = page * a.c_ps + kvh * a.c_hs + in * a.c_ts;
-        srow = page * a.s_ps + kvh * a.s_hs + in * a.s_ts;
-        return page >= 0 && page < a.pages;
-    };
-    if (tid == 0) bad = wrong;
-    for (int e = tid; e < a.d; e += 256) qs[e] = at16(reinterpret_cast<const uint8_t*>(a.q), b * a.q_bs + h * a.q_hs + e);
-    acc[tid] = 0.0f;
-    __syncthreads();
-    float m = -3.402823466e38f, l = 0.0f;
-    for (int64_t j0 = 0; j0 < n && !bad; j0 += 256) {
-        float s = -INFINITY;
-        int64_t row = 0, srow = 0;
-        if (j0 + tid < n) {
-            if (place(j0 + tid, row, srow)) {
-                s = 0.0f;
-                for (int e = 0; e < a.d; ++e) s += qs[e] * (a.i8 ? (float)(int8_t)a.ck[row + e] : at16(a.ck, row + e));
-                s *= a.scale * 1.44269504f * (a.i8 ? a.cks[srow] : 1.0f);
-            } else {
-                bad = 1;
-            }
+    // The row blocks of a chunk and key head, which read the same rows, follow
+    // each other on one XCD (blocks go to the eight in turn).
+    const int64_t per = 8 * (int64_t)a.prows, unit = blockIdx.x / per * 8 + blockIdx.x % 8;
+    int slot = (int)(blockIdx.x % per / 8);
+    if (unit >= (int64_t)a.hk * a.psplits) return false;
+    w.slot = (int)(unit % a.psplits);
+    w.kvh = (int)(unit / a.psplits);
+    constexpr int most = 1 << 29;
+    int p = -1;
+    for (int base = 0; base < a.prefixes; base += 64) {      // whose row block it is: a sum over the prefixes before
+        int s0 = 0, blocks = 0, members = 0;
+        if (base + lane < a.prefixes) {
+            s0 = min(max(a.starts[base + lane], 0), a.batch);
+            members = min(max(a.starts[base + lane + 1], s0), a.batch) - s0;
+            blocks = (int)min<int64_t>(((int64_t)members * a.group + ROWS - 1) / ROWS, most);
         }
-        red[tid] = s;
-        __syncthreads();
-        float top = m;
-        for (int i = 0; i < 256; ++i) top = fmaxf(top, red[i]);
-        __syncthreads();
-        red[tid] = exp2f(s - top);
-        __syncthreads();
-        const float f = exp2f(m - top);
-        l *= f;
-        m = top;
-        float o = acc[tid] * f;
-        for (int i = 0; i < 256 && j0 + i < n; ++i) {
-            l += red[i];
-            if (tid < a.d && place(j0 + i, row, srow))
-                o += red[i] * (a.i8 ? (float)(int8_t)a.cv[row + tid] * a.cvs[srow] : at16(a.cv, row + tid));
+        int sum = blocks;                                    // at most `most`, whatever starts holds
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(sum, off);
+            if (lane >= off) sum = min(sum + o, most);
         }
-        acc[tid] = o;
-        __syncthreads();
+        const int prev = __shfl_up(sum, 1);
+        const unsigned long long past = __ballot(sum > slot);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            p = base + at;
+            if (at > 0) slot -= __shfl(prev, at);
+            w.seq0 = __shfl(s0, at);
+            w.row0 = slot * ROWS;
+            w.rows = min(ROWS, __shfl(members, at) * a.group - w.row0);
+            break;
+        }
+        slot -= __shfl(sum, 63);
     }
-    if (tid < a.d) {
-        const float v = bad ? NAN : n == 0 ? 0.0f : acc[tid] / l;
-        a.out[b * a.o_bs + h * a.o_hs + tid] = (uint16_t)((a.f16 ? narrow2<CK_DT_FP16>(v, 0.0f) : narrow2<CK_DT_BF16>(v, 0.0f)) & 0xffffu);
+    if (p < 0) return false;
+    p = __builtin_amdgcn_readfirstlane(p);
+    w.seq0 = __builtin_amdgcn_readfirstlane(w.seq0);
+    w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
+    w.rows = __builtin_amdgcn_readfirstlane(w.rows);
+    w.table = a.ptable + p * a.pt_stride;
+    w.first = (int64_t)w.slot * a.pchunk;
+    w.n = (int)min<int64_t>(a.pchunk, min((int64_t)a.plens[p], a.pcap) - w.first);
+    return w.n > 0;
+}
+
+// The queries of 16 rows: lane 16 G + i holds elements 32 kk + 8 G + 0 .. 7 of
+// row i; for an int8 cache as fp16, its largest element in [2^13, 2^14).
+// -> what a score is to be multiplied by.
+template <int DT, bool I8, int D>
+__device__ __forceinline__ float prefix_queries(const PrefixArgs& a, const PrefixWork& w, int row, v4i (&qf)[D / 32])
+{
+    constexpr int KK = D / 32;
+    const int G = (threadIdx.x & 63) >> 4;
+    const int r = w.row0 + min(row, w.rows - 1), seq = r / a.group, head = w.kvh * a.group + r - seq * a.group;
+    const uint16_t* const qp = a.q + (int64_t)(w.seq0 + seq) * a.q_bs + head * a.q_hs + 8 * G;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) qf[kk] = *reinterpret_cast<const v4i*>(qp + 32 * kk);
+    if constexpr (!I8) {
+        // Take them now: a later wait would also wait for the direct-to-LDS
+        // loads, which the compiler does not count.
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) asm volatile("" : "+v"(qf[kk]));
+        return a.scale * 1.44269504f;
+    } else {
+        float f[KK][8], m = 0.0f;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            widen8<DT>(qf[kk], f[kk]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_fabsf(f[kk][e]));
+        }
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const int e = m > 0.0f ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                qf[kk][x] = (int)f16x2_rne_bits(__builtin_amdgcn_ldexpf(f[kk][2 * x], e), __builtin_amdgcn_ldexpf(f[kk][2 * x + 1], e));
+        return __builtin_amdgcn_ldexpf(1.0f, -e);
     }
 }
+
+// Where the sums of row `row` go.
+__device__ __forceinline__ int64_t prefix_part(const PrefixArgs& a, const PrefixWork& w, int row)
+{
+    const int r = w.row0 + row, seq = r / a.group, head = w.kvh * a.group + r - seq * a.group;
+    return ((int64_t)(w.seq0 + seq) * a.hq + head) * (a.psplits + a.splits) + w.slot;
+}
+
+template <int RB, bool I8>
+struct PrefixShared {
+    __attribute__((aligned(1024))) uint8_t ring[PrefixShape<RB>::ring];
+    __attribute__((aligned(16))) uint32_t offs[kAttnChunk];
+    __attribute__((aligned(16))) float kscale[I8 ? kAttnChunk : 4], vscale[I8 ? kAttnChunk : 4];
+    float wave_m[4][16], wave_l[4][16], wave_v[2][4];
+    int bad_page;
+};
+
+// Row offsets (in 16-byte units) and scales of the chunk's tokens from ..
+// from + 256 PT - 1 into places dst and on; the last token's again up to
+// `end`, so that masked places hold values of a visible row.  A thread's loads
+// go out together, the pages of all its tokens and then the scales.
+// -> the largest value scale of the wave's tokens.
+template <int RB, bool I8, int PT>
+__device__ __forceinline__ float prefix_fill(const PrefixArgs& a, const PrefixWork& w, PrefixShared<RB, I8>& sh, int from,
+                                             int dst, int end)
+{
+    const int tid = threadIdx.x;
+    int32_t pages[PT], ats[PT];
+    float ks[PT], vs[PT], vmax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+        const int i = from + tid + j * 256;
+        if (i < end) {
+            const int64_t tok = w.first + min(i, w.n - 1);
+            pages[j] = w.table[tok >> a.page_shift];
+            ats[j] = (int32_t)(tok & ((1 << a.page_shift) - 1));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+        if (from + tid + j * 256 < end) {
+            int64_t page = pages[j];
+            if (page < 0 || page >= a.pages) {
+                sh.bad_page = 1;
+                page = 0;
+            }
+            sh.offs[dst + tid + j * 256] = (uint32_t)((page * a.c_ps + w.kvh * a.c_hs + ats[j] * a.c_ts) * (I8 ? 1 : 2) / 16);
+            if constexpr (I8) {
+                const int64_t so = page * a.s_ps + w.kvh * a.s_hs + ats[j] * a.s_ts;
+                ks[j] = a.cks[so];
+                vs[j] = a.cvs[so];
+            }
+        }
+    }
+    if constexpr (I8) {
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            if (from + tid + j * 256 < end) {
+                sh.kscale[dst + tid + j * 256] = ks[j] * a.scale * 1.44269504f;
+                sh.vscale[dst + tid + j * 256] = vs[j];
+                vmax = fmaxf(vmax, __builtin_fabsf(vs[j]));
+            }
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, off));
+    }
+    return vmax;
+}
+
+// Up to 16 rows: the waves split the tokens (at most kAttnChunk of them).
+template <int DT, bool I8, int D>
+__device__ __forceinline__ void prefix_walk(const PrefixArgs& a, const PrefixWork& w, PrefixShared<D * (I8 ? 1 : 2), I8>& sh)
+{
+    constexpr int RB = D * (I8 ? 1 : 2);
+    using Sh = AttnShape<RB>;
+    using Kind = AttnKind<DT, I8, kPrefixParts>;
+    constexpr int NW = PrefixShape<RB>::walkers, NL = Sh::loads, DB = D / 16, NA = Kind::NA;
+    const int tid = threadIdx.x, lane = tid & 63, G = lane >> 4, i16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tiles = (w.n + kAttnTile - 1) / kAttnTile;
+    v4i qf[1][D / 32];
+    float sc[1];
+    const float vwave = prefix_fill<RB, I8, 4>(a, w, sh, 0, 0, tiles * kAttnTile);
+    if (I8 && lane == 0) sh.wave_v[0][wave] = vwave;
+    sc[0] = prefix_queries<DT, I8, D>(a, w, i16, qf[0]);
+    __syncthreads();
+    int ve = 0;                                              // value scales are taken relative to 2^ve
+    if constexpr (I8) {
+        const float vmax = fmaxf(fmaxf(sh.wave_v[0][0], sh.wave_v[0][1]), fmaxf(sh.wave_v[0][2], sh.wave_v[0][3]));
+        ve = vmax > 0.0f ? __builtin_amdgcn_frexp_expf(vmax) : 0;
+    }
+    float M[1] = {kAttnLow}, L[1] = {0.0f};
+    f32x4v acc[1][NA][DB];
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[0][i][d] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    uint8_t* const kring = sh.ring + (wave < NW ? wave : 0) * (2 * Sh::tile);
+    uint8_t* const vring = kring + Sh::tile;
+    const uint32_t klds = lds_addr(kring), vlds = klds + Sh::tile;
+    uint32_t off[NL];
+    auto read_offs = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) off[j] = sh.offs[t * kAttnTile + (64 * j + lane) / Sh::chunks];
+    };
+    auto issue_k = [&]() {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int row = (64 * j + lane) / Sh::chunks, pc = (64 * j + lane) % Sh::chunks;
+            dma16_at(a.ck + (uint64_t)(off[j] + (uint32_t)(pc ^ Sh::swz(row))) * 16, klds + j * 1024);
+        }
+    };
+    auto issue_v = [&]() {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int row = (64 * j + lane) / Sh::chunks, pc = (64 * j + lane) % Sh::chunks;
+            dma16_at(a.cv + (uint64_t)(off[j] + (uint32_t)(pc ^ (I8 ? Sh::swz(row) : Sh::swz2(row)))) * 16, vlds + j * 1024);
+        }
+    };
+    if (wave < NW) {
+        if (wave < tiles) {
+            read_offs(wave);
+            issue_k();
+            issue_v();
+        }
+        for (int t = wave; t < tiles; t += NW) {
+            const bool more = t + NW < tiles;
+            wait_vmcnt<NL>();                                // K of this tile; V came after it
+            attn_tile<DT, I8, D, 1, kPrefixParts>(
+                kring, vring, qf, sc, &sh.kscale[I8 ? t * kAttnTile : 0], &sh.vscale[I8 ? t * kAttnTile : 0], ve,
+                w.n - t * kAttnTile, t == wave, M, L, acc,
+                [&] {
+                    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // K is read: its place is free
+                    if (more) {
+                        read_offs(t + NW);
+                        issue_k();
+                    }
+                },
+                [&] {
+                    if (more) wait_vmcnt<NL>();              // V of this tile; the next K came after it
+                    else wait_vmcnt<0>();
+                },
+                [&] {
+                    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // V is read
+                    if (more) issue_v();
+                });
+        }
+        // The waves' sums meet in LDS: each in its own ring, [row][d], 16-byte
+        // pieces exchanged by xor.
+        L[0] += __shfl_xor(L[0], 16);
+        L[0] += __shfl_xor(L[0], 32);
+        float* const own = reinterpret_cast<float*>(kring);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            f32x4v sum = acc[0][0][d];
+            if constexpr (NA == 2) sum = sum + acc[0][1][d] * (1.0f / Kind::fine);
+            *reinterpret_cast<f32x4v*>(own + i16 * D + (((4 * d + G) ^ (i16 & 7)) << 2)) = sum;
+        }
+        if (lane < 16) {
+            sh.wave_m[wave][lane] = M[0];
+            sh.wave_l[wave][lane] = L[0];
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < w.rows * (D / 4); e += 256) {
+        const int h = e / (D / 4), c = e % (D / 4);
+        float m = sh.wave_m[0][h];
+#pragma unroll
+        for (int x = 1; x < NW; ++x) m = fmaxf(m, sh.wave_m[x][h]);
+        float l = 0.0f;
+        f32x4v o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int x = 0; x < NW; ++x) {
+            const float f = __builtin_amdgcn_exp2f(sh.wave_m[x][h] - m);   // a wave without tiles: 0
+            l = __builtin_fmaf(f, sh.wave_l[x][h], l);
+            const f32x4v v = *reinterpret_cast<const f32x4v*>(reinterpret_cast<const float*>(sh.ring + x * (2 * Sh::tile)) + h * D + ((c ^ (h & 7)) << 2));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, v[r], o[r]);
+        }
+        if constexpr (I8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = __builtin_amdgcn_ldexpf(o[r], ve);
+        }
+        const int64_t at = prefix_part(a, w, h);
+        *reinterpret_cast<f32x4v*>(a.part + at * D + 4 * c) = o;
+        if (c == 0) a.part_ml[at] = sh.bad_page ? make_float2(0.0f, NAN) : make_float2(m, l);
+    }
+}
+
+// More rows: row block b of wave x is the group's b * 4 + x th of 16, and all
+// waves go through the same tiles.
+template <int DT, bool I8, int D, int MB>
+__device__ __forceinline__ void prefix_share(const PrefixArgs& a, const PrefixWork& w, PrefixShared<D * (I8 ? 1 : 2), I8>& sh)
+{
+    constexpr int RB = D * (I8 ? 1 : 2), T = PrefixShape<RB>::tile;
+    using Sh = AttnShape<RB>;
+    using Kind = AttnKind<DT, I8, kPrefixParts>;
+    constexpr int DB = D / 16, NA = Kind::NA, LT = T * RB / 1024;    // 1 KiB loads of a tile's K
+    constexpr int NL = (LT + 3) / 4;                         // and of those a wave's
+    constexpr int TS = kPrefixSeg / T;                       // tiles of a segment
+    const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = (w.n + T - 1) / T, end = tiles * T;
+    v4i qf[MB][D / 32];
+    float sc[MB], M[MB], L[MB];
+    f32x4v acc[MB][NA][DB];
+    auto fill = [&](int seg) {
+        const float v = prefix_fill<RB, I8, kPrefixSeg / 256>(a, w, sh, seg * kPrefixSeg, (seg & 1) * kPrefixSeg, end);
+        if (I8 && lane == 0) sh.wave_v[seg & 1][wave] = v;
+    };
+    fill(0);
+    if (end > kPrefixSeg) fill(1);
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        sc[b] = prefix_queries<DT, I8, D>(a, w, (b * 4 + wave) * 16 + i16, qf[b]);
+        M[b] = kAttnLow;
+        L[b] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) acc[b][i][d] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const uint32_t lds0 = lds_addr(sh.ring);
+    // A wave copies every fourth KiB of a tile.
+    auto issue = [&](int t) {
+        const uint32_t dst = lds0 + (t & 1) * (2 * T * RB);
+        uint32_t off[NL];
+#pragma unroll
+        for (int j = 0; j < NL; ++j)
+            if (4 * j + wave < LT) off[j] = sh.offs[t % (2 * TS) * T + (64 * (4 * j + wave) + lane) / Sh::chunks];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            if (4 * j + wave >= LT) break;
+            const int at = 64 * (4 * j + wave) + lane, row = at / Sh::chunks, pc = at % Sh::chunks;
+            dma16_at(a.ck + (uint64_t)(off[j] + (uint32_t)(pc ^ Sh::swz(row))) * 16, dst + (4 * j + wave) * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            if (4 * j + wave >= LT) break;
+            const int at = 64 * (4 * j + wave) + lane, row = at / Sh::chunks, pc = at % Sh::chunks;
+            dma16_at(a.cv + (uint64_t)(off[j] + (uint32_t)(pc ^ (I8 ? Sh::swz(row) : Sh::swz2(row)))) * 16,
+                     dst + T * RB + (4 * j + wave) * 1024);
+        }
+    };
+    const bool busy = wave * 16 < w.rows;
+    int ve = -300;                                           // value scales are taken relative to 2^ve: none yet
+    __syncthreads();
+    issue(0);
+    for (int t = 0; t < tiles; ++t) {
+        wait_vmcnt<0>();
+        __syncthreads();                                     // the tile has landed, the one before it is read
+        if (t % TS == 0 && t > 0 && (t / TS + 1) * kPrefixSeg < end) fill(t / TS + 1);
+        if (t + 1 < tiles) issue(t + 1);
+        if constexpr (I8) {
+            if (t % TS == 0) {                               // raised where a segment's scales are far above it
+                const float* const v = sh.wave_v[t / TS & 1];
+                const float vmax = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                const int e = vmax > 0.0f ? __builtin_amdgcn_frexp_expf(vmax) : -300;
+                if (e > (ve == -300 ? -300 : ve + 8)) {
+#pragma unroll
+                    for (int b = 0; b < MB; ++b)
+#pragma unroll
+                        for (int i = 0; i < NA; ++i)
+#pragma unroll
+                            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) acc[b][i][d][r] = __builtin_amdgcn_ldexpf(acc[b][i][d][r], ve - e);
+                    ve = e;
+                }
+            }
+        }
+        if (busy) {
+#pragma unroll 1
+            for (int u = 0; u < T / kAttnTile; ++u) {
+                const int limit = w.n - t * T - u * kAttnTile;
+                if (limit <= 0) break;
+                const uint8_t* const kr = sh.ring + (t & 1) * (2 * T * RB) + u * (kAttnTile * RB);
+                const int at = t % (2 * TS) * T + u * kAttnTile;
+                attn_tile<DT, I8, D, MB, kPrefixParts>(kr, kr + T * RB, qf, sc, &sh.kscale[I8 ? at : 0], &sh.vscale[I8 ? at : 0],
+                                                       ve, limit, t + u == 0, M, L, acc, [] {}, [] {}, [] {});
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        L[b] += __shfl_xor(L[b], 16);
+        L[b] += __shfl_xor(L[b], 32);
+        const int row = (b * 4 + wave) * 16 + i16;
+        if (row < w.rows) {
+            const int64_t at = prefix_part(a, w, row);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                f32x4v sum = acc[b][0][d];
+                if constexpr (NA == 2) sum = sum + acc[b][1][d] * (1.0f / Kind::fine);
+                if constexpr (I8) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sum[r] = __builtin_amdgcn_ldexpf(sum[r], ve);
+                }
+                *reinterpret_cast<f32x4v*>(a.part + at * D + 16 * d + 4 * G) = sum;
+            }
+            if (G == 0) a.part_ml[at] = sh.bad_page ? make_float2(0.0f, NAN) : make_float2(M[b], L[b]);
+        }
+    }
+}
+
+template <int DT, bool I8, int D>
+__global__ __launch_bounds__(256, 2) void shared_prefix_kernel(PrefixArgs a)
+{
+    constexpr int RB = D * (I8 ? 1 : 2);
+    __shared__ PrefixShared<RB, I8> sh;
+    PrefixWork w;
+    if (!prefix_work<prefix_rows(D)>(a, w)) return;
+    if (threadIdx.x == 0) sh.bad_page = 0;
+    __syncthreads();
+    if (a.pages == 0) {                                      // no page is inside the cache
+        for (int r = threadIdx.x; r < w.rows; r += 256) a.part_ml[prefix_part(a, w, r)] = make_float2(0.0f, NAN);
+        return;
+    }
+    if (w.rows <= 16 && w.n <= kAttnChunk) prefix_walk<DT, I8, D>(a, w, sh);
+    else if (D > 128 || w.rows <= 64) prefix_share<DT, I8, D, 1>(a, w, sh);
+    else if constexpr (D <= 128) prefix_share<DT, I8, D, 2>(a, w, sh);
+}
+
+// Joins the chunks of one sequence and head, those of its prefix and its own:
+// a lane has four elements of the values, P groups of lanes each add every
+// P-th chunk (four at a time, under a running M), and their sums are added in
+// LDS, all in an order that the sizes fix.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void shared_prefix_join_kernel(PrefixArgs a)
+{
+    constexpr int C = D / 4;                                 // lanes that hold the values, four each
+    constexpr int P = 256 / C;                               // chunks added side by side
+    constexpr int U = 4;
+    __shared__ f32x4v sums[P][C];
+    __shared__ float ms[P], ls[P];
+    const int tid = threadIdx.x, c = tid % C, g = tid / C;
+    const int64_t bh = blockIdx.x;
+    const int h = (int)(bh % a.hq);
+    const int64_t b = bh / a.hq;
+    // Its prefix: as many entries of starts as are not past b, less one.
+    int before = 0, wrong = 0;
+    if (a.prefixes > 0) {
+        for (int i = tid; i <= a.prefixes; i += 256) {
+            const int s = a.starts[i];
+            before += s <= b;
+            wrong |= s < 0 || s > a.batch || (i > 0 && s < a.starts[i - 1]);
+        }
+        wrong = __syncthreads_or(wrong);
+        if (a.prefixes < 256) {
+            before = __syncthreads_count(before);
+        } else {
+            __shared__ int total;
+            if (tid == 0) total = 0;
+            __syncthreads();
+            if (before) atomicAdd(&total, before);
+            __syncthreads();
+            before = total;
+        }
+    }
+    const int p = before - 1;
+    const int64_t np = p < 0 || p >= a.prefixes ? 0 : min(max((int64_t)a.plens[p], (int64_t)0), a.pcap);
+    const int64_t no = min(max((int64_t)a.lens[b], (int64_t)0), a.cap);
+    const int shared = (int)((np + a.pchunk - 1) / a.pchunk), count = shared + (int)((no + a.chunk - 1) / a.chunk);
+    const int64_t slots = a.psplits + a.splits;
+    const float2* const ml = a.part_ml + bh * slots;
+    const float* const part = a.part + bh * slots * D + 4 * c;
+    uint16_t* const out = a.out + b * a.o_bs + h * a.o_hs;
+    if (count == 0 || wrong) {
+        if (tid < C) {
+            const uint32_t v = wrong ? kNan2<DT> : 0u;
+            *reinterpret_cast<uint2*>(out + 4 * tid) = make_uint2(v, v);
+        }
+        return;
+    }
+    float m = kAttnLow, l = 0.0f;
+    f32x4v o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = g; g < P && s0 < count; s0 += P * U) {
+        float2 x[U];
+        f32x4v v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + P * u;
+            if (s < count) {
+                const int64_t slot = s < shared ? s : a.psplits + (s - shared);
+                x[u] = ml[slot];
+                v[u] = *reinterpret_cast<const f32x4v*>(part + slot * D);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + P * u < count) top = fmaxf(top, x[u].x);
+        const float old = __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        l *= old;
+        o = o * old;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s0 + P * u < count) {
+                const float f = __builtin_amdgcn_exp2f(x[u].x - m);
+                l = __builtin_fmaf(f, x[u].y, l);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, v[u][r], o[r]);
+            }
+        }
+    }
+    if (g < P) {
+        sums[g][c] = o;
+        if (c == 0) {
+            ms[g] = m;
+            ls[g] = l;
+        }
+    }
+    __syncthreads();
+    if (tid < C) {
+        m = ms[0];
+#pragma unroll
+        for (int i = 1; i < P; ++i) m = fmaxf(m, ms[i]);
+        o = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float f = __builtin_amdgcn_exp2f(ms[i] - m);   // a group without chunks: 0
+            l = __builtin_fmaf(f, ls[i], l);
+            const f32x4v q = sums[i][tid];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, q[r], o[r]);
+        }
+        const float inv = 1.0f / l;
+        uint2 w;
+        w.x = narrow2<DT>(o[0] * inv, o[1] * inv);
+        w.y = narrow2<DT>(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<uint2*>(out + 4 * tid) = w;
+    }
+}
+
+namespace {
+
+struct PrefixPlan {
+    int64_t prows, psplits, pchunk, pblocks;                 // of prefixes
+    int64_t row_blocks, splits, chunk, blocks;               // of sequences; blocks: the whole grid
+    int64_t bytes;
+};
+
+// Chunks.  A prefix's are as long as two blocks a CU allow in one round, or in
+// as many whole rounds as waste least (a round of blocks takes as long as its
+// chunk and a fixed part), and 128 tokens at least; where groups have up to 16
+// rows on average 1024 at most, which the form for few rows takes.  Sequences'
+// own chunks follow the rule of paged_attention.hip.
+bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_dim, int64_t prefixes,
+                 int64_t pcap, int64_t cap)
+{
+    const int64_t limit = 0x7fffffff, group = hq / hk, round = 2 * kNumCUs;
+    if (batch * hq > limit) return false;
+    p = PrefixPlan{};
+    const int64_t used = std::min(prefixes, batch);          // prefixes with a sequence, at most
+    p.pchunk = 128;
+    if (used > 0 && pcap > 0 && hq > 0) {
+        p.prows = cdiv(batch * group, prefix_rows((int)head_dim)) + used - 1;
+        const int64_t pairs = p.prows * hk, most = batch * group <= 16 * used ? kAttnChunk : int64_t(1) << 30;
+        int64_t least = INT64_MAX;
+        for (int64_t r = 1; r <= 8; ++r) {
+            const int64_t s = std::max<int64_t>(1, r * round / pairs);
+            const int64_t chunk = std::min(most, cdiv(cdiv(pcap, s), 128) * 128);
+            const int64_t time = cdiv(pairs * cdiv(pcap, chunk), round) * (chunk + 128);
+            if (time < least) least = time, p.pchunk = chunk;
+        }
+        p.psplits = cdiv(pcap, p.pchunk);
+        if (pairs > limit / (p.psplits + 8)) return false;
+        p.pblocks = cdiv(hk * p.psplits, 8) * 8 * p.prows;
+    }
+    p.row_blocks = cdiv(group, 16);
+    const int64_t pairs = batch * hk * p.row_blocks, tiles = std::min<int64_t>(cdiv(cap, kAttnTile), 1 << 20);
+    p.chunk = std::min<int64_t>(std::max<int64_t>(cdiv(cdiv(tiles * pairs, round), 4) * 4, 4) * kAttnTile, kAttnChunk);
+    p.splits = std::max<int64_t>(1, cdiv(cap, p.chunk));
+    if (pairs > limit / p.splits || pairs * p.splits + p.pblocks > limit) return false;
+    p.blocks = p.pblocks + pairs * p.splits;
+    p.bytes = batch * hq * (p.psplits + p.splits) * (head_dim + 2) * 4;
+    return true;
+}
+
+template <int DT, bool I8>
+const void* prefix_fn(int64_t d)
+{
+    switch (d) {
+    case 64: return reinterpret_cast<const void*>(&shared_prefix_kernel<DT, I8, 64>);
+    case 96: return reinterpret_cast<const void*>(&shared_prefix_kernel<DT, I8, 96>);
+    case 128: return reinterpret_cast<const void*>(&shared_prefix_kernel<DT, I8, 128>);
+    case 192: return reinterpret_cast<const void*>(&shared_prefix_kernel<DT, I8, 192>);
+    default: return reinterpret_cast<const void*>(&shared_prefix_kernel<DT, I8, 256>);
+    }
+}
+
+template <int DT>
+const void* prefix_join_fn(int64_t d)
+{
+    switch (d) {
+    case 64: return reinterpret_cast<const void*>(&shared_prefix_join_kernel<DT, 64>);
+    case 96: return reinterpret_cast<const void*>(&shared_prefix_join_kernel<DT, 96>);
+    case 128: return reinterpret_cast<const void*>(&shared_prefix_join_kernel<DT, 128>);
+    case 192: return reinterpret_cast<const void*>(&shared_prefix_join_kernel<DT, 192>);
+    default: return reinterpret_cast<const void*>(&shared_prefix_join_kernel<DT, 256>);
+    }
+}
+
+}  // namespace
 
 extern "C" int64_t ck_shared_prefix_attention_workspace(int64_t batch, int64_t hq, int64_t hk, int64_t head_dim,
                                                         int64_t prefixes, int64_t prefix_width, int64_t table_width,
@@ -97,9 +680,10 @@ extern "C" int64_t ck_shared_prefix_attention_workspace(int64_t batch, int64_t h
 {
     if (batch < 0 || hq < 0 || hk < 1 || hq % hk != 0 || !attention_dim_ok(head_dim) || prefixes < 0 || prefix_width < 0 ||
         table_width < 0 || !is_pow2(page_size) || page_size > 32768 || prefixes > (1 << 20) ||
-        batch * hq > 0x7fffffff || !attention_sizes_ok(batch, hq, hk, table_width, page_size) || !attention_sizes_ok(batch, hq, hk, prefix_width, page_size))
+        !attention_sizes_ok(batch, hq, hk, table_width, page_size) || !attention_sizes_ok(batch, hq, hk, prefix_width, page_size))
         return -1;
-    return 0;
+    PrefixPlan plan;
+    return prefix_plan(plan, batch, hq, hk, head_dim, prefixes, prefix_width * page_size, table_width * page_size) ? plan.bytes : -1;
 }
 
 extern "C" ck_status ck_shared_prefix_attention(const ck_prefix_args* args, const ck_kv_cache* cache, hipStream_t stream)
@@ -135,7 +719,12 @@ extern "C" ck_status ck_shared_prefix_attention(const ck_prefix_args* args, cons
         return fail(CK_ERR_UNSUPPORTED, "the cache spans more than 64 GiB");
     if (!rows_apart(d, {p.batch, p.out_batch_stride}, {p.hq, p.out_head_stride}))
         return fail(CK_ERR_INVALID_ARG, "rows of out overlap");
-    if (p.batch * p.hq > 0x7fffffff) return fail(CK_ERR_UNSUPPORTED, "too many blocks");
+    PrefixPlan plan;
+    if (!prefix_plan(plan, p.batch, p.hq, cache->heads, d, p.prefixes, p.prefix_width * cache->page_size, p.table_width * cache->page_size))
+        return fail(CK_ERR_UNSUPPORTED, "too many blocks");
+    if (!p.workspace || p.workspace_bytes < plan.bytes)
+        return fail(CK_ERR_INVALID_ARG, "the workspace needs %lld bytes", (long long)plan.bytes);
+    if (!aligned(p.workspace, 256)) return fail(CK_ERR_UNSUPPORTED, "misaligned workspace");
     if ((s = check_device()) != CK_OK) return s;
     PrefixArgs a{};
     a.q = (const uint16_t*)p.q; a.out = (uint16_t*)p.out; a.ptable = p.prefix_table; a.plens = p.prefix_lens; a.starts = p.starts;
@@ -147,8 +736,16 @@ extern "C" ck_status ck_shared_prefix_attention(const ck_prefix_args* args, cons
     a.s_ps = cache->scale_page_stride; a.s_hs = cache->scale_head_stride; a.s_ts = cache->scale_token_stride;
     a.pages = cache->pages; a.pcap = p.prefix_width * cache->page_size; a.cap = p.table_width * cache->page_size;
     a.scale = p.scale; a.batch = (int)p.batch; a.hq = (int)p.hq; a.hk = (int)cache->heads; a.prefixes = (int)p.prefixes;
-    a.page_shift = ilog2(cache->page_size); a.d = (int)d; a.i8 = i8; a.f16 = f16;
+    a.page_shift = ilog2(cache->page_size); a.group = (int)(p.hq / cache->heads);
+    a.part = (float*)p.workspace;
+    a.part_ml = (float2*)(a.part + p.batch * p.hq * (plan.psplits + plan.splits) * d);
+    a.prows = (int)plan.prows; a.psplits = (int)plan.psplits; a.pchunk = (int)plan.pchunk; a.pblocks = plan.pblocks;
+    a.row_blocks = (int)plan.row_blocks; a.splits = (int)plan.splits; a.chunk = (int)plan.chunk;
+    const void* fn = f16 ? (i8 ? prefix_fn<CK_DT_FP16, true>(d) : prefix_fn<CK_DT_FP16, false>(d))
+                         : (i8 ? prefix_fn<CK_DT_BF16, true>(d) : prefix_fn<CK_DT_BF16, false>(d));
+    const void* join = f16 ? prefix_join_fn<CK_DT_FP16>(d) : prefix_join_fn<CK_DT_BF16>(d);
     void* kargs[] = {&a};
-    s = launch(reinterpret_cast<const void*>(&shared_prefix_kernel), (unsigned)(p.batch * p.hq), 256, kargs, stream, "shared_prefix");
-    return s == CK_OK ? ok() : s;
+    if ((s = launch(fn, (unsigned)plan.blocks, 256, kargs, stream, "shared_prefix_attention")) != CK_OK) return s;
+    if ((s = launch(join, (unsigned)(p.batch * p.hq), 256, kargs, stream, "shared_prefix_join")) != CK_OK) return s;
+    return ok();
 }
