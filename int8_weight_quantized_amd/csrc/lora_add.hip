@@ -29,13 +29,16 @@ struct LoraArgs {
     void* out;
     float* v;                            // [ksplits][m][vstride], of the first launch
     int64_t ldx, ldy, ldo, a_stride, b_stride, m;
-    int n, k, rank, adapters, out_dtype;
-    int vstride, ksplits, slices;
+    int n, k, rank, adapters;
+    int vstride, ksplits, slices, slice; // slice: columns of one
+    int turn;                            // where B's pieces are in LDS
     int copy, wide;                      // rows without an adapter are copied; 16-byte accesses of y and out
 };
 
 constexpr int kLoraRows = 512;           // rows up to which every adapter of 64 rows has its own blocks
-constexpr int kLoraWaves = 8;
+constexpr int kLoraWaves = 8;            // of a block that makes v
+
+template <int N> struct IntTag { static constexpr int value = N; };
 
 // The next adapter among up to 64 rows, each lane with its row's id, and the
 // rows that have it; `left`: those still to come.
@@ -47,6 +50,32 @@ __device__ __forceinline__ uint64_t lora_members(uint64_t& left, int ids, int& i
     return members;
 }
 
+// The rows of a block: `left` of them have an adapter (`without`: those that
+// have none).  With units > 0 the block has the unit-th adapter alone, and of the
+// others every units-th row.
+struct LoraRows {
+    int64_t r0;
+    int count, ids;                      // this lane's row's id
+    uint64_t left, without;
+
+    __device__ __forceinline__ LoraRows(const LoraArgs& a, int64_t block, int group, int units)
+    {
+        const int lane = threadIdx.x & 63;
+        int unit = units > 0 ? (int)(block % units) : 0;
+        r0 = (units > 0 ? block / units : block) * group;
+        count = (int)min<int64_t>(group, a.m - r0);
+        ids = lane < count ? a.ids[r0 + lane] : -1;
+        left = __ballot(ids >= 0 && ids < a.adapters);
+        without = __ballot(lane < count && (units == 0 || lane % units == unit)) & ~left;
+        int id;
+        for (; unit > 0 && left; --unit) lora_members(left, ids, id);
+        if (units > 0 && left) {
+            uint64_t rest = left;
+            left = lora_members(rest, ids, id);
+        }
+    }
+};
+
 // The members in order: lane p gets the p-th one's row.
 __device__ __forceinline__ int lora_places(uint64_t members)
 {
@@ -54,222 +83,326 @@ __device__ __forceinline__ int lora_places(uint64_t members)
     return __builtin_amdgcn_ds_permute((members >> lane & 1 ? before : __popcll(members) + lane - before) * 4, lane);
 }
 
-// v^T of 16 rows over the columns k0 .. k1 - 1 of this wave: lane 16 G + i gets
-// ranks 16 f + 4 G + r of the row that its xp points at.
-template <int DT, int RF>
-__device__ __forceinline__ void lora_shrink(const LoraArgs& a, const uint16_t* xp, const uint16_t* ap, int k0, int k1,
-                                            f32x4v (&acc)[RF])
+// d[0] of a quad's first lane + d[1] of its second + d[2] of its third + d[3] of
+// its fourth, in all four.
+__device__ __forceinline__ float quad_diagonal(const f32x4v& d)
 {
-    constexpr int U = RF == 1 ? 8 : RF == 2 ? 6 : RF == 4 ? 4 : RF == 8 ? 2 : 1;     // steps whose loads go out together
-    const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
-    const uint16_t* rows[RF];
+    const int t0 = __builtin_amdgcn_update_dpp(0, __float_as_int(d[0]), 0x00, 0xf, 0xf, true);
+    const int t1 = __builtin_amdgcn_update_dpp(0, __float_as_int(d[1]), 0x55, 0xf, 0xf, true);
+    const int t2 = __builtin_amdgcn_update_dpp(0, __float_as_int(d[2]), 0xaa, 0xf, 0xf, true);
+    const int t3 = __builtin_amdgcn_update_dpp(0, __float_as_int(d[3]), 0xff, 0xf, 0xf, true);
+    return (__int_as_float(t0) + __int_as_float(t1)) + (__int_as_float(t2) + __int_as_float(t3));
+}
+
+// The first product, 16 RP ranks from rank0 on of 4 XG rows, over steps s0 ..
+// s1 - 1 of 128 columns.  A load of 16 bytes a lane costs as many cycles as the
+// 64-byte segments that each four lanes in a row touch, so such four take 64
+// bytes of a row of A or x, which makes them different operand rows: row 4 a + b
+// of the first operand is piece b (8 columns) of A's row a, column 4 c + b of the
+// second piece b of x's row c, and where the two b agree the product is a part
+// of v, four of which add up to it.  (With operand rows that are A's and x's the
+// loads took three times as long.)  Lane 16 G + 4 c + b ends up with ranks rank0 +
+// 4 q + G of row 4 g + c in v[g][q], for every b.
+// xo: the rows' byte offsets from xb, with this lane's columns of 128.
+template <int DT, int XG, int RP, int U>
+__device__ __forceinline__ void lora_shrink(const LoraArgs& a, const uint16_t* xb, const uint32_t (&xo)[XG], const uint16_t* wb,
+                                            int rank0, int s0, int s1, float (&v)[XG][4 * RP])
+{
+    const int lane = threadIdx.x & 63;
+    const int at = (lane >> 4) * 32 + (lane & 3) * 8;        // this lane's columns of 128
+    const int last = (a.rank - rank0) / 4 - 1;               // of the groups of four ranks
+    const uint32_t wo = (uint32_t)(((lane >> 2) & 3) * a.k + at) * 2;
+    const char* const x = reinterpret_cast<const char*>(xb);
+    const char* w[4 * RP];
 #pragma unroll
-    for (int f = 0; f < RF; ++f) {
-        acc[f] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-        rows[f] = ap + (int64_t)min(16 * f + i16, a.rank - 1) * a.k;
-    }
-    for (int k = k0; k < k1; k += 32 * U) {
-        v4i x[U], w[U][RF];
+    for (int q = 0; q < 4 * RP; ++q) w[q] = reinterpret_cast<const char*>(wb + (int64_t)(rank0 + 4 * min(q, last)) * a.k);
+    f32x4v acc[XG][4 * RP];
+#pragma unroll
+    for (int g = 0; g < XG; ++g)
+#pragma unroll
+        for (int q = 0; q < 4 * RP; ++q) acc[g][q] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = s0; s < s1; s += U) {
+        v4i xs[U][XG], ws[U][4 * RP];
+        // past the end: the last piece of the row again, then zeros
+        const bool whole = s + U <= s1 && (s + U) * 128 <= a.k;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int at = k + 32 * u + 8 * G;
-            const bool in = at < k1;
-            x[u] = in ? *reinterpret_cast<const v4i*>(xp + at) : v4i{0, 0, 0, 0};
+            const uint32_t c = (s + u) * 256, off = whole ? c : min(c + 2 * at, (uint32_t)(2 * a.k - 16)) - 2 * at;
 #pragma unroll
-            for (int f = 0; f < RF; ++f) w[u][f] = in ? *reinterpret_cast<const v4i*>(rows[f] + at) : v4i{0, 0, 0, 0};
+            for (int g = 0; g < XG; ++g) xs[u][g] = *reinterpret_cast<const v4i*>(x + (xo[g] + off));
+#pragma unroll
+            for (int q = 0; q < 4 * RP; ++q) ws[u][q] = *reinterpret_cast<const v4i*>(w[q] + (wo + off));
+        }
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s + u >= s1 || (s + u) * 128 + at >= a.k) {
+#pragma unroll
+                    for (int g = 0; g < XG; ++g) xs[u][g] = v4i{0, 0, 0, 0};
+#pragma unroll
+                    for (int q = 0; q < 4 * RP; ++q) ws[u][q] = v4i{0, 0, 0, 0};
+                }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int f = 0; f < RF; ++f) acc[f] = mfma16<DT>(w[u][f], x[u], acc[f]);
+            for (int q = 0; q < 4 * RP; ++q)
+#pragma unroll
+                for (int g = 0; g < XG; ++g) acc[g][q] = mfma16<DT>(ws[u][q], xs[u][g], acc[g][q]);
     }
+#pragma unroll
+    for (int g = 0; g < XG; ++g)
+#pragma unroll
+        for (int q = 0; q < 4 * RP; ++q) v[g][q] = quad_diagonal(acc[g][q]);
 }
 
-// The first launch: v of a group of rows, over one part of k.
-template <int DT, int RF>
-__global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs a, int group, int each)
+// The rows that a lane's x are, as byte offsets: row 4 g + c of 16 from place t0
+// on, the last one again past the end.
+template <int XG>
+__device__ __forceinline__ void lora_x(const LoraArgs& a, int places, int t0, int rows, uint32_t (&xo)[XG])
 {
-    __shared__ f32x4v red[kLoraWaves][RF][64];
-    const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, G = lane >> 4;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int g = 0; g < XG; ++g)
+        xo[g] = (uint32_t)(__shfl(places, min(t0 + 4 * g + ((lane >> 2) & 3), rows - 1)) * (uint32_t)a.ldx + (lane >> 4) * 32 + (lane & 3) * 8) * 2;
+}
+
+// The first launch: v of a group of rows, over one part of k.  XG: 1 for groups
+// of up to 64 rows whose adapters have a few each (four at a time), 4 for 16
+// rows in a row.
+template <int DT, int XG, int RP>
+__global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArgs a, int group, int units)
+{
+    constexpr int NW = kLoraWaves, U = XG == 4 ? 2 : RP == 4 ? 2 : 4;
+    __shared__ float red[NW][4 * XG][16 * RP + 4];
+    const int tid = threadIdx.x, lane = tid & 63, G = lane >> 4, c = (lane >> 2) & 3;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int split = blockIdx.x % a.ksplits;
-    const int64_t unit = blockIdx.x / a.ksplits;
-    // `each`: a block for every row, which works if it is the first of its
-    // adapter among its group; otherwise one for every group.
-    const int64_t r0 = each ? unit / group * group : unit * group;
-    const int count = (int)min<int64_t>(group, a.m - r0);
-    const int ids = lane < count ? a.ids[r0 + lane] : -1;
-    uint64_t left = __ballot(ids >= 0 && ids < a.adapters);
-    if (each) {
-        const int u = (int)(unit - r0);
-        if (!(left >> u & 1)) return;
-        left &= __ballot(ids == __builtin_amdgcn_readlane(ids, u));
-        if (__builtin_ctzll(left) != u) return;
-    }
-    const int steps = (a.k + 31) / 32;
-    const int part = split * kLoraWaves + wave, parts = a.ksplits * kLoraWaves;
-    const int k0 = (int)((int64_t)steps * part / parts) * 32, k1 = min(a.k, (int)((int64_t)steps * (part + 1) / parts) * 32);
-    while (left) {
+    LoraRows r(a, blockIdx.x / a.ksplits, group, units);
+    const int steps = (a.k + 127) / 128, part = split * NW + wave, parts = a.ksplits * NW;
+    const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
+    while (r.left) {
         int id;
-        const uint64_t members = lora_members(left, ids, id);
+        const uint64_t members = lora_members(r.left, r.ids, id);
         const int rows = __popcll(members), places = lora_places(members);
-        for (int t = 0; t < rows; t += 16) {
-            const int64_t row = r0 + __shfl(places, min(t + i16, rows - 1));
-            f32x4v acc[RF];
-            lora_shrink<DT, RF>(a, a.x + row * a.ldx, a.a + id * a.a_stride, k0, k1, acc);
+        for (int t0 = 0; t0 < rows; t0 += 4 * XG) {
+            uint32_t xo[XG];
+            lora_x<XG>(a, places, t0, rows, xo);
+            for (int rank0 = 0; rank0 < a.rank; rank0 += 16 * RP) {
+                float v[XG][4 * RP];
+                lora_shrink<DT, XG, RP, U>(a, a.x + r.r0 * a.ldx, xo, a.a + id * a.a_stride, rank0, s0, s1, v);
+                if ((lane & 3) == 0) {
 #pragma unroll
-            for (int f = 0; f < RF; ++f) red[wave][f][lane] = acc[f];
-            __syncthreads();
-            for (int f = wave; f < RF; f += kLoraWaves) {
-                f32x4v sum = red[0][f][lane];
+                    for (int g = 0; g < XG; ++g)
 #pragma unroll
-                for (int w = 1; w < kLoraWaves; ++w) sum = sum + red[w][f][lane];
-                if (t + i16 < rows) *reinterpret_cast<f32x4v*>(a.v + ((int64_t)split * a.m + row) * a.vstride + 16 * f + 4 * G) = sum;
+                        for (int q = 0; q < 4 * RP; ++q) red[wave][4 * g + c][4 * q + G] = v[g][q];
+                }
+                __syncthreads();
+                for (int e = tid; e < 4 * XG * 16 * RP; e += 64 * NW) {
+                    const int i = e / (16 * RP), rr = e % (16 * RP);
+                    float sum = red[0][i][rr];
+#pragma unroll
+                    for (int x = 1; x < NW; ++x) sum = sum + red[x][i][rr];
+                    const int row = __shfl(places, min(t0 + i, rows - 1));
+                    if (t0 + i < rows && rank0 + rr < a.rank) a.v[((int64_t)split * a.m + r.r0 + row) * a.vstride + rank0 + rr] = sum;
+                }
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
 }
 
-// 16 columns of a row, from c on: out = y + d.
+// A lane's 16 of 64 columns of a row of y, from c on: the 16-byte pieces G, G + 4
+// and so on.
 template <int OUT>
-__device__ __forceinline__ void lora_store(const LoraArgs& a, int64_t row, int c, const float (&d)[16])
-{
-    constexpr int E = OUT == CK_OUT_FP32 ? 4 : 8;
-    constexpr int T = OUT == CK_OUT_FP16 ? CK_DT_FP16 : CK_DT_BF16;
-    if (a.wide && c + 16 <= a.n) {
-        const v4i* const yp = reinterpret_cast<const v4i*>(static_cast<const char*>(a.y) + (row * a.ldy + c) * (16 / E));
-        v4i* const op = reinterpret_cast<v4i*>(static_cast<char*>(a.out) + (row * a.ldo + c) * (16 / E));
-        v4i y[16 / E];
+struct LoraRow {
+    static constexpr int E = OUT == CK_OUT_FP32 ? 4 : 8;     // columns of a piece
+    static constexpr int T = OUT == CK_OUT_FP16 ? CK_DT_FP16 : CK_DT_BF16;
+    v4i y[16 / E];
+
+    __device__ __forceinline__ void load(const LoraArgs& a, bool wide, int64_t row, int c, int G)
+    {
+        const char* const yp = static_cast<const char*>(a.y) + (row * a.ldy + c + G * E) * (16 / E);
+        if (wide) {
 #pragma unroll
-        for (int j = 0; j < 16 / E; ++j) y[j] = yp[j];
+            for (int j = 0; j < 16 / E; ++j) y[j] = *reinterpret_cast<const v4i*>(yp + 64 * j);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 16 / E; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = c + (4 * j + G) * E + i * (E / 4);
+                uint32_t w = 0;
+                if constexpr (OUT == CK_OUT_FP32) {
+                    if (col < a.n) w = *reinterpret_cast<const uint32_t*>(yp + 64 * j + 4 * i);
+                } else {
+                    if (col < a.n) w = *reinterpret_cast<const uint16_t*>(yp + 64 * j + 4 * i);
+                    if (col + 1 < a.n) w |= (uint32_t)*reinterpret_cast<const uint16_t*>(yp + 64 * j + 4 * i + 2) << 16;
+                }
+                y[j][i] = (int)w;
+            }
+    }
+    // out = y + d scale
+    __device__ __forceinline__ void store(const LoraArgs& a, bool wide, int64_t row, int c, int G, const f32x4v (&d)[4], float up)
+    {
+        char* const op = static_cast<char*>(a.out) + (row * a.ldo + c + G * E) * (16 / E);
 #pragma unroll
         for (int j = 0; j < 16 / E; ++j) {
             v4i o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (OUT == CK_OUT_FP32) {
-                    o[i] = __float_as_int(__int_as_float(y[j][i]) + d[4 * j + i]);
+                    o[i] = __float_as_int(__int_as_float(y[j][i]) + d[j][i] * up);
                 } else {
                     const float2 f = widen2<T>((uint32_t)y[j][i]);
-                    o[i] = (int)narrow2<T>(f.x + d[8 * j + 2 * i], f.y + d[8 * j + 2 * i + 1]);
+                    o[i] = (int)narrow2<T>(f.x + d[2 * j + i / 2][i % 2 * 2] * up, f.y + d[2 * j + i / 2][i % 2 * 2 + 1] * up);
                 }
             }
-            op[j] = o;
-        }
-        return;
-    }
+            if (wide) {
+                *reinterpret_cast<v4i*>(op + 64 * j) = o;
+                continue;
+            }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if (c + i >= a.n) break;
-        const int64_t yi = row * a.ldy + c + i, oi = row * a.ldo + c + i;
-        if constexpr (OUT == CK_OUT_FP32)
-            static_cast<float*>(a.out)[oi] = static_cast<const float*>(a.y)[yi] + d[i];
-        else
-            static_cast<uint16_t*>(a.out)[oi] =
-                (uint16_t)narrow2<T>(widen2<T>((uint32_t) static_cast<const uint16_t*>(a.y)[yi]).x + d[i], 0.0f);
+            for (int i = 0; i < 4; ++i) {
+                const int col = c + (4 * j + G) * E + i * (E / 4);
+                if constexpr (OUT == CK_OUT_FP32) {
+                    if (col < a.n) *reinterpret_cast<int*>(op + 64 * j + 4 * i) = o[i];
+                } else {
+                    if (col < a.n) *reinterpret_cast<uint16_t*>(op + 64 * j + 4 * i) = (uint16_t)o[i];
+                    if (col + 1 < a.n) *reinterpret_cast<uint16_t*>(op + 64 * j + 4 * i + 2) = (uint16_t)((uint32_t)o[i] >> 16);
+                }
+            }
+        }
     }
-}
+};
 
-// The second product for MB blocks of 16 rows, or all of it (RF > 0: v is made
-// here).  A wave has 64 columns at a time, as four tiles: tile t's operand row
-// p is column 16 (p / 4) + 4 t + p % 4, so that lane 16 G + i ends up with 16
-// columns in a row, 16 G and on, of row i.
-template <int DT, int MB, int RF>
-__global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs a, int each)
+// The second product, or all of it (RF > 0: v is made here), for up to `blocks`
+// blocks of 16 rows at a time.  A wave has 64 columns at a time, as four tiles
+// whose operand rows are such columns that lane 16 G + i ends up with whole
+// 16-byte pieces of row i, G and every fourth one on: a load or store of y has 64
+// bytes of each row.
+template <int DT, int OUT, int RF, int PR>
+__global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_expand_kernel(LoraArgs a, int units, int blocks)
 {
-    constexpr int PARTS = DT == CK_DT_FP16 ? 2 : 3;
+    constexpr int PARTS = DT == CK_DT_FP16 ? 2 : 3, NW = RF > 0 ? 8 : 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, G = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slice = blockIdx.x % a.slices;
-    const int64_t unit = blockIdx.x / a.slices, r0 = each ? unit / 64 * 64 : unit * 64;
-    const int count = (int)min<int64_t>(64, a.m - r0);
-    const int chunks = (a.n + 63) / 64;
-    const int c0 = (int)((int64_t)chunks * slice / a.slices), c1 = (int)((int64_t)chunks * (slice + 1) / a.slices);
-    const int ids = lane < count ? a.ids[r0 + lane] : -1;
-    const uint64_t having = __ballot(ids >= 0 && ids < a.adapters);
-    uint64_t left = having, without = (count == 64 ? ~0ull : (1ull << count) - 1) & ~having;
-    if (each) {
-        const int u = (int)(unit - r0);
-        without &= 1ull << u;
-        left &= __ballot(ids == __builtin_amdgcn_readlane(ids, u));
-        if (left && __builtin_ctzll(left) != u) left = 0;
-    }
+    const int c0 = slice * a.slice, c1 = min(a.n, c0 + a.slice);
+    LoraRows r(a, blockIdx.x / a.slices, 64, units);
     if (a.copy) {                                            // rows without an adapter, as they are
-        const int esz = a.out_dtype == CK_OUT_FP32 ? 4 : 2;
-        for (; without; without &= without - 1) {
-            const int64_t row = r0 + __builtin_ctzll(without);
-            const char* const yp = static_cast<const char*>(a.y) + row * a.ldy * esz;
-            char* const op = static_cast<char*>(a.out) + row * a.ldo * esz;
-            const int end = min(a.n, c1 * 64);
-            for (int c = c0 * 64 + tid; c < end; c += 64 * kLoraWaves) {
-                if (esz == 4) reinterpret_cast<uint32_t*>(op)[c] = reinterpret_cast<const uint32_t*>(yp)[c];
-                else reinterpret_cast<uint16_t*>(op)[c] = reinterpret_cast<const uint16_t*>(yp)[c];
+        for (; r.without; r.without &= r.without - 1) {
+            const int64_t row = r.r0 + __builtin_ctzll(r.without);
+            for (int c = c0 + tid; c < c1; c += 64 * NW) {
+                if constexpr (OUT == CK_OUT_FP32) static_cast<uint32_t*>(a.out)[row * a.ldo + c] = static_cast<const uint32_t*>(a.y)[row * a.ldy + c];
+                else static_cast<uint16_t*>(a.out)[row * a.ldo + c] = static_cast<const uint16_t*>(a.y)[row * a.ldy + c];
             }
         }
     }
     const int steps = (a.rank + 31) / 32, vs = 32 * steps + 4;       // of the second product's sum; floats of a row of v
-    v4i* const frags = reinterpret_cast<v4i*>(lds);                  // [MB][PARTS][steps][64]
-    float* const v = reinterpret_cast<float*>(frags + MB * PARTS * steps * 64);   // [16 MB][vs]
-    float* const back = v + 16 * MB * vs;                            // [16 MB] powers of two that v was divided by
-    while (left) {
+    v4i* const frags = reinterpret_cast<v4i*>(lds);                  // [blocks][PARTS][steps][64]
+    float* const v = reinterpret_cast<float*>(frags + blocks * PARTS * steps * 64);   // [16 blocks][vs]
+    float* const back = v + 16 * blocks * vs;                        // [16 blocks] powers of two that v was divided by
+    // B of 64 columns comes in 16-byte pieces in their order, up to 8 PR ranks at
+    // a time, and goes through this wave's part of LDS into the operands' order
+    // (rows an odd number of pieces apart).
+    v4i* const turn = reinterpret_cast<v4i*>(lds + a.turn) + wave * 64 * (PR | 1);
+    int cols[4];                                             // the column of this lane's operand row of each tile, of 64
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        cols[t] = OUT == CK_OUT_FP32 ? 16 * t + i16 : 32 * (t >> 1) + 8 * (i16 >> 2) + 4 * (t & 1) + (i16 & 3);
+    while (r.left) {
         int id;
-        const uint64_t members = lora_members(left, ids, id);
+        const uint64_t members = lora_members(r.left, r.ids, id);
         const int rows = __popcll(members), places = lora_places(members);
         const float scale = a.scale ? a.scale[id] : 1.0f;
         const uint16_t* const bp = a.b + id * a.b_stride;
-        for (int t0 = 0; t0 < rows; t0 += 16 * MB) {
-            const int here = min(16 * MB, rows - t0);
-            int64_t row[MB];                                 // this lane's of each block; the last one again past the end
+        // pieces of ranks 8 PR h and on of columns c and on
+        const int prow = lane / PR, piece = lane % PR;
+        auto load_b = [&](v4i (&w)[PR], int c, int h) {
+            if (8 * (PR * h + piece) >= a.rank) return;
+            const uint16_t* const from = bp + 8 * (PR * h + piece);
+            if (c + 64 <= a.n) {
+                const uint16_t* const at = from + (int64_t)(c + prow) * a.rank;
 #pragma unroll
-            for (int b = 0; b < MB; ++b) row[b] = r0 + __shfl(places, min(t0 + 16 * b + i16, rows - 1));
+                for (int j = 0; j < PR; ++j) w[j] = *reinterpret_cast<const v4i*>(at + j * (64 / PR) * a.rank);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PR; ++j)
+                    w[j] = *reinterpret_cast<const v4i*>(from + (int64_t)min(c + j * (64 / PR) + prow, a.n - 1) * a.rank);
+            }
+        };
+        auto turn_b = [&](const v4i (&w)[PR]) {
+#pragma unroll
+            for (int j = 0; j < PR; ++j) turn[(j * (64 / PR) + prow) * (PR | 1) + piece] = w[j];
+        };
+        v4i w[PR];
+#pragma unroll
+        for (int j = 0; j < PR; ++j) w[j] = v4i{0, 0, 0, 0};
+        load_b(w, c0 + wave * 64, 0);                        // on its way while v is made
+        for (int t0 = 0; t0 < rows; t0 += 16 * blocks) {
+            const int here = min(16 * blocks, rows - t0);
             // v, fp32, with the adapter's scale; ranks past the last are zero
             if constexpr (RF > 0) {
-                f32x4v* const red = reinterpret_cast<f32x4v*>(back + 16 * MB);   // [waves][RF][64]
-                const int part = wave, all = (a.k + 31) / 32;
-                const int k0 = all * part / kLoraWaves * 32, k1 = min(a.k, all * (part + 1) / kLoraWaves * 32);
-                f32x4v acc[RF];
-                lora_shrink<DT, RF>(a, a.x + row[0] * a.ldx, a.a + id * a.a_stride, k0, k1, acc);
+                float* const red = back + 16;                // [waves][16 rows][16 RF ranks + 4]
+                constexpr int RS = 16 * RF + 4;
+                const int all = (a.k + 127) / 128, s0 = all * wave / NW, s1 = all * (wave + 1) / NW, cc = (lane >> 2) & 3;
+                for (int g0 = 0; g0 < here; g0 += 4) {
+                    uint32_t xo[1];
+                    lora_x<1>(a, places, t0 + g0, rows, xo);
+                    float part[1][4 * RF];
+                    lora_shrink<DT, 1, RF, 4 / RF>(a, a.x + r.r0 * a.ldx, xo, a.a + id * a.a_stride, 0, s0, s1, part);
+                    if ((lane & 3) == 0) {
 #pragma unroll
-                for (int f = 0; f < RF; ++f) red[(wave * RF + f) * 64 + lane] = acc[f];
-                for (int i = tid; i < 16 * vs; i += 64 * kLoraWaves) v[i] = 0.0f;
-                __syncthreads();
-                if (wave < RF) {
-                    f32x4v sum = red[wave * 64 + lane];
-#pragma unroll
-                    for (int w = 1; w < kLoraWaves; ++w) sum = sum + red[(w * RF + wave) * 64 + lane];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (i16 < here && 16 * wave + 4 * G + r < a.rank) v[i16 * vs + 16 * wave + 4 * G + r] = sum[r] * scale;
+                        for (int q = 0; q < 4 * RF; ++q) red[(wave * 16 + g0 + cc) * RS + 4 * q + G] = part[0][q];
+                    }
                 }
+                __syncthreads();
+                const int i = tid >> 5, rr = tid & 31;       // 512 threads, 16 rows of 32 ranks
+                float sum = 0.0f;
+                if (i < here && rr < a.rank) {
+                    sum = red[i * RS + rr];
+#pragma unroll
+                    for (int x = 1; x < NW; ++x) sum = sum + red[(x * 16 + i) * RS + rr];
+                }
+                v[i * vs + rr] = sum * scale;
             } else {
-                for (int e = tid; e < 16 * MB * 32 * steps; e += 64 * kLoraWaves) {
-                    const int i = e / (32 * steps), r = e % (32 * steps);
-                    const int64_t at = r0 + __shfl(places, min(t0 + i, rows - 1));
+                for (int e = tid; e < 16 * blocks * 32 * steps; e += 64 * NW) {
+                    const int i = e / (32 * steps), rr = e % (32 * steps);
+                    const int64_t at = r.r0 + __shfl(places, min(t0 + i, rows - 1));
                     float sum = 0.0f;
-                    if (i < here && r < a.rank) {
-                        sum = a.v[at * a.vstride + r];
-                        for (int s = 1; s < a.ksplits; ++s) sum = sum + a.v[(s * a.m + at) * a.vstride + r];
+                    if (i < here && rr < a.rank) {
+                        const float* const p = a.v + at * a.vstride + rr;
+                        for (int s = 0; s < a.ksplits; s += 8) {     // (loads of eight parts go out together)
+                            float f[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) f[j] = s + j < a.ksplits ? p[(int64_t)(s + j) * a.m * a.vstride] : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) sum = sum + f[j];
+                        }
                         sum *= scale;
                     }
-                    v[i * vs + r] = sum;
+                    v[i * vs + rr] = sum;
                 }
             }
             __syncthreads();
-            // and its 16-bit parts, as the second product's second operand
-            for (int i = wave; i < 16 * MB; i += kLoraWaves) {
-                float top = 0.0f;
+            // and its 16-bit parts, as the second product's second operand (what
+            // the other rows' places hold is not used)
+            for (int i = wave; i < here; i += NW) {
+                int e = 0;
                 if constexpr (DT == CK_DT_FP16) {
-                    for (int r = lane; r < 32 * steps; r += 64) top = fmaxf(top, __builtin_fabsf(v[i * vs + r]));
+                    float top = 0.0f;
+                    for (int k = lane; k < 32 * steps; k += 64) top = fmaxf(top, __builtin_fabsf(v[i * vs + k]));
 #pragma unroll
                     for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+                    e = top > 0.0f && top < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
+                    if (lane == 0) back[i] = __builtin_amdgcn_ldexpf(1.0f, -e);
                 }
-                const int e = top > 0.0f && top < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-                if (lane == 0) back[i] = __builtin_amdgcn_ldexpf(1.0f, -e);
-                for (int r = 2 * lane; r < 32 * steps; r += 128) {
-                    float x = __builtin_amdgcn_ldexpf(v[i * vs + r], e), z = __builtin_amdgcn_ldexpf(v[i * vs + r + 1], e);
-                    uint32_t* const to = reinterpret_cast<uint32_t*>(frags + (i / 16 * PARTS * steps + r / 32) * 64 + r / 8 % 4 * 16 + i % 16) + r % 8 / 2;
+                for (int k = 2 * lane; k < 32 * steps; k += 128) {
+                    float x = __builtin_amdgcn_ldexpf(v[i * vs + k], e), z = __builtin_amdgcn_ldexpf(v[i * vs + k + 1], e);
+                    uint32_t* const to = reinterpret_cast<uint32_t*>(frags + (i / 16 * PARTS * steps + k / 32) * 64 + k / 8 % 4 * 16 + i % 16) + k % 8 / 2;
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) {
                         const uint32_t h = narrow2<DT>(x, z);
@@ -281,41 +414,49 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs a
                 }
             }
             __syncthreads();
-            for (int c = (c0 + wave) * 64; c < c1 * 64; c += 64 * kLoraWaves) {
-                f32x4v acc[MB][4];
-#pragma unroll
-                for (int b = 0; b < MB; ++b)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[b][t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-                for (int s = 0; s < steps; ++s) {
-                    v4i w[4];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int col = min(c + 16 * (i16 >> 2) + 4 * t + (i16 & 3), a.n - 1);
-                        w[t] = 32 * s + 8 * G < a.rank ? *reinterpret_cast<const v4i*>(bp + (int64_t)col * a.rank + 32 * s + 8 * G)
-                                                       : v4i{0, 0, 0, 0};
-                    }
-#pragma unroll
-                    for (int b = 0; b < MB; ++b)
-#pragma unroll
-                        for (int p = 0; p < PARTS; ++p) {
-                            const v4i f = frags[((b * PARTS + p) * steps + s) * 64 + lane];
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) acc[b][t] = mfma16<DT>(w[t], f, acc[b][t]);
-                        }
+            for (int c = c0 + wave * 64; c < c1; c += 64 * NW) {
+                // the columns that follow, or the first ones again for the next rows
+                const int next = c + 64 * NW < c1 ? c + 64 * NW : c0 + wave * 64;
+                const bool wide = a.wide && c + 64 <= a.n;
+                const int groups = (a.rank + 8 * PR - 1) / (8 * PR);
+                if (groups == 1) {
+                    turn_b(w);
+                    load_b(w, next, 0);
                 }
+#pragma unroll 1
+                for (int b = 0; 16 * b < here; ++b) {
+                    const int place = t0 + 16 * b + i16;
+                    const int64_t row = r.r0 + __shfl(places, min(place, rows - 1));
+                    LoraRow<OUT> io;
+                    if (place < rows) io.load(a, wide, row, c, G);
+                    f32x4v acc[4];
 #pragma unroll
-                for (int b = 0; b < MB; ++b) {
-                    if (16 * b + i16 >= here) continue;
-                    const float up = DT == CK_DT_FP16 ? back[16 * b + i16] : 1.0f;
-                    float d[16];
+                    for (int t = 0; t < 4; ++t) acc[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int h = 0; h < groups; ++h) {
+                        if (groups > 1) {
+                            turn_b(w);
+                            load_b(w, h + 1 < groups || 16 * (b + 1) < here ? c : next, h + 1 < groups ? h + 1 : 0);
+                        }
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                        for (int s = 0; s < (PR + 3) / 4; ++s) {
+                            const int k = PR * h + 4 * s;        // pieces before
+                            if (8 * k >= a.rank) break;
+                            const bool in = 8 * (k + G) < a.rank;
+                            v4i f[4];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) d[4 * t + r] = acc[b][t][r] * up;
-                    if (a.out_dtype == CK_OUT_FP32) lora_store<CK_OUT_FP32>(a, row[b], c + 16 * G, d);
-                    else if (a.out_dtype == CK_OUT_FP16) lora_store<CK_OUT_FP16>(a, row[b], c + 16 * G, d);
-                    else lora_store<CK_OUT_BF16>(a, row[b], c + 16 * G, d);
+                            for (int t = 0; t < 4; ++t) {
+                                f[t] = turn[cols[t] * (PR | 1) + (in ? 4 * s + G : 0)];
+                                if (!in) f[t] = v4i{0, 0, 0, 0};
+                            }
+#pragma unroll
+                            for (int p = 0; p < PARTS; ++p) {
+                                const v4i y = frags[((b * PARTS + p) * steps + k / 4) * 64 + lane];
+#pragma unroll
+                                for (int t = 0; t < 4; ++t) acc[t] = mfma16<DT>(f[t], y, acc[t]);
+                            }
+                        }
+                    }
+                    if (place < rows) io.store(a, wide, row, c, G, acc, DT == CK_DT_FP16 ? back[16 * b + i16] : 1.0f);
                 }
             }
             __syncthreads();
@@ -332,43 +473,52 @@ bool lora_sizes_ok(int64_t m, int64_t n, int64_t k, int64_t rank)
 }
 
 struct LoraPlan {
-    bool each, fused;
-    int mb;                                                  // row blocks of the second product
-    int64_t group, ksplits, vstride, bytes;                  // of the first launch: rows of a block, parts of k
+    bool each, fused;                                        // an adapter a block; one launch
+    int blocks;                                              // row blocks that the second product has in LDS
+    int64_t group, ksplits, bytes;                           // of the first launch: rows of a block, parts of k
 };
 
 LoraPlan lora_plan(int64_t m, int64_t n, int64_t k, int64_t rank)
 {
     LoraPlan p{};
     p.each = m <= kLoraRows;
-    p.fused = p.each && rank <= 32 && rank * k <= 131072;
-    p.mb = p.each || rank > 64 ? 1 : 4;                      // within 64 KiB of LDS
-    p.vstride = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : rank <= 128 ? 128 : 256;   // 16 RF of the first launch
+    p.fused = p.each && rank <= 32 && rank * k <= 131072 && m <= 8;
+    p.blocks = p.fused || rank > 128 ? 1 : rank > 64 ? 2 : 4;    // within 64 KiB
     p.group = p.each ? 64 : 16;
     const int64_t units = p.each ? std::min<int64_t>(m, 16) : cdiv(m, p.group);
-    p.ksplits = std::max<int64_t>(1, std::min<int64_t>(cdiv(kNumCUs, std::max<int64_t>(units, 1)), k / (64 * kLoraWaves)));
-    if (!p.fused) p.bytes = p.ksplits * m * p.vstride * 4;
+    p.ksplits = std::max<int64_t>(1, std::min<int64_t>(cdiv(kNumCUs, std::max<int64_t>(units, 1)), k / (128 * kLoraWaves)));
+    if (!p.fused) p.bytes = p.ksplits * m * rank * 4;
     return p;
 }
 
 template <int DT>
-const void* lora_shrink_fn(int64_t rank)
+const void* lora_shrink_fn(bool each, int64_t rank)
 {
-    return rank <= 16   ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1>)
-           : rank <= 32 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 2>)
-           : rank <= 64 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4>)
-           : rank <= 128 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 8>)
-                         : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 16>);
+    if (each)
+        return rank <= 16   ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1, 1>)
+               : rank <= 32 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1, 2>)
+                            : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1, 4>);
+    return rank <= 16 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4, 1>)
+                      : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4, 2>);
+}
+
+template <int DT, int OUT>
+const void* lora_expand_out(bool fused, int64_t rank)
+{
+    if (fused)
+        return rank <= 16 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 1, 2>)
+                          : reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 2, 4>);
+    return rank <= 16   ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 0, 2>)
+           : rank <= 32 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 0, 4>)
+                        : reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 0, 8>);
 }
 
 template <int DT>
-const void* lora_expand_fn(const LoraPlan& p, int64_t rank)
+const void* lora_expand_fn(int out_dtype, bool fused, int64_t rank)
 {
-    if (p.fused)
-        return rank <= 16 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, 1, 1>)
-                          : reinterpret_cast<const void*>(&lora_expand_kernel<DT, 1, 2>);
-    return p.mb == 1 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, 1, 0>)
-                  : reinterpret_cast<const void*>(&lora_expand_kernel<DT, 4, 0>);
+    return out_dtype == CK_OUT_FP32   ? lora_expand_out<DT, CK_OUT_FP32>(fused, rank)
+           : out_dtype == CK_OUT_FP16 ? lora_expand_out<DT, CK_OUT_FP16>(fused, rank)
+                                      : lora_expand_out<DT, CK_OUT_BF16>(fused, rank);
 }
 
 }  // namespace
@@ -402,6 +552,8 @@ extern "C" ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream)
             !aligned(p.x, 16) || !aligned(p.a, 16) || !aligned(p.b, 16))
             return fail(CK_ERR_UNSUPPORTED, "rows of x and adapters must start 16 bytes apart");
     }
+    if (p.adapters > 0 && p.k > 0 && p.m > 1 && p.ldx > (1 << 24) + 128)
+        return fail(CK_ERR_UNSUPPORTED, "rows of x too far apart for 32-bit offsets");
     const int esz = p.out_dtype == CK_OUT_FP32 ? 4 : 2;
     if (!aligned(p.y, esz) || !aligned(p.out, esz) || !aligned(p.ids, 4) || !aligned(p.scale, 4))
         return fail(CK_ERR_UNSUPPORTED, "misaligned y, out, ids or scale");
@@ -413,26 +565,31 @@ extern "C" ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream)
     if (s != CK_OK) return s;
     LoraArgs a{(const uint16_t*)p.x, (const uint16_t*)p.a, (const uint16_t*)p.b, p.scale, p.ids, p.y, p.out, (float*)p.workspace,
                p.ldx, p.ldy, p.ldo, p.a_stride, p.b_stride, p.m, (int)p.n, (int)p.k, (int)p.rank,
-               (int)(p.k > 0 ? p.adapters : 0), p.out_dtype, (int)plan.vstride, (int)plan.ksplits, 1, p.out != p.y, 0};
+               (int)(p.k > 0 ? p.adapters : 0), (int)p.rank, (int)plan.ksplits, 1, 0, 0, p.out != p.y, 0};
     a.wide = aligned(p.y, 16) && aligned(p.out, 16) && p.ldy * esz % 16 == 0 && p.ldo * esz % 16 == 0;
     const bool f16 = p.dtype == CK_DT_FP16;
-    int group = (int)plan.group, each = plan.each;
+    // As many blocks for 64 rows as they can have adapters, or one.
+    int group = (int)plan.group, units = plan.each ? (int)std::max<int64_t>(1, std::min(std::min<int64_t>(64, p.m), p.adapters)) : 0;
+    const int64_t per64 = cdiv(p.m, 64) * std::max(units, 1);
     if (!plan.fused && a.adapters > 0) {
-        void* kargs[] = {&a, &group, &each};
-        const int64_t blocks = (plan.each ? p.m : cdiv(p.m, plan.group)) * plan.ksplits;
-        const void* fn = f16 ? lora_shrink_fn<CK_DT_FP16>(p.rank) : lora_shrink_fn<CK_DT_BF16>(p.rank);
+        void* kargs[] = {&a, &group, &units};
+        const int64_t blocks = (plan.each ? per64 : cdiv(p.m, plan.group)) * plan.ksplits;
+        const void* fn = f16 ? lora_shrink_fn<CK_DT_FP16>(plan.each, p.rank) : lora_shrink_fn<CK_DT_BF16>(plan.each, p.rank);
         if ((s = launch(fn, (unsigned)blocks, 64 * kLoraWaves, kargs, stream, "lora_shrink")) != CK_OK) return s;
     }
-    // Column slices: as many blocks as give every CU two, of 512 columns at least.
-    const int64_t units = plan.each ? std::min(p.m, std::max<int64_t>(p.adapters, 1)) : cdiv(p.m, 64);
-    a.slices = (int)std::max<int64_t>(1, std::min(cdiv(2 * kNumCUs, units), cdiv(p.n, 64 * kLoraWaves)));
-    const int mb = plan.mb, parts = f16 ? 2 : 3;
-    const int64_t steps = cdiv(p.rank, 32), rf = plan.fused ? cdiv(p.rank, 16) : 0;
-    const size_t lds = mb * parts * steps * 1024 + 16 * mb * (32 * steps + 4) * 4 + 64 * mb + kLoraWaves * rf * 1024;
-    const void* fn = f16 ? lora_expand_fn<CK_DT_FP16>(plan, p.rank) : lora_expand_fn<CK_DT_BF16>(plan, p.rank);
-    void* kargs[] = {&a, &each};
-    const int64_t blocks = (plan.each ? p.m : cdiv(p.m, 64)) * a.slices;
-    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * kLoraWaves), kargs, lds, stream);
+    // Column slices, of whole rounds of a block's waves: as many blocks as give every CU two.
+    const int64_t waves = plan.fused ? 8 : 4;
+    const int64_t turns = cdiv(p.n, 64 * waves);             // of all columns
+    a.slice = (int)(cdiv(turns, std::min(cdiv((plan.fused ? 2 : 3) * kNumCUs, per64), turns)) * 64 * waves);
+    a.slices = (int)cdiv(p.n, a.slice);
+    int held = plan.blocks;
+    const int64_t parts = f16 ? 2 : 3, steps = cdiv(p.rank, 32), rf = plan.fused ? cdiv(p.rank, 16) : 0;
+    a.turn = (int)(cdiv(held * parts * steps * 1024 + 16 * held * (32 * steps + 4) * 4 + 64 * held + (rf ? waves * 64 * (16 * rf + 4) : 0), 16) * 16);
+    const size_t lds = a.turn + waves * 64 * 16 * ((p.rank <= 16 ? 2 : p.rank <= 32 ? 4 : 8) + 1);
+    const void* fn = f16 ? lora_expand_fn<CK_DT_FP16>(p.out_dtype, plan.fused, p.rank) : lora_expand_fn<CK_DT_BF16>(p.out_dtype, plan.fused, p.rank);
+    void* kargs[] = {&a, &units, &held};
+    const int64_t blocks = per64 * a.slices;
+    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * (unsigned)waves), kargs, lds, stream);
     if (e != hipSuccess) return fail(CK_ERR_HIP, "lora_add launch: %s", hipGetErrorString(e));
     return ok();
 }
