@@ -121,35 +121,36 @@ __device__ __forceinline__ void lora_shrink(const LoraArgs& a, const uint16_t* x
     for (int g = 0; g < XG; ++g)
 #pragma unroll
         for (int q = 0; q < 4 * RP; ++q) acc[g][q] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = s0; s < s1; s += U) {
-        v4i xs[U][XG], ws[U][4 * RP];
-        // past the end: the last piece of the row again, then zeros
-        const bool whole = s + U <= s1 && (s + U) * 128 <= a.k;
+    auto run = [&](int s, auto count, auto whole) {
+        constexpr int N = decltype(count)::value;
+        v4i xs[N][XG], ws[N][4 * RP];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t c = (s + u) * 256, off = whole ? c : min(c + 2 * at, (uint32_t)(2 * a.k - 16)) - 2 * at;
+        for (int u = 0; u < N; ++u) {
+            // past the end: the last piece of the row again, then zeros
+            const uint32_t c = (s + u) * 256, off = whole.value ? c : min(c + 2 * at, (uint32_t)(2 * a.k - 16)) - 2 * at;
 #pragma unroll
             for (int g = 0; g < XG; ++g) xs[u][g] = *reinterpret_cast<const v4i*>(x + (xo[g] + off));
 #pragma unroll
             for (int q = 0; q < 4 * RP; ++q) ws[u][q] = *reinterpret_cast<const v4i*>(w[q] + (wo + off));
-        }
-        if (!whole) {
+            if (!whole.value && (s + u) * 128 + at >= a.k) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (s + u >= s1 || (s + u) * 128 + at >= a.k) {
+                for (int g = 0; g < XG; ++g) xs[u][g] = v4i{0, 0, 0, 0};
 #pragma unroll
-                    for (int g = 0; g < XG; ++g) xs[u][g] = v4i{0, 0, 0, 0};
-#pragma unroll
-                    for (int q = 0; q < 4 * RP; ++q) ws[u][q] = v4i{0, 0, 0, 0};
-                }
+                for (int q = 0; q < 4 * RP; ++q) ws[u][q] = v4i{0, 0, 0, 0};
+            }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < N; ++u)
 #pragma unroll
             for (int q = 0; q < 4 * RP; ++q)
 #pragma unroll
                 for (int g = 0; g < XG; ++g) acc[g][q] = mfma16<DT>(ws[u][q], xs[u][g], acc[g][q]);
-    }
+    };
+    const int full = min(s1, a.k / 128);
+    int s = s0;
+    for (; s + U <= full; s += U) run(s, IntTag<U>{}, BoolTag<true>{});
+    for (; s < full; ++s) run(s, IntTag<1>{}, BoolTag<true>{});
+    if (s < s1) run(s, IntTag<1>{}, BoolTag<false>{});
 #pragma unroll
     for (int g = 0; g < XG; ++g)
 #pragma unroll
@@ -212,68 +213,44 @@ __global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArg
     }
 }
 
-// A lane's 16 of 64 columns of a row of y, from c on: the 16-byte pieces G, G + 4
-// and so on.
+// A lane's 16 of 64 columns of a row of y: the 16-byte pieces G, G + 4 and so on,
+// at `off` and every 64 bytes on.
 template <int OUT>
 struct LoraRow {
-    static constexpr int E = OUT == CK_OUT_FP32 ? 4 : 8;     // columns of a piece
+    static constexpr int E = OUT == CK_OUT_FP32 ? 4 : 8, B = 16 / E;         // columns of a piece, bytes of a column
     static constexpr int T = OUT == CK_OUT_FP16 ? CK_DT_FP16 : CK_DT_BF16;
-    v4i y[16 / E];
+    v4i y[B];
 
-    __device__ __forceinline__ void load(const LoraArgs& a, bool wide, int64_t row, int c, int G)
+    __device__ __forceinline__ void load(const char* base, uint32_t off)
     {
-        const char* const yp = static_cast<const char*>(a.y) + (row * a.ldy + c + G * E) * (16 / E);
-        if (wide) {
 #pragma unroll
-            for (int j = 0; j < 16 / E; ++j) y[j] = *reinterpret_cast<const v4i*>(yp + 64 * j);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < 16 / E; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = c + (4 * j + G) * E + i * (E / 4);
-                uint32_t w = 0;
-                if constexpr (OUT == CK_OUT_FP32) {
-                    if (col < a.n) w = *reinterpret_cast<const uint32_t*>(yp + 64 * j + 4 * i);
-                } else {
-                    if (col < a.n) w = *reinterpret_cast<const uint16_t*>(yp + 64 * j + 4 * i);
-                    if (col + 1 < a.n) w |= (uint32_t)*reinterpret_cast<const uint16_t*>(yp + 64 * j + 4 * i + 2) << 16;
-                }
-                y[j][i] = (int)w;
-            }
+        for (int j = 0; j < B; ++j) y[j] = *reinterpret_cast<const v4i*>(base + (off + 64 * j));
     }
-    // out = y + d scale
-    __device__ __forceinline__ void store(const LoraArgs& a, bool wide, int64_t row, int c, int G, const f32x4v (&d)[4], float up)
+    // out = y + d
+    __device__ __forceinline__ void store(char* base, uint32_t off, const f32x4v (&d)[4])
     {
-        char* const op = static_cast<char*>(a.out) + (row * a.ldo + c + G * E) * (16 / E);
 #pragma unroll
-        for (int j = 0; j < 16 / E; ++j) {
+        for (int j = 0; j < B; ++j) {
             v4i o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (OUT == CK_OUT_FP32) {
-                    o[i] = __float_as_int(__int_as_float(y[j][i]) + d[j][i] * up);
+                    o[i] = __float_as_int(__int_as_float(y[j][i]) + d[j][i]);
                 } else {
                     const float2 f = widen2<T>((uint32_t)y[j][i]);
-                    o[i] = (int)narrow2<T>(f.x + d[2 * j + i / 2][i % 2 * 2] * up, f.y + d[2 * j + i / 2][i % 2 * 2 + 1] * up);
+                    o[i] = (int)narrow2<T>(f.x + d[2 * j + i / 2][i % 2 * 2], f.y + d[2 * j + i / 2][i % 2 * 2 + 1]);
                 }
             }
-            if (wide) {
-                *reinterpret_cast<v4i*>(op + 64 * j) = o;
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = c + (4 * j + G) * E + i * (E / 4);
-                if constexpr (OUT == CK_OUT_FP32) {
-                    if (col < a.n) *reinterpret_cast<int*>(op + 64 * j + 4 * i) = o[i];
-                } else {
-                    if (col < a.n) *reinterpret_cast<uint16_t*>(op + 64 * j + 4 * i) = (uint16_t)o[i];
-                    if (col + 1 < a.n) *reinterpret_cast<uint16_t*>(op + 64 * j + 4 * i + 2) = (uint16_t)((uint32_t)o[i] >> 16);
-                }
-            }
+            *reinterpret_cast<v4i*>(base + (off + 64 * j)) = o;
         }
+    }
+    // One column.
+    __device__ static __forceinline__ void add(const char* y, char* out, float d)
+    {
+        if constexpr (OUT == CK_OUT_FP32)
+            *reinterpret_cast<float*>(out) = *reinterpret_cast<const float*>(y) + d;
+        else
+            *reinterpret_cast<uint16_t*>(out) = (uint16_t)narrow2<T>(widen2<T>(*reinterpret_cast<const uint16_t*>(y)).x + d, 0.0f);
     }
 };
 
@@ -301,14 +278,28 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
             }
         }
     }
-    const int steps = (a.rank + 31) / 32, vs = 32 * steps + 4;       // of the second product's sum; floats of a row of v
-    v4i* const frags = reinterpret_cast<v4i*>(lds);                  // [blocks][PARTS][steps][64]
-    float* const v = reinterpret_cast<float*>(frags + blocks * PARTS * steps * 64);   // [16 blocks][vs]
-    float* const back = v + 16 * blocks * vs;                        // [16 blocks] powers of two that v was divided by
+    const int steps = (a.rank + 31) / 32;                    // of the second product's sum
+    v4i* const frags = reinterpret_cast<v4i*>(lds);          // [blocks][PARTS][steps][64]: v, its second operand
+    float* const back = reinterpret_cast<float*>(frags + blocks * PARTS * steps * 64);   // [16 blocks] powers of two that v was divided by
+    uint32_t* const tops = reinterpret_cast<uint32_t*>(back + 16 * blocks);              // [16 blocks] fp16: the rows' largest
+    // Two values of a row, of ranks k and k + 1 (k even), in their 16-bit parts.
+    auto put = [&](int i, int k, float x, float z) {
+        uint32_t* const to = reinterpret_cast<uint32_t*>(frags + (i / 16 * PARTS * steps + k / 32) * 64 + k / 8 % 4 * 16 + i % 16) + k % 8 / 2;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            const uint32_t h = narrow2<DT>(x, z);
+            const float2 f = widen2<DT>(h);
+            to[p * steps * 256] = h;
+            x -= f.x;
+            z -= f.y;
+        }
+    };
+    auto lift = [&](int i) { return 14 - __builtin_amdgcn_frexp_expf(__uint_as_float(tops[i])); };   // of a finite largest > 0
     // B of 64 columns comes in 16-byte pieces in their order, up to 8 PR ranks at
     // a time, and goes through this wave's part of LDS into the operands' order
     // (rows an odd number of pieces apart).
     v4i* const turn = reinterpret_cast<v4i*>(lds + a.turn) + wave * 64 * (PR | 1);
+    float* const line = reinterpret_cast<float*>(lds + a.turn + NW * 64 * (PR | 1) * 16) + wave * 64;
     int cols[4];                                             // the column of this lane's operand row of each tile, of 64
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -319,19 +310,18 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
         const int rows = __popcll(members), places = lora_places(members);
         const float scale = a.scale ? a.scale[id] : 1.0f;
         const uint16_t* const bp = a.b + id * a.b_stride;
+        const char* const yb = static_cast<const char*>(a.y) + r.r0 * a.ldy * LoraRow<OUT>::B;
+        char* const ob = static_cast<char*>(a.out) + r.r0 * a.ldo * LoraRow<OUT>::B;
         // pieces of ranks 8 PR h and on of columns c and on
         const int prow = lane / PR, piece = lane % PR;
         auto load_b = [&](v4i (&w)[PR], int c, int h) {
-            if (8 * (PR * h + piece) >= a.rank) return;
-            const uint16_t* const from = bp + 8 * (PR * h + piece);
-            if (c + 64 <= a.n) {
-                const uint16_t* const at = from + (int64_t)(c + prow) * a.rank;
+            if (c >= a.n || 8 * (PR * h + piece) >= a.rank) return;      // (a wave may have no columns)
+            const uint16_t* const from = bp + (int64_t)c * a.rank + 8 * PR * h;
+            const int rest = a.n - 1 - c;                    // the last column again past the end
 #pragma unroll
-                for (int j = 0; j < PR; ++j) w[j] = *reinterpret_cast<const v4i*>(at + j * (64 / PR) * a.rank);
-            } else {
-#pragma unroll
-                for (int j = 0; j < PR; ++j)
-                    w[j] = *reinterpret_cast<const v4i*>(from + (int64_t)min(c + j * (64 / PR) + prow, a.n - 1) * a.rank);
+            for (int j = 0; j < PR; ++j) {
+                const int row = j * (64 / PR) + prow;
+                w[j] = *reinterpret_cast<const v4i*>(reinterpret_cast<const char*>(from) + (uint32_t)((rest >= 63 ? row : min(row, rest)) * a.rank + 8 * piece) * 2);
             }
         };
         auto turn_b = [&](const v4i (&w)[PR]) {
@@ -344,9 +334,20 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
         load_b(w, c0 + wave * 64, 0);                        // on its way while v is made
         for (int t0 = 0; t0 < rows; t0 += 16 * blocks) {
             const int here = min(16 * blocks, rows - t0);
-            // v, fp32, with the adapter's scale; ranks past the last are zero
+            using Row = LoraRow<OUT>;
+            Row io;                                          // y of the first rows and columns, on its way too
+            auto load_y = [&](int c, int b) {                // this lane's row of the b-th 16, whole pieces only
+                if (!a.wide || c + 64 > a.n || 16 * b + i16 >= here) return;
+                const int row = __shfl(places, t0 + 16 * b + i16);
+                io.load(yb + (int64_t)c * Row::B, (uint32_t)row * (uint32_t)a.ldy * Row::B + 16 * G);
+            };
+            load_y(c0 + wave * 64, 0);
+            // v with the adapter's scale, four ranks of a row a thread; zeros past the last rank
+            float val[4][4];
+            int count = 0;
+            if (DT == CK_DT_FP16 && tid < 16 * blocks) tops[tid] = 0;
             if constexpr (RF > 0) {
-                float* const red = back + 16;                // [waves][16 rows][16 RF ranks + 4]
+                float* const red = reinterpret_cast<float*>(tops + 16);      // [waves][16 rows][16 RF ranks + 4]
                 constexpr int RS = 16 * RF + 4;
                 const int all = (a.k + 127) / 128, s0 = all * wave / NW, s1 = all * (wave + 1) / NW, cc = (lane >> 2) & 3;
                 for (int g0 = 0; g0 < here; g0 += 4) {
@@ -360,64 +361,74 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
                     }
                 }
                 __syncthreads();
-                const int i = tid >> 5, rr = tid & 31;       // 512 threads, 16 rows of 32 ranks
-                float sum = 0.0f;
-                if (i < here && rr < a.rank) {
-                    sum = red[i * RS + rr];
+                const int i = tid >> 3, k = tid % 8 * 4;
+                if (i < here) {
+                    f32x4v sum = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (k < a.rank) {
 #pragma unroll
-                    for (int x = 1; x < NW; ++x) sum = sum + red[(x * 16 + i) * RS + rr];
+                        for (int x = 0; x < NW; ++x) sum = sum + *reinterpret_cast<const f32x4v*>(red + (x * 16 + i) * RS + k);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) val[0][j] = sum[j] * scale;
+                    count = 1;
                 }
-                v[i * vs + rr] = sum * scale;
             } else {
-                for (int e = tid; e < 16 * blocks * 32 * steps; e += 64 * NW) {
-                    const int i = e / (32 * steps), rr = e % (32 * steps);
+                // up to 1024 of them (16 rows of 256 ranks, or 64 of 64): four a thread, all loads together
+                f32x4v sum[4];
+                const int per = 8 * steps, total = (here + 15) / 16 * 16 * per;
+                count = (total - tid + 64 * NW - 1) / (64 * NW);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int q = tid + j * 64 * NW, i = q / per, k = (q - i * per) * 4;
                     const int64_t at = r.r0 + __shfl(places, min(t0 + i, rows - 1));
-                    float sum = 0.0f;
-                    if (i < here && rr < a.rank) {
-                        const float* const p = a.v + at * a.vstride + rr;
-                        for (int s = 0; s < a.ksplits; s += 8) {     // (loads of eight parts go out together)
-                            float f[8];
+                    sum[j] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (j < count && i < here && k < a.rank) {
+                        const float* const p = a.v + at * a.vstride + k;
+                        for (int x = 0; x < a.ksplits; x += 4) {
+                            f32x4v f[4];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] = s + j < a.ksplits ? p[(int64_t)(s + j) * a.m * a.vstride] : 0.0f;
+                            for (int y = 0; y < 4; ++y)
+                                f[y] = x + y < a.ksplits ? *reinterpret_cast<const f32x4v*>(p + (int64_t)(x + y) * a.m * a.vstride)
+                                                         : f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) sum = sum + f[j];
+                            for (int y = 0; y < 4; ++y) sum[j] = sum[j] + f[y];
                         }
-                        sum *= scale;
                     }
-                    v[i * vs + rr] = sum;
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) val[j][x] = sum[j][x] * scale;
             }
-            __syncthreads();
-            // and its 16-bit parts, as the second product's second operand (what
-            // the other rows' places hold is not used)
-            for (int i = wave; i < here; i += NW) {
-                int e = 0;
-                if constexpr (DT == CK_DT_FP16) {
+            const int per = RF > 0 ? 8 : 8 * steps;
+            if constexpr (DT == CK_DT_FP16) {
+                if (RF == 0) __syncthreads();                // tops is cleared
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
                     float top = 0.0f;
-                    for (int k = lane; k < 32 * steps; k += 64) top = fmaxf(top, __builtin_fabsf(v[i * vs + k]));
 #pragma unroll
-                    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-                    e = top > 0.0f && top < INFINITY ? 14 - __builtin_amdgcn_frexp_expf(top) : 0;
-                    if (lane == 0) back[i] = __builtin_amdgcn_ldexpf(1.0f, -e);
+                    for (int x = 0; x < 4; ++x) top = fmaxf(top, __builtin_fabsf(val[j][x]));
+                    if (j < count && top > 0.0f && top < INFINITY) atomicMax(&tops[(tid + j * 64 * NW) / per], __float_as_uint(top));
                 }
-                for (int k = 2 * lane; k < 32 * steps; k += 128) {
-                    float x = __builtin_amdgcn_ldexpf(v[i * vs + k], e), z = __builtin_amdgcn_ldexpf(v[i * vs + k + 1], e);
-                    uint32_t* const to = reinterpret_cast<uint32_t*>(frags + (i / 16 * PARTS * steps + k / 32) * 64 + k / 8 % 4 * 16 + i % 16) + k % 8 / 2;
+                __syncthreads();
+                if (tid < here) back[tid] = tops[tid] ? __builtin_amdgcn_ldexpf(1.0f, -lift(tid)) : 1.0f;
+            }
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        const uint32_t h = narrow2<DT>(x, z);
-                        const float2 f = widen2<DT>(h);
-                        to[p * steps * 256] = h;
-                        x -= f.x;
-                        z -= f.y;
-                    }
+            for (int j = 0; j < 4; ++j) {
+                if (j >= count) break;
+                const int q = tid + j * 64 * NW, i = q / per, k = (q - i * per) * 4;
+                if constexpr (DT == CK_DT_FP16) {
+                    const int e = tops[i] ? lift(i) : 0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) val[j][x] = __builtin_amdgcn_ldexpf(val[j][x], e);
                 }
+                put(i, k, val[j][0], val[j][1]);
+                put(i, k + 2, val[j][2], val[j][3]);
             }
             __syncthreads();
             for (int c = c0 + wave * 64; c < c1; c += 64 * NW) {
                 // the columns that follow, or the first ones again for the next rows
                 const int next = c + 64 * NW < c1 ? c + 64 * NW : c0 + wave * 64;
-                const bool wide = a.wide && c + 64 <= a.n;
                 const int groups = (a.rank + 8 * PR - 1) / (8 * PR);
                 if (groups == 1) {
                     turn_b(w);
@@ -425,10 +436,6 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
                 }
 #pragma unroll 1
                 for (int b = 0; 16 * b < here; ++b) {
-                    const int place = t0 + 16 * b + i16;
-                    const int64_t row = r.r0 + __shfl(places, min(place, rows - 1));
-                    LoraRow<OUT> io;
-                    if (place < rows) io.load(a, wide, row, c, G);
                     f32x4v acc[4];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) acc[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
@@ -456,7 +463,28 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
                             }
                         }
                     }
-                    if (place < rows) io.store(a, wide, row, c, G, acc, DT == CK_DT_FP16 ? back[16 * b + i16] : 1.0f);
+                    if constexpr (DT == CK_DT_FP16) {
+                        const float up = back[16 * b + i16];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) acc[t] = acc[t] * up;
+                    }
+                    if (a.wide && c + 64 <= a.n) {
+                        const int row = __shfl(places, min(t0 + 16 * b + i16, rows - 1));
+                        if (16 * b + i16 < here) io.store(ob + (int64_t)c * Row::B, (uint32_t)row * (uint32_t)a.ldo * Row::B + 16 * G, acc);
+                    } else {                                 // a row's 64 columns, one a lane
+                        for (int i = 0; i < min(16, here - 16 * b); ++i) {
+                            if (i16 == i) {
+#pragma unroll
+                                for (int t = 0; t < 4; ++t)
+                                    *reinterpret_cast<f32x4v*>(line + (OUT == CK_OUT_FP32 ? 16 * t + 4 * G : 32 * (t >> 1) + 8 * G + 4 * (t & 1))) = acc[t];
+                            }
+                            const int64_t row = __shfl(places, t0 + 16 * b + i);
+                            const float d = line[lane];
+                            if (c + lane < a.n) Row::add(yb + (row * a.ldy + c + lane) * Row::B, ob + (row * a.ldo + c + lane) * Row::B, d);
+                        }
+                    }
+                    if (16 * (b + 1) < here) load_y(c, b + 1);
+                    else if (c + 64 * NW < c1) load_y(c + 64 * NW, 0);
                 }
             }
             __syncthreads();
@@ -552,8 +580,9 @@ extern "C" ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream)
             !aligned(p.x, 16) || !aligned(p.a, 16) || !aligned(p.b, 16))
             return fail(CK_ERR_UNSUPPORTED, "rows of x and adapters must start 16 bytes apart");
     }
-    if (p.adapters > 0 && p.k > 0 && p.m > 1 && p.ldx > (1 << 24) + 128)
-        return fail(CK_ERR_UNSUPPORTED, "rows of x too far apart for 32-bit offsets");
+    // 32-bit offsets of 64 rows
+    if (p.m > 1 && ((p.adapters > 0 && p.k > 0 && p.ldx > (1 << 24) + 128) || p.ldy > (1 << 24) + 128 || p.ldo > (1 << 24) + 128))
+        return fail(CK_ERR_UNSUPPORTED, "rows of x, y or out more than 2^24 + 128 elements apart");
     const int esz = p.out_dtype == CK_OUT_FP32 ? 4 : 2;
     if (!aligned(p.y, esz) || !aligned(p.out, esz) || !aligned(p.ids, 4) || !aligned(p.scale, 4))
         return fail(CK_ERR_UNSUPPORTED, "misaligned y, out, ids or scale");
@@ -584,8 +613,8 @@ extern "C" ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream)
     a.slices = (int)cdiv(p.n, a.slice);
     int held = plan.blocks;
     const int64_t parts = f16 ? 2 : 3, steps = cdiv(p.rank, 32), rf = plan.fused ? cdiv(p.rank, 16) : 0;
-    a.turn = (int)(cdiv(held * parts * steps * 1024 + 16 * held * (32 * steps + 4) * 4 + 64 * held + (rf ? waves * 64 * (16 * rf + 4) : 0), 16) * 16);
-    const size_t lds = a.turn + waves * 64 * 16 * ((p.rank <= 16 ? 2 : p.rank <= 32 ? 4 : 8) + 1);
+    a.turn = (int)(held * parts * steps * 1024 + 128 * held + (rf ? waves * 64 * (16 * rf + 4) : 0));
+    const size_t lds = a.turn + waves * 256 + waves * 64 * 16 * ((p.rank <= 16 ? 2 : p.rank <= 32 ? 4 : 8) + 1);
     const void* fn = f16 ? lora_expand_fn<CK_DT_FP16>(p.out_dtype, plan.fused, p.rank) : lora_expand_fn<CK_DT_BF16>(p.out_dtype, plan.fused, p.rank);
     void* kargs[] = {&a, &units, &held};
     const int64_t blocks = per64 * a.slices;
