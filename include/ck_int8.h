@@ -699,13 +699,17 @@ int64_t ck_shared_prefix_attention_workspace(int64_t batch, int64_t hq, int64_t 
  *   out[i, j] = round_out( y[i, j] + scale[t] sum_r v[r] b[t, j, r] ),
  *   v[r] = sum_c x[i, c] a[t, r, c],  t = ids[i];
  * out[i] = y[i], bit for bit, for an id outside [0, adapters) (-1, say).
- * v and all sums are fp32 (v enters the product in 16-bit parts that hold it
- * to 2^-22 of itself (fp16) or better; see below for fp16's range).
+ * v and all sums are fp32; v enters the second product in 16-bit parts, which
+ * hold it to 2^-24 of itself (bf16), or to 2^-22 of itself or 2^-39 of the row's
+ * largest (fp16).  The a and b of an adapter that a row asks for must be finite
+ * (an infinite value can give NaN in place of infinity); x and y may be anything,
+ * and reach their own row only.
  *
  * x        [in]  16-bit (dtype) [m, ldx]; ldx >= k, ldx % 8 == 0, 16-B aligned.
  * a        [in]  16-bit (dtype) [adapters][rank][k], adapters a_stride apart.
  * b        [in]  16-bit (dtype) [adapters][n][rank], adapters b_stride apart.
- *                Strides are multiples of 8, a and b 16-B aligned.
+ *                Strides are multiples of 8, a and b 16-B aligned.  ldx, ldy and
+ *                ldo at most 2^24 + 128.
  * scale    [in]  fp32 [adapters], or NULL for 1.
  * ids      [in]  int32 [m], in any order; rows of one adapter that stand
  *                together are cheaper.

@@ -94,68 +94,82 @@ __device__ __forceinline__ float quad_diagonal(const f32x4v& d)
     return (__int_as_float(t0) + __int_as_float(t1)) + (__int_as_float(t2) + __int_as_float(t3));
 }
 
-// The first product, 16 RP ranks from rank0 on of 4 XG rows, over steps s0 ..
-// s1 - 1 of 128 columns.  A load of 16 bytes a lane costs as many cycles as the
-// 64-byte segments that each four lanes in a row touch, so such four take 64
-// bytes of a row of A or x, which makes them different operand rows: row 4 a + b
-// of the first operand is piece b (8 columns) of A's row a, column 4 c + b of the
-// second piece b of x's row c, and where the two b agree the product is a part
-// of v, four of which add up to it.  (With operand rows that are A's and x's the
-// loads took three times as long.)  Lane 16 G + 4 c + b ends up with ranks rank0 +
-// 4 q + G of row 4 g + c in v[g][q], for every b.
+// The first product, 16 ranks from rank0 on of 4 XG rows, over steps s0 .. s1 - 1
+// of 128 columns.  A load of 16 bytes a lane costs as many cycles as the 64-byte
+// segments that each four lanes in a row touch, so such four take 64 bytes of
+// a row of A or x, which makes them different operand rows: row 4 a + b of the
+// first operand is piece b (8 columns) of A's row a, column 4 c + b of the second
+// piece b of x's row c, and where the two b agree the product is a part of v, four
+// of which add up to it.  (With operand rows that are A's and x's the loads took
+// three times as long.)  Lane 16 G + 4 c + b ends up with ranks rank0 + 4 q + G of
+// row 4 g + c in v[g][q], for every b.  The code is short on purpose: a call runs
+// most of it once or twice, and it comes from a cold instruction cache at some
+// 10 cycles an instruction (64 ranks a wave instead of 16 took 13 us for 8).
 // xo: the rows' byte offsets from xb, with this lane's columns of 128.
-template <int DT, int XG, int RP, int U>
+template <int DT, int XG>
 __device__ __forceinline__ void lora_shrink(const LoraArgs& a, const uint16_t* xb, const uint32_t (&xo)[XG], const uint16_t* wb,
-                                            int rank0, int s0, int s1, float (&v)[XG][4 * RP])
+                                            int rank0, int s0, int s1, float (&v)[XG][4])
 {
+    constexpr int U = XG == 4 ? 2 : 4;                       // steps whose loads go out together
     const int lane = threadIdx.x & 63;
     const int at = (lane >> 4) * 32 + (lane & 3) * 8;        // this lane's columns of 128
     const int last = (a.rank - rank0) / 4 - 1;               // of the groups of four ranks
     const uint32_t wo = (uint32_t)(((lane >> 2) & 3) * a.k + at) * 2;
     const char* const x = reinterpret_cast<const char*>(xb);
-    const char* w[4 * RP];
+    const char* w[4];
 #pragma unroll
-    for (int q = 0; q < 4 * RP; ++q) w[q] = reinterpret_cast<const char*>(wb + (int64_t)(rank0 + 4 * min(q, last)) * a.k);
-    f32x4v acc[XG][4 * RP];
+    for (int q = 0; q < 4; ++q) w[q] = reinterpret_cast<const char*>(wb + (int64_t)(rank0 + 4 * min(q, last)) * a.k);
+    f32x4v acc[XG][4];
 #pragma unroll
     for (int g = 0; g < XG; ++g)
 #pragma unroll
-        for (int q = 0; q < 4 * RP; ++q) acc[g][q] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-    auto run = [&](int s, auto count, auto whole) {
+        for (int q = 0; q < 4; ++q) acc[g][q] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    auto run = [&](int s, auto count) {
         constexpr int N = decltype(count)::value;
-        v4i xs[N][XG], ws[N][4 * RP];
+        v4i xs[N][XG], ws[N][4];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
-            // past the end: the last piece of the row again, then zeros
-            const uint32_t c = (s + u) * 256, off = whole.value ? c : min(c + 2 * at, (uint32_t)(2 * a.k - 16)) - 2 * at;
+            uint32_t off = (s + u) * 256;
+            if (N == 1) off = min(off + 2 * at, (uint32_t)(2 * a.k - 16)) - 2 * at;      // past the end the row's last piece again, times zeros
 #pragma unroll
             for (int g = 0; g < XG; ++g) xs[u][g] = *reinterpret_cast<const v4i*>(x + (xo[g] + off));
 #pragma unroll
-            for (int q = 0; q < 4 * RP; ++q) ws[u][q] = *reinterpret_cast<const v4i*>(w[q] + (wo + off));
-            if (!whole.value && (s + u) * 128 + at >= a.k) {
+            for (int q = 0; q < 4; ++q) ws[u][q] = *reinterpret_cast<const v4i*>(w[q] + (wo + off));
+        }
+        if (N == 1 && s * 128 + at >= a.k) {
 #pragma unroll
-                for (int g = 0; g < XG; ++g) xs[u][g] = v4i{0, 0, 0, 0};
-#pragma unroll
-                for (int q = 0; q < 4 * RP; ++q) ws[u][q] = v4i{0, 0, 0, 0};
-            }
+            for (int g = 0; g < XG; ++g) xs[0][g] = v4i{0, 0, 0, 0};
         }
 #pragma unroll
         for (int u = 0; u < N; ++u)
 #pragma unroll
-            for (int q = 0; q < 4 * RP; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int g = 0; g < XG; ++g) acc[g][q] = mfma16<DT>(ws[u][q], xs[u][g], acc[g][q]);
     };
     const int full = min(s1, a.k / 128);
     int s = s0;
-    for (; s + U <= full; s += U) run(s, IntTag<U>{}, BoolTag<true>{});
-    for (; s < full; ++s) run(s, IntTag<1>{}, BoolTag<true>{});
-    if (s < s1) run(s, IntTag<1>{}, BoolTag<false>{});
+    for (; s + U <= full; s += U) run(s, IntTag<U>{});
+    for (; s < s1; ++s) run(s, IntTag<1>{});
 #pragma unroll
     for (int g = 0; g < XG; ++g)
 #pragma unroll
-        for (int q = 0; q < 4 * RP; ++q) v[g][q] = quad_diagonal(acc[g][q]);
+        for (int q = 0; q < 4; ++q) v[g][q] = quad_diagonal(acc[g][q]);
 }
+
+// How a block's waves share the first product: a wave has 16 ranks, and the
+// waves with the same ones each a part of k.
+struct LoraShare {
+    int groups, mine, part, parts;       // groups of 16 ranks at a time (a power of two), this wave's; its part of k
+    __device__ __forceinline__ LoraShare(int rank, int wave, int split, int splits)
+    {
+        groups = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : kLoraWaves;
+        mine = wave & (groups - 1);
+        parts = kLoraWaves / groups * splits;
+        part = split * (kLoraWaves / groups) + wave / groups;
+    }
+    __device__ __forceinline__ int begin(int steps, int more) const { return (int)((int64_t)steps * (part + more) / parts); }
+};
 
 // The rows that a lane's x are, as byte offsets: row 4 g + c of 16 from place t0
 // on, the last one again past the end.
@@ -171,17 +185,17 @@ __device__ __forceinline__ void lora_x(const LoraArgs& a, int places, int t0, in
 // The first launch: v of a group of rows, over one part of k.  XG: 1 for groups
 // of up to 64 rows whose adapters have a few each (four at a time), 4 for 16
 // rows in a row.
-template <int DT, int XG, int RP>
+template <int DT, int XG>
 __global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArgs a, int group, int units)
 {
-    constexpr int NW = kLoraWaves, U = XG == 4 ? 2 : RP == 4 ? 2 : 4;
-    __shared__ float red[NW][4 * XG][16 * RP + 4];
+    constexpr int NW = kLoraWaves;
+    __shared__ float red[NW][4 * XG][20];                    // [wave][row][rank]
     const int tid = threadIdx.x, lane = tid & 63, G = lane >> 4, c = (lane >> 2) & 3;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int split = blockIdx.x % a.ksplits;
     LoraRows r(a, blockIdx.x / a.ksplits, group, units);
-    const int steps = (a.k + 127) / 128, part = split * NW + wave, parts = a.ksplits * NW;
-    const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
+    const LoraShare share(a.rank, wave, split, a.ksplits);
+    const int steps = (a.k + 127) / 128, s0 = share.begin(steps, 0), s1 = share.begin(steps, 1);
     while (r.left) {
         int id;
         const uint64_t members = lora_members(r.left, r.ids, id);
@@ -189,23 +203,26 @@ __global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArg
         for (int t0 = 0; t0 < rows; t0 += 4 * XG) {
             uint32_t xo[XG];
             lora_x<XG>(a, places, t0, rows, xo);
-            for (int rank0 = 0; rank0 < a.rank; rank0 += 16 * RP) {
-                float v[XG][4 * RP];
-                lora_shrink<DT, XG, RP, U>(a, a.x + r.r0 * a.ldx, xo, a.a + id * a.a_stride, rank0, s0, s1, v);
-                if ((lane & 3) == 0) {
+            for (int rank0 = 0; rank0 < a.rank; rank0 += 16 * share.groups) {
+                if (rank0 + 16 * share.mine < a.rank) {
+                    float v[XG][4];
+                    lora_shrink<DT, XG>(a, a.x + r.r0 * a.ldx, xo, a.a + id * a.a_stride, rank0 + 16 * share.mine, s0, s1, v);
+                    if ((lane & 3) == 0) {
 #pragma unroll
-                    for (int g = 0; g < XG; ++g)
+                        for (int g = 0; g < XG; ++g)
 #pragma unroll
-                        for (int q = 0; q < 4 * RP; ++q) red[wave][4 * g + c][4 * q + G] = v[g][q];
+                            for (int q = 0; q < 4; ++q) red[wave][4 * g + c][4 * q + G] = v[g][q];
+                    }
                 }
                 __syncthreads();
-                for (int e = tid; e < 4 * XG * 16 * RP; e += 64 * NW) {
-                    const int i = e / (16 * RP), rr = e % (16 * RP);
-                    float sum = red[0][i][rr];
-#pragma unroll
-                    for (int x = 1; x < NW; ++x) sum = sum + red[x][i][rr];
+                for (int e = tid; e < 64 * XG * share.groups; e += 64 * NW) {
+                    const int rr = e & 15, i = (e >> 4) % (4 * XG), g = e / (64 * XG), k = rank0 + 16 * g + rr;
                     const int row = __shfl(places, min(t0 + i, rows - 1));
-                    if (t0 + i < rows && rank0 + rr < a.rank) a.v[((int64_t)split * a.m + r.r0 + row) * a.vstride + rank0 + rr] = sum;
+                    if (t0 + i < rows && k < a.rank) {
+                        float sum = red[g][i][rr];
+                        for (int x = g + share.groups; x < NW; x += share.groups) sum = sum + red[x][i][rr];
+                        a.v[((int64_t)split * a.m + r.r0 + row) * a.vstride + k] = sum;
+                    }
                 }
                 __syncthreads();
             }
@@ -254,15 +271,15 @@ struct LoraRow {
     }
 };
 
-// The second product, or all of it (RF > 0: v is made here), for up to `blocks`
+// The second product, or all of it (FUSED: v is made here), for up to `blocks`
 // blocks of 16 rows at a time.  A wave has 64 columns at a time, as four tiles
 // whose operand rows are such columns that lane 16 G + i ends up with whole
 // 16-byte pieces of row i, G and every fourth one on: a load or store of y has 64
 // bytes of each row.
-template <int DT, int OUT, int RF, int PR>
-__global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_expand_kernel(LoraArgs a, int units, int blocks)
+template <int DT, int OUT, bool FUSED, int PR>
+__global__ __launch_bounds__(64 * (FUSED ? 8 : 4), FUSED ? 4 : 3) void lora_expand_kernel(LoraArgs a, int units, int blocks)
 {
-    constexpr int PARTS = DT == CK_DT_FP16 ? 2 : 3, NW = RF > 0 ? 8 : 4;
+    constexpr int PARTS = DT == CK_DT_FP16 ? 2 : 3, NW = FUSED ? kLoraWaves : 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, G = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -346,28 +363,27 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
             float val[4][4];
             int count = 0;
             if (DT == CK_DT_FP16 && tid < 16 * blocks) tops[tid] = 0;
-            if constexpr (RF > 0) {
-                float* const red = reinterpret_cast<float*>(tops + 16);      // [waves][16 rows][16 RF ranks + 4]
-                constexpr int RS = 16 * RF + 4;
-                const int all = (a.k + 127) / 128, s0 = all * wave / NW, s1 = all * (wave + 1) / NW, cc = (lane >> 2) & 3;
+            if constexpr (FUSED) {
+                float* const red = reinterpret_cast<float*>(tops + 16);      // [waves][16 rows][16 ranks + 4]
+                const LoraShare share(a.rank, wave, 0, 1);
+                const int all = (a.k + 127) / 128, s0 = share.begin(all, 0), s1 = share.begin(all, 1), cc = (lane >> 2) & 3;
                 for (int g0 = 0; g0 < here; g0 += 4) {
                     uint32_t xo[1];
                     lora_x<1>(a, places, t0 + g0, rows, xo);
-                    float part[1][4 * RF];
-                    lora_shrink<DT, 1, RF, 4 / RF>(a, a.x + r.r0 * a.ldx, xo, a.a + id * a.a_stride, 0, s0, s1, part);
+                    float part[1][4];
+                    if (16 * share.mine < a.rank)
+                        lora_shrink<DT, 1>(a, a.x + r.r0 * a.ldx, xo, a.a + id * a.a_stride, 16 * share.mine, s0, s1, part);
                     if ((lane & 3) == 0) {
 #pragma unroll
-                        for (int q = 0; q < 4 * RF; ++q) red[(wave * 16 + g0 + cc) * RS + 4 * q + G] = part[0][q];
+                        for (int q = 0; q < 4; ++q) red[(wave * 16 + g0 + cc) * 20 + 4 * q + G] = part[0][q];
                     }
                 }
                 __syncthreads();
                 const int i = tid >> 3, k = tid % 8 * 4;
                 if (i < here) {
                     f32x4v sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (k < a.rank) {
-#pragma unroll
-                        for (int x = 0; x < NW; ++x) sum = sum + *reinterpret_cast<const f32x4v*>(red + (x * 16 + i) * RS + k);
-                    }
+                    if (k < a.rank)
+                        for (int x = k / 16; x < NW; x += share.groups) sum = sum + *reinterpret_cast<const f32x4v*>(red + (x * 16 + i) * 20 + k % 16);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) val[0][j] = sum[j] * scale;
                     count = 1;
@@ -400,9 +416,9 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
 #pragma unroll
                     for (int x = 0; x < 4; ++x) val[j][x] = sum[j][x] * scale;
             }
-            const int per = RF > 0 ? 8 : 8 * steps;
+            const int per = FUSED ? 8 : 8 * steps;
             if constexpr (DT == CK_DT_FP16) {
-                if (RF == 0) __syncthreads();                // tops is cleared
+                if (!FUSED) __syncthreads();                 // tops is cleared
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float top = 0.0f;
@@ -448,13 +464,11 @@ __global__ __launch_bounds__(64 * (RF > 0 ? 8 : 4), RF > 0 ? 2 : 3) void lora_ex
                         for (int s = 0; s < (PR + 3) / 4; ++s) {
                             const int k = PR * h + 4 * s;        // pieces before
                             if (8 * k >= a.rank) break;
-                            const bool in = 8 * (k + G) < a.rank;
+                            // (pieces past the last rank meet zeros of v: any that is there does)
+                            const int have = 8 * (k + G) < a.rank ? 4 * s + G : 0;
                             v4i f[4];
 #pragma unroll
-                            for (int t = 0; t < 4; ++t) {
-                                f[t] = turn[cols[t] * (PR | 1) + (in ? 4 * s + G : 0)];
-                                if (!in) f[t] = v4i{0, 0, 0, 0};
-                            }
+                            for (int t = 0; t < 4; ++t) f[t] = turn[cols[t] * (PR | 1) + have];
 #pragma unroll
                             for (int p = 0; p < PARTS; ++p) {
                                 const v4i y = frags[((b * PARTS + p) * steps + k / 4) * 64 + lane];
@@ -510,35 +524,30 @@ LoraPlan lora_plan(int64_t m, int64_t n, int64_t k, int64_t rank)
 {
     LoraPlan p{};
     p.each = m <= kLoraRows;
-    p.fused = p.each && rank <= 32 && rank * k <= 131072 && m <= 8;
+    p.fused = p.each && rank <= 32 && rank * k <= 131072 && m <= 64;
     p.blocks = p.fused || rank > 128 ? 1 : rank > 64 ? 2 : 4;    // within 64 KiB
     p.group = p.each ? 64 : 16;
     const int64_t units = p.each ? std::min<int64_t>(m, 16) : cdiv(m, p.group);
-    p.ksplits = std::max<int64_t>(1, std::min<int64_t>(cdiv(kNumCUs, std::max<int64_t>(units, 1)), k / (128 * kLoraWaves)));
+    p.ksplits = std::max<int64_t>(1, std::min<int64_t>(cdiv(kNumCUs, std::max<int64_t>(units, 1)), cdiv(k * std::min<int64_t>(cdiv(rank, 16), kLoraWaves), 128 * 2 * kLoraWaves)));
     if (!p.fused) p.bytes = p.ksplits * m * rank * 4;
     return p;
 }
 
 template <int DT>
-const void* lora_shrink_fn(bool each, int64_t rank)
+const void* lora_shrink_fn(bool each)
 {
-    if (each)
-        return rank <= 16   ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1, 1>)
-               : rank <= 32 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1, 2>)
-                            : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1, 4>);
-    return rank <= 16 ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4, 1>)
-                      : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4, 2>);
+    return each ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1>) : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4>);
 }
 
 template <int DT, int OUT>
 const void* lora_expand_out(bool fused, int64_t rank)
 {
     if (fused)
-        return rank <= 16 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 1, 2>)
-                          : reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 2, 4>);
-    return rank <= 16   ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 0, 2>)
-           : rank <= 32 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 0, 4>)
-                        : reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, 0, 8>);
+        return rank <= 16 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, true, 2>)
+                          : reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, true, 4>);
+    return rank <= 16   ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, false, 2>)
+           : rank <= 32 ? reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, false, 4>)
+                        : reinterpret_cast<const void*>(&lora_expand_kernel<DT, OUT, false, 8>);
 }
 
 template <int DT>
@@ -603,17 +612,17 @@ extern "C" ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream)
     if (!plan.fused && a.adapters > 0) {
         void* kargs[] = {&a, &group, &units};
         const int64_t blocks = (plan.each ? per64 : cdiv(p.m, plan.group)) * plan.ksplits;
-        const void* fn = f16 ? lora_shrink_fn<CK_DT_FP16>(plan.each, p.rank) : lora_shrink_fn<CK_DT_BF16>(plan.each, p.rank);
+        const void* fn = f16 ? lora_shrink_fn<CK_DT_FP16>(plan.each) : lora_shrink_fn<CK_DT_BF16>(plan.each);
         if ((s = launch(fn, (unsigned)blocks, 64 * kLoraWaves, kargs, stream, "lora_shrink")) != CK_OK) return s;
     }
     // Column slices, of whole rounds of a block's waves: as many blocks as give every CU two.
     const int64_t waves = plan.fused ? 8 : 4;
     const int64_t turns = cdiv(p.n, 64 * waves);             // of all columns
-    a.slice = (int)(cdiv(turns, std::min(cdiv((plan.fused ? 2 : 3) * kNumCUs, per64), turns)) * 64 * waves);
+    a.slice = (int)(cdiv(turns, std::min(cdiv(2 * kNumCUs, per64), turns)) * 64 * waves);
     a.slices = (int)cdiv(p.n, a.slice);
     int held = plan.blocks;
-    const int64_t parts = f16 ? 2 : 3, steps = cdiv(p.rank, 32), rf = plan.fused ? cdiv(p.rank, 16) : 0;
-    a.turn = (int)(held * parts * steps * 1024 + 128 * held + (rf ? waves * 64 * (16 * rf + 4) : 0));
+    const int64_t parts = f16 ? 2 : 3, steps = cdiv(p.rank, 32);
+    a.turn = (int)(held * parts * steps * 1024 + 128 * held + (plan.fused ? waves * 64 * 20 : 0));
     const size_t lds = a.turn + waves * 256 + waves * 64 * 16 * ((p.rank <= 16 ? 2 : p.rank <= 32 ? 4 : 8) + 1);
     const void* fn = f16 ? lora_expand_fn<CK_DT_FP16>(p.out_dtype, plan.fused, p.rank) : lora_expand_fn<CK_DT_BF16>(p.out_dtype, plan.fused, p.rank);
     void* kargs[] = {&a, &units, &held};
