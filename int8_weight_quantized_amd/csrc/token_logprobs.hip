@@ -114,7 +114,7 @@ __device__ __forceinline__ LogSums join_sums(LogSums t)
     float high = t.m;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) high = fmaxf(high, __shfl_xor(high, off));
-    const double d = fmax((double)t.m - high, -1e4), f = t.m == high ? 1.0 : exp(d);
+    const double d = fmaxf(t.m - high, -1e4f), f = __builtin_amdgcn_exp2f((float)d * kLog2e);    // 1 exactly where m is the highest
     t.w = (t.w + t.s * d) * f;
     t.s *= f;
 #pragma unroll
@@ -155,16 +155,19 @@ __device__ __forceinline__ float log_probability(float x, const LogSums& t, doub
     return (float)((double)x - (double)t.m - logs);
 }
 
+// The given token's logit, NaN for a token outside the vocabulary; loaded
+// before the row's sums are there.
 template <int DT>
-__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const LogSums& t)
+__device__ __forceinline__ float token_logit(const LogprobArgs& a, int64_t row)
 {
-    const double logs = log(t.s);
-    if (a.logprob) {
-        const int64_t tok = a.tokens[row];
-        const bool in = tok >= 0 && tok < a.vocab;
-        const float x = logit_at<DT>(a.logits, row * a.ld + (in ? tok : 0));
-        a.logprob[row] = in ? log_probability(x, t, logs) : NAN;
-    }
+    if (!a.logprob) return 0.0f;
+    const int64_t tok = a.tokens[row];
+    return tok >= 0 && tok < a.vocab ? logit_at<DT>(a.logits, row * a.ld + tok) : NAN;
+}
+
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, float x, const LogSums& t, double logs)
+{
+    if (a.logprob) a.logprob[row] = log_probability(x, t, logs);
     if (a.entropy) a.entropy[row] = (float)(logs - t.w / t.s);
 }
 
@@ -267,6 +270,8 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
             if (p + 256 * j + tid < p1) to[j] = vec[p + 256 * j + tid];
     };
     load(v, p0);
+    float given = 0.0f;
+    if (tid == 0 && a.splits == 1) given = token_logit<DT>(a, row);
     any = p0 + tid < p1;
     for (int p = p0; p < p1; p += 256 * B) {
         load(next, p + 256 * B);
@@ -369,9 +374,9 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
         }
         return;
     }
-    if (tid == 0) write_row<DT>(a, row, t);
+    const double logs = log(t.s);
+    if (tid == 0) write_row(a, row, given, t, logs);
     if constexpr (TOP) {
-        const double logs = log(t.s);
         cand.rank(a.top, [&](int place, u64 key) { write_top(a, row * a.top + place, key, t, logs); });
     }
 }
@@ -386,6 +391,8 @@ __global__ __launch_bounds__(256) void token_logprobs_join_kernel(LogprobArgs a)
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row = blockIdx.x;
     LogSums t{0.0, 0.0, kLogLow};
+    float given = 0.0f;
+    if (tid == 0) given = token_logit<DT>(a, row);
     if (lane < a.splits) {
         const double2 v = a.sums[row * a.splits + lane];
         t = {v.x, v.y, a.refs[row * a.splits + lane]};
@@ -403,10 +410,10 @@ __global__ __launch_bounds__(256) void token_logprobs_join_kernel(LogprobArgs a)
             if (keys[i] >= least) cand.add(keys[i]);
     }
     t = join_sums(t);
-    if (tid == 0) write_row<DT>(a, row, t);
+    const double logs = log(t.s);
+    if (tid == 0) write_row(a, row, given, t, logs);
     if (a.top == 0) return;
     __syncthreads();
-    const double logs = log(t.s);
     cand.rank(a.top, [&](int place, u64 key) { write_top(a, row * a.top + place, key, t, logs); });
 }
 
