@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
     constexpr int E = DT == CK_OUT_FP32 ? 4 : 8, B = kLogprobBatch;   // logits of a load, loads of a batch
     __shared__ LogSums sums[4];
     __shared__ Candidates cand;
-    __shared__ __attribute__((aligned(16))) uint32_t highs[TOP ? 256 : 4];
+    __shared__ uint32_t highs[TOP ? 256 : 4];
     __shared__ uint8_t owners[TOP ? 256 : 4];
     __shared__ int owning;
     __shared__ float bound;
@@ -292,34 +292,28 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
     const LogSums mine = wave_sums(m, s, w);
     if (lane == 0) sums[wave] = mine;
     if constexpr (TOP) {
-        // The bound: the k-th of the lanes' maxima, or for few alternatives of
-        // those of four lanes each.  Their order goes by 24 bits of the value,
-        // then the lane: the bound is what these 24 bits begin with.  Lanes
-        // without a logit (0) are among the first k only in a small chunk,
-        // which has few logits: no bound then.
-        const uint32_t lane_id = 255u - tid, mine = any ? (order_key(top) & ~255u) | lane_id : lane_id;
-        highs[tid] = mine;
+        // The bound: what the k-th of the lanes' maxima begins with, found bit by
+        // bit by the first wave, as many bits as it takes until k reach it and no
+        // more, or as the type has (of fp32 20).  (Lanes without a logit, 0, are among them only in a small chunk,
+        // which has few logits: no bound then.)
+        highs[tid] = any ? order_key(top) : 0;
         if (tid == 0) {
             cand.count = 0;
             owning = 0;
         }
         __syncthreads();
-        uint32_t high = mine;
-        int n = 256;
-        if (a.top <= 16) {
-            n = 64;
-            high = max(max(highs[lane], highs[lane + 64]), max(highs[lane + 128], highs[lane + 192]));
-            __syncthreads();
-            if (tid < 64) highs[tid] = high;
-            __syncthreads();
+        if (wave == 0) {
+            const uint32_t h0 = highs[lane], h1 = highs[lane + 64], h2 = highs[lane + 128], h3 = highs[lane + 192];
+            uint32_t reach = 0;
+            for (uint32_t bit = 0x80000000u; bit >= (DT == CK_OUT_BF16 ? 0x10000u : 0x1000u); bit >>= 1) {
+                const uint32_t t = reach | bit;
+                const int n = __popcll(__ballot(h0 >= t)) + __popcll(__ballot(h1 >= t)) + __popcll(__ballot(h2 >= t)) + __popcll(__ballot(h3 >= t));
+                if (n < a.top) continue;
+                reach = t;
+                if (n == a.top) break;
+            }
+            if (lane == 0) bound = reach >= 0x00800000u ? order_value(reach) : -INFINITY;
         }
-        int place = 0;
-#pragma unroll 4
-        for (int i = 0; i < n; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(&highs[i]);
-            place += (int)(o.x > high) + (int)(o.y > high) + (int)(o.z > high) + (int)(o.w > high);
-        }
-        if (tid < n && place == a.top - 1) bound = high >= 0x00800000u ? order_value(high & ~255u) : -INFINITY;
         __syncthreads();
         const float least = bound;
         if (any && top >= least) owners[atomicAdd(&owning, 1)] = (uint8_t)tid;
