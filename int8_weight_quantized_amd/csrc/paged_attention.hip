@@ -201,65 +201,112 @@ struct AttnKind {
     static constexpr float fine = each == 2 ? 8388608.0f : 2048.0f;
 };
 
-// One tile of 32 tokens for MB blocks of 16 rows of queries: kr and vr are its
-// K and V rows in LDS, kscale and vscale (int8) the tokens' scales there, and
-// `limit` the number of its tokens that count.  M, L and acc are the rows'
-// running reference, sums of weights and weighted values; `empty`: the sums
-// are still zero.  k_read(), v_ready() and v_read() are called when K has been
-// read, before V is read and after.
-template <int DT, bool I8, int D, int MB, int PARTS, class KRead, class VReady, class VRead>
-__device__ __forceinline__ void attn_tile(const uint8_t* kr, const uint8_t* vr, const v4i (&qf)[MB][D / 32],
+// Where a lane reads K and V of a tile, whose rows begin at kr and vr in LDS: what
+// of its places does not follow from the others by a constant.
+template <bool I8, int D>
+struct AttnLane {
+    static constexpr int RB = D * (I8 ? 1 : 2), KK = D / 32, DB = D / 16;
+    using Sh = AttnShape<RB>;
+    static constexpr int kstep = I8 ? 2 : 4, vstep = I8 ? 1 : 2;             // 16-byte pieces of a K step, of 16 columns of V
+    static constexpr int least(int x, int y) { return x < y ? (x < 1 ? 1 : x) : y; }
+    static constexpr int KN = least(Sh::span / 16 / kstep, KK), VN = least(Sh::span / 16 / vstep, DB);
+    const uint8_t *k[KN], *v[VN];
+
+    __device__ __forceinline__ AttnLane(const uint8_t* kr, const uint8_t* vr)
+    {
+        const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            const int piece = 4 * i + G;                     // int8: of eight codes
+            k[i] = kr + i16 * RB + (I8 ? (((piece >> 1) ^ Sh::swz(i16)) << 4) + (piece & 1) * 8 : (piece ^ Sh::swz(i16)) << 4);
+        }
+        // transposing reads; int8: row r of the eight is token 4 G + r of the first tile or 4 G + r - 4 of the second
+        const int r = i16 >> 1, row = I8 ? 4 * G + (r & 3) + 16 * (r >> 2) : 4 * G + (i16 >> 2);
+#pragma unroll
+        for (int i = 0; i < VN; ++i)
+            v[i] = vr + row * RB + ((I8 ? i ^ Sh::swz(row) : (2 * i + ((i16 >> 1) & 1)) ^ Sh::swz2(row)) << 4) + (i16 & 1) * 8;
+    }
+    // (rows 16 apart have the same place among the banks)
+    __device__ __forceinline__ const uint8_t* k_at(int u, int kk) const { return k[kk % KN] + 16 * u * RB + kk / KN * (KN * kstep * 16); }
+    __device__ __forceinline__ const uint8_t* v_at(int u, int d) const { return v[d % VN] + 16 * u * RB + d / VN * (VN * vstep * 16); }
+};
+
+// One tile of 32 tokens for MB blocks of 16 rows of queries: `at` are this
+// lane's places in the tile's K and V, `off` bytes on; kscale and vscale (int8)
+// are the tokens' scales, and `limit` is the number of its tokens that count.
+// M, L and acc are the rows' running reference, sums of weights and weighted
+// values; `empty`: the sums are still zero.  k_read(), v_ready() and v_read() are
+// called when K has been read, before V is read and after.  FOLD: a score is
+// scaled in the step that takes the reference off, one rounding for two; V,
+// which has to be there, is read before the weights are made where there are
+// registers for it; and a wave in its products goes before one in its weights (128
+// sequences behind 65536 tokens, 64/8 heads of 128: 453 us, 421 and 408).
+template <int DT, bool I8, int D, int MB, int PARTS, bool FOLD, class KRead, class VReady, class VRead>
+__device__ __forceinline__ void attn_tile(const AttnLane<I8, D>& at, int off, const v4i (&qf)[MB][D / 32],
                                           const float (&sc)[MB], const float* kscale, const float* vscale, int ve,
                                           int limit, bool empty, float (&M)[MB], float (&L)[MB],
                                           f32x4v (&acc)[MB][AttnKind<DT, I8, PARTS>::NA][D / 16], KRead k_read,
                                           VReady v_ready, VRead v_read)
 {
-    constexpr int RB = D * (I8 ? 1 : 2), KK = D / 32, DB = D / 16;
-    using Sh = AttnShape<RB>;
+    constexpr int KK = D / 32, DB = D / 16;
     using Kind = AttnKind<DT, I8, PARTS>;
     constexpr int KT = Kind::KT, VT = Kind::VT, NA = Kind::NA;
-    const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
+    const int G = (threadIdx.x & 63) >> 4;
     f32x4v s[MB][2];
+    if constexpr (FOLD) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int b = 0; b < MB; ++b) s[b][u] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-        const int row = 16 * u + i16;
-        const uint8_t* const at = kr + row * RB;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             v4i kf;
-            if constexpr (I8) {
-                const int piece = 4 * kk + G;
-                kf = codes8_f16(*reinterpret_cast<const uint2*>(at + (((piece >> 1) ^ Sh::swz(row)) << 4) + (piece & 1) * 8));
-            } else {
-                kf = *reinterpret_cast<const v4i*>(at + (((4 * kk + G) ^ Sh::swz(row)) << 4));
-            }
+            if constexpr (I8) kf = codes8_f16(*reinterpret_cast<const uint2*>(at.k_at(u, kk) + off));
+            else kf = *reinterpret_cast<const v4i*>(at.k_at(u, kk) + off);
 #pragma unroll
             for (int b = 0; b < MB; ++b) s[b][u] = mfma16<KT>(kf, qf[b][kk], s[b][u]);
         }
     }
     k_read();
+    if constexpr (FOLD) __builtin_amdgcn_s_setprio(0);
+    constexpr bool EARLY = FOLD && MB * (NA * DB + KK) <= 24;
+    uint2 vr[EARLY ? DB : 1][2];
+    auto read_v = [&](int d, uint2 (&v)[2]) {
+        if constexpr (I8) {
+            v[0] = read_tr8(at.v_at(0, d) + off);
+        } else {
+            v[0] = read_tr16(at.v_at(0, d) + off);
+            v[1] = read_tr16(at.v_at(1, d) + off);
+        }
+    };
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) read_v(d, vr[d]);
+    }
     v4i part[MB][PARTS];                                     // the weights are their sum
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
-        float p[8];
+        float p[8], by[8];                                   // by: what a score is multiplied by
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = s[b][e >> 2][e & 3] * sc[b];
-        if constexpr (I8) {
+        for (int e = 0; e < 8; ++e) by[e] = sc[b];
+        if constexpr (I8 && FOLD) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float4 ks = *reinterpret_cast<const float4*>(&kscale[4 * G + 16 * u]);
-                p[4 * u] *= ks.x; p[4 * u + 1] *= ks.y; p[4 * u + 2] *= ks.z; p[4 * u + 3] *= ks.w;
+                by[4 * u] *= ks.x; by[4 * u + 1] *= ks.y; by[4 * u + 2] *= ks.z; by[4 * u + 3] *= ks.w;
             }
         }
-        if (limit < kAttnTile) {
+        auto hide = [&]() {
+            if (limit < kAttnTile) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (4 * G + 16 * (e >> 2) + (e & 3) >= limit) p[e] = -INFINITY;
-        }
-        float top = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
-        if (__any(top > M[b] + kAttnSlack)) {
+                for (int e = 0; e < 8; ++e)
+                    if (4 * G + 16 * (e >> 2) + (e & 3) >= limit) p[e] = -INFINITY;
+            }
+        };
+        auto highest = [&]() {
+            return fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7])));
+        };
+        auto raise = [&](float top) {                        // M to at least `top` of any lane of the row
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const float m = fmaxf(M[b], top);
@@ -272,13 +319,47 @@ __device__ __forceinline__ void attn_tile(const uint8_t* kr, const uint8_t* vr, 
 #pragma unroll
                     for (int d = 0; d < DB; ++d) acc[b][i][d] = acc[b][i][d] * f;
             }
-        }
-        const float ref = M[b] - Kind::lift;
+        };
         float sum = 0.0f;
+        if constexpr (FOLD) {
+            auto less = [&]() {                              // the exponents of the weights
+                const float ref = M[b] - Kind::lift;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(p[e] - ref);
-            sum += p[e];
+                for (int e = 0; e < 8; ++e) p[e] = __builtin_fmaf(s[b][e >> 2][e & 3], by[e], -ref);
+                hide();
+            };
+            less();
+            if (__any(highest() > kAttnSlack + Kind::lift)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = s[b][e >> 2][e & 3] * by[e];
+                hide();
+                raise(highest());
+                less();
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] = __builtin_amdgcn_exp2f(p[e]);
+                sum += p[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = s[b][e >> 2][e & 3] * sc[b];
+            if constexpr (I8) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float4 ks = *reinterpret_cast<const float4*>(&kscale[4 * G + 16 * u]);
+                    p[4 * u] *= ks.x; p[4 * u + 1] *= ks.y; p[4 * u + 2] *= ks.z; p[4 * u + 3] *= ks.w;
+                }
+            }
+            hide();
+            const float top = highest();
+            if (__any(top > M[b] + kAttnSlack)) raise(top);
+            const float ref = M[b] - Kind::lift;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                p[e] = __builtin_amdgcn_exp2f(p[e] - ref);
+                sum += p[e];
+            }
         }
         L[b] += sum;
         if constexpr (I8) {
@@ -296,8 +377,9 @@ __device__ __forceinline__ void attn_tile(const uint8_t* kr, const uint8_t* vr, 
 #pragma unroll
             for (int i = 0; i < PARTS; ++i) {
                 const uint32_t h = narrow2<VT>(x, y);
-                const float2 back = widen2<VT>(h);
                 part[b][i][w] = (int)h;
+                if (i + 1 == PARTS) break;
+                const float2 back = widen2<VT>(h);
                 x -= back.x;
                 y -= back.y;
                 if (NA == 2 && i == Kind::each - 1) {
@@ -308,27 +390,23 @@ __device__ __forceinline__ void attn_tile(const uint8_t* kr, const uint8_t* vr, 
         }
     }
     v_ready();
+    if constexpr (FOLD) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
+        if constexpr (!EARLY) read_v(d, vr[0]);
+        const uint2 (&v)[2] = vr[EARLY ? d : 0];
         v4i vf;
-        if constexpr (I8) {
-            // row r of the eight: token 4 G + r of the first tile or 4 G + r - 4 of the second
-            const int r = i16 >> 1, row = 4 * G + (r & 3) + 16 * (r >> 2);
-            vf = codes8_bf16(read_tr8(vr + row * RB + ((d ^ Sh::swz(row)) << 4) + (i16 & 1) * 8));
-        } else {
-            const int row = 4 * G + (i16 >> 2), c = 2 * d + ((i16 >> 1) & 1);
-            const uint2 x = read_tr16(vr + row * RB + ((c ^ Sh::swz2(row)) << 4) + (i16 & 1) * 8);
-            const uint2 y = read_tr16(vr + (row + 16) * RB + ((c ^ Sh::swz2(row + 16)) << 4) + (i16 & 1) * 8);
-            vf = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
-        }
+        if constexpr (I8) vf = codes8_bf16(v[0]);
+        else vf = v4i{(int)v[0].x, (int)v[0].y, (int)v[1].x, (int)v[1].y};
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
+        for (int i = 0; i < PARTS; ++i)
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
+            for (int b = 0; b < MB; ++b) {
                 f32x4v& sum = acc[b][i / Kind::each < NA ? i / Kind::each : NA - 1][d];
                 sum = mfma16<VT>(vf, part[b][i], sum);
             }
     }
+    if constexpr (FOLD) __builtin_amdgcn_s_setprio(0);
     v_read();
 }
 
@@ -513,11 +591,12 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         issue_k();
         issue_v();
     }
+    const AttnLane<I8, D> at(kring, vring);
     for (int t = wave; t < tiles; t += NW) {
         const bool more = t + NW < tiles;
         wait_vmcnt<NL>();                                    // K of this tile; V came after it
-        attn_tile<DT, I8, D, 1, WP>(
-            kring, vring, qf, sc, &kscale[I8 ? t * kAttnTile : 0], &vscale[I8 ? t * kAttnTile : 0], ve,
+        attn_tile<DT, I8, D, 1, WP, false>(
+            at, 0, qf, sc, &kscale[I8 ? t * kAttnTile : 0], &vscale[I8 ? t * kAttnTile : 0], ve,
             n - t * kAttnTile, t == wave, Ms, Ls, acc,
             [&] {
                 asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // K is read: its place is free

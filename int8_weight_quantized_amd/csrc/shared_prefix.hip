@@ -291,11 +291,12 @@ __device__ __forceinline__ void prefix_walk(const PrefixArgs& a, const PrefixWor
             issue_k();
             issue_v();
         }
+        const AttnLane<I8, D> at(kring, vring);
         for (int t = wave; t < tiles; t += NW) {
             const bool more = t + NW < tiles;
             wait_vmcnt<NL>();                                // K of this tile; V came after it
-            attn_tile<DT, I8, D, 1, kPrefixParts>(
-                kring, vring, qf, sc, &sh.kscale[I8 ? t * kAttnTile : 0], &sh.vscale[I8 ? t * kAttnTile : 0], ve,
+            attn_tile<DT, I8, D, 1, kPrefixParts, false>(
+                at, 0, qf, sc, &sh.kscale[I8 ? t * kAttnTile : 0], &sh.vscale[I8 ? t * kAttnTile : 0], ve,
                 w.n - t * kAttnTile, t == wave, M, L, acc,
                 [&] {
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); // K is read: its place is free
@@ -414,7 +415,9 @@ __device__ __forceinline__ void prefix_share(const PrefixArgs& a, const PrefixWo
     int ve = -300;                                           // value scales are taken relative to 2^ve: none yet
     __syncthreads();
     issue(0);
-    for (int t = 0; t < tiles; ++t) {
+    const AttnLane<I8, D> at(sh.ring, sh.ring + T * RB);
+    auto tile = [&](int t, auto odd) {
+        constexpr int place = decltype(odd)::value ? 2 * T * RB : 0;
         wait_vmcnt<0>();
         __syncthreads();                                     // the tile has landed, the one before it is read
         if (t % TS == 0 && t > 0 && (t / TS + 1) * kPrefixSeg < end) fill(t / TS + 1);
@@ -437,18 +440,20 @@ __device__ __forceinline__ void prefix_share(const PrefixArgs& a, const PrefixWo
                 }
             }
         }
-        if (busy) {
-#pragma unroll 1
-            for (int u = 0; u < T / kAttnTile; ++u) {
-                const int limit = w.n - t * T - u * kAttnTile;
-                if (limit <= 0) break;
-                const uint8_t* const kr = sh.ring + (t & 1) * (2 * T * RB) + u * (kAttnTile * RB);
-                const int at = t % (2 * TS) * T + u * kAttnTile;
-                attn_tile<DT, I8, D, MB, kPrefixParts>(kr, kr + T * RB, qf, sc, &sh.kscale[I8 ? at : 0], &sh.vscale[I8 ? at : 0],
-                                                       ve, limit, t + u == 0, M, L, acc, [] {}, [] {}, [] {});
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        if (!busy) return;
+#pragma unroll
+        for (int u = 0; u < T / kAttnTile; ++u) {
+            const int limit = w.n - t * T - u * kAttnTile, from = t % (2 * TS) * T + u * kAttnTile;
+            if (limit <= 0) break;
+            attn_tile<DT, I8, D, MB, kPrefixParts, true>(at, place + u * (kAttnTile * RB), qf, sc, &sh.kscale[I8 ? from : 0],
+                                                         &sh.vscale[I8 ? from : 0], ve, limit, t + u == 0, M, L, acc,
+                                                         [] {}, [] {}, [] {});
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    };
+    for (int t = 0; t < tiles; t += 2) {
+        tile(t, BoolTag<false>{});
+        if (t + 1 < tiles) tile(t + 1, BoolTag<true>{});
     }
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
@@ -490,69 +495,53 @@ __global__ __launch_bounds__(256, 2) void shared_prefix_kernel(PrefixArgs a)
     else if constexpr (D <= 128) prefix_share<DT, I8, D, 2>(a, w, sh);
 }
 
-// Joins the chunks of one sequence and head, those of its prefix and its own:
-// a lane has four elements of the values, P groups of lanes each add every
-// P-th chunk (four at a time, under a running M), and their sums are added in
-// LDS, all in an order that the sizes fix.
+// Joins the chunks of a sequence and head, those of its prefix and its own, one
+// wave for each: a lane has four elements of the values, P groups of lanes
+// each add every P-th chunk (four at a time, under a running M), and then theirs,
+// all in an order that the sizes fix.  Each wave looks through starts itself.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void shared_prefix_join_kernel(PrefixArgs a)
 {
-    constexpr int C = D / 4;                                 // lanes that hold the values, four each
-    constexpr int P = 256 / C;                               // chunks added side by side
+    constexpr int C = D <= 128 ? D / 4 : D / 8, V = D / 4 / C;       // lanes that hold the values, 16-byte pieces of each
+    constexpr int P = 64 / C;                                // chunks added side by side
     constexpr int U = 4;
-    __shared__ f32x4v sums[P][C];
-    __shared__ float ms[P], ls[P];
-    const int tid = threadIdx.x, c = tid % C, g = tid / C;
-    const int64_t bh = blockIdx.x;
+    const int lane = threadIdx.x & 63, c = lane % C, g = lane / C;
+    const int64_t bh = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (bh >= (int64_t)a.batch * a.hq) return;
     const int h = (int)(bh % a.hq);
     const int64_t b = bh / a.hq;
     // Its prefix: as many entries of starts as are not past b, less one.
-    int before = 0, wrong = 0;
-    if (a.prefixes > 0) {
-        for (int i = tid; i <= a.prefixes; i += 256) {
-            const int s = a.starts[i];
-            before += s <= b;
-            wrong |= s < 0 || s > a.batch || (i > 0 && s < a.starts[i - 1]);
-        }
-        wrong = __syncthreads_or(wrong);
-        if (a.prefixes < 256) {
-            before = __syncthreads_count(before);
-        } else {
-            __shared__ int total;
-            if (tid == 0) total = 0;
-            __syncthreads();
-            if (before) atomicAdd(&total, before);
-            __syncthreads();
-            before = total;
-        }
+    int before = 0;
+    bool wrong = false;
+    for (int base = 0; base <= a.prefixes && a.prefixes > 0; base += 64) {
+        const int i = base + lane;
+        const bool in = i <= a.prefixes;
+        const int s = in ? a.starts[i] : 0;
+        before += __popcll(__ballot(in && s <= b));
+        wrong |= __any(in && (s < 0 || s > a.batch || (i > 0 && s < a.starts[i - 1])));
     }
     const int p = before - 1;
     const int64_t np = p < 0 || p >= a.prefixes ? 0 : min(max((int64_t)a.plens[p], (int64_t)0), a.pcap);
     const int64_t no = min(max((int64_t)a.lens[b], (int64_t)0), a.cap);
-    const int shared = (int)((np + a.pchunk - 1) / a.pchunk), count = shared + (int)((no + a.chunk - 1) / a.chunk);
+    const int shared = (int)((np + a.pchunk - 1) / a.pchunk), count = wrong ? 0 : shared + (int)((no + a.chunk - 1) / a.chunk);
     const int64_t slots = a.psplits + a.splits;
     const float2* const ml = a.part_ml + bh * slots;
     const float* const part = a.part + bh * slots * D + 4 * c;
-    uint16_t* const out = a.out + b * a.o_bs + h * a.o_hs;
-    if (count == 0 || wrong) {
-        if (tid < C) {
-            const uint32_t v = wrong ? kNan2<DT> : 0u;
-            *reinterpret_cast<uint2*>(out + 4 * tid) = make_uint2(v, v);
-        }
-        return;
-    }
     float m = kAttnLow, l = 0.0f;
-    f32x4v o = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4v o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
     for (int s0 = g; g < P && s0 < count; s0 += P * U) {
         float2 x[U];
-        f32x4v v[U];
+        f32x4v f[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + P * u;
             if (s < count) {
                 const int64_t slot = s < shared ? s : a.psplits + (s - shared);
                 x[u] = ml[slot];
-                v[u] = *reinterpret_cast<const f32x4v*>(part + slot * D);
+#pragma unroll
+                for (int v = 0; v < V; ++v) f[u][v] = *reinterpret_cast<const f32x4v*>(part + slot * D + 4 * C * v);
             }
         }
         float top = m;
@@ -562,44 +551,48 @@ __global__ __launch_bounds__(256) void shared_prefix_join_kernel(PrefixArgs a)
         const float old = __builtin_amdgcn_exp2f(m - top);
         m = top;
         l *= old;
-        o = o * old;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = o[v] * old;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + P * u < count) {
-                const float f = __builtin_amdgcn_exp2f(x[u].x - m);
-                l = __builtin_fmaf(f, x[u].y, l);
+                const float w = __builtin_amdgcn_exp2f(x[u].x - m);
+                l = __builtin_fmaf(w, x[u].y, l);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, v[u][r], o[r]);
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[v][r] = __builtin_fmaf(w, f[u][v][r], o[v][r]);
             }
         }
     }
-    if (g < P) {
-        sums[g][c] = o;
-        if (c == 0) {
-            ms[g] = m;
-            ls[g] = l;
-        }
+    // the groups' sums, in their order, in every group
+    float high = m;
+#pragma unroll
+    for (int i = 0; i < P; ++i) high = fmaxf(high, __shfl(m, i * C));
+    const float w = __builtin_amdgcn_exp2f(m - high);        // a group without chunks: 0
+    float sum = 0.0f;
+    f32x4v t[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) t[v] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        sum += __shfl(l * w, i * C);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[v][r] += __shfl(o[v][r] * w, i * C + c);
     }
-    __syncthreads();
-    if (tid < C) {
-        m = ms[0];
+    if (g != 0) return;
+    uint16_t* const out = a.out + b * a.o_bs + h * a.o_hs + 4 * c;
+    const float inv = 1.0f / sum;
 #pragma unroll
-        for (int i = 1; i < P; ++i) m = fmaxf(m, ms[i]);
-        o = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-        l = 0.0f;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float f = __builtin_amdgcn_exp2f(ms[i] - m);   // a group without chunks: 0
-            l = __builtin_fmaf(f, ls[i], l);
-            const f32x4v q = sums[i][tid];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(f, q[r], o[r]);
-        }
-        const float inv = 1.0f / l;
-        uint2 w;
-        w.x = narrow2<DT>(o[0] * inv, o[1] * inv);
-        w.y = narrow2<DT>(o[2] * inv, o[3] * inv);
-        *reinterpret_cast<uint2*>(out + 4 * tid) = w;
+    for (int v = 0; v < V; ++v) {
+        uint2 y;
+        y.x = narrow2<DT>(t[v][0] * inv, t[v][1] * inv);
+        y.y = narrow2<DT>(t[v][2] * inv, t[v][3] * inv);
+        if (wrong) y = make_uint2(kNan2<DT>, kNan2<DT>);
+        else if (count == 0) y = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(out + 4 * C * v) = y;
     }
 }
 
@@ -746,6 +739,6 @@ extern "C" ck_status ck_shared_prefix_attention(const ck_prefix_args* args, cons
     const void* join = f16 ? prefix_join_fn<CK_DT_FP16>(d) : prefix_join_fn<CK_DT_BF16>(d);
     void* kargs[] = {&a};
     if ((s = launch(fn, (unsigned)plan.blocks, 256, kargs, stream, "shared_prefix_attention")) != CK_OK) return s;
-    if ((s = launch(join, (unsigned)(p.batch * p.hq), 256, kargs, stream, "shared_prefix_join")) != CK_OK) return s;
+    if ((s = launch(join, (unsigned)cdiv(p.batch * p.hq, 4), 256, kargs, stream, "shared_prefix_join")) != CK_OK) return s;
     return ok();
 }
