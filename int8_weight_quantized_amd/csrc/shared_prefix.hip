@@ -497,14 +497,14 @@ __global__ __launch_bounds__(256, 2) void shared_prefix_kernel(PrefixArgs a)
 
 // Joins the chunks of a sequence and head, those of its prefix and its own, one
 // wave for each: a lane has four elements of the values, P groups of lanes
-// each add every P-th chunk (four at a time, under a running M), and then theirs,
+// each add every P-th chunk (eight at a time, under a running M), and then theirs,
 // all in an order that the sizes fix.  Each wave looks through starts itself.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void shared_prefix_join_kernel(PrefixArgs a)
 {
     constexpr int C = D <= 128 ? D / 4 : D / 8, V = D / 4 / C;       // lanes that hold the values, 16-byte pieces of each
     constexpr int P = 64 / C;                                // chunks added side by side
-    constexpr int U = 4;
+    constexpr int U = 8;
     const int lane = threadIdx.x & 63, c = lane % C, g = lane / C;
     const int64_t bh = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (bh >= (int64_t)a.batch * a.hq) return;
@@ -604,11 +604,14 @@ struct PrefixPlan {
     int64_t bytes;
 };
 
-// Chunks.  A prefix's are as long as two blocks a CU allow in one round, or in
-// as many whole rounds as waste least (a round of blocks takes as long as its
-// chunk and a fixed part), and 128 tokens at least; where groups have up to 16
-// rows on average 1024 at most, which the form for few rows takes.  Sequences'
-// own chunks follow the rule of paged_attention.hip.
+// Chunks.  A prefix's are of such a length that the blocks take the least time,
+// where a round of up to two blocks a CU takes as long as its chunk, a fixed part
+// and its rows' sums, which are written and read; up to one block a CU run
+// half as fast again.  (128 sequences behind 65536 tokens: 512 blocks 402 us, 256
+// blocks 602; 48 behind three int8 prefixes: 512 blocks 61 us, 256 blocks 56; 24
+// behind 20000 tokens at head_dim 256: 42 and 39.)  At least 128 tokens, and where
+// groups have up to 16 rows on average 1024 at most, which the form for few rows
+// takes.  Sequences' own chunks follow the rule of paged_attention.hip.
 bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_dim, int64_t prefixes,
                  int64_t pcap, int64_t cap)
 {
@@ -621,10 +624,12 @@ bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t h
         p.prows = cdiv(batch * group, prefix_rows((int)head_dim)) + used - 1;
         const int64_t pairs = p.prows * hk, most = batch * group <= 16 * used ? kAttnChunk : int64_t(1) << 30;
         int64_t least = INT64_MAX;
-        for (int64_t r = 1; r <= 8; ++r) {
-            const int64_t s = std::max<int64_t>(1, r * round / pairs);
+        for (int64_t r = 1; r <= 16; r += r < 2 ? 1 : 2) {   // half a round, and whole ones
+            const int64_t s = std::max<int64_t>(1, r * kNumCUs / pairs);
             const int64_t chunk = std::min(most, cdiv(cdiv(pcap, s), 128) * 128);
-            const int64_t time = cdiv(pairs * cdiv(pcap, chunk), round) * (chunk + 128);
+            const int64_t n = pairs * cdiv(pcap, chunk), rest = n % round;
+            const int64_t each = chunk + 128 + 2 * prefix_rows((int)head_dim);
+            const int64_t time = n / round * each + (rest > kNumCUs ? each : rest > 0 ? each * 2 / 3 : 0);
             if (time < least) least = time, p.pchunk = chunk;
         }
         p.psplits = cdiv(pcap, p.pchunk);
