@@ -11,15 +11,16 @@
 // digits.  A masked logit has e^d = 0 and d = -inf: d is cut at -10^4 in W.
 //
 // The alternatives, k of them, cost the pass over the logits nothing: of the
-// 256 lanes' maxima the k-th is a bound that k logits reach, and those that do
+// maxima of 256 lanes (or groups of four) the k-th is a bound that k logits reach, and those that do
 // are in lanes whose maximum does, few more than k of them.  The logits of these
 // lanes are read again and what reaches the bound is ranked, as 64-bit keys
 // (value, then lowest index), each by how many others are larger.  Where too
 // many reach it (rows of equal logits, masks that leave fewer than k) the waves
 // go through all logits again with a sorted list each.
 //
-// A block takes a row, or a chunk of it where there are few rows; a second
-// launch joins the chunks.
+// A block of four waves takes a row, or a chunk of it where there are few rows;
+// a second launch joins the chunks.  Where that launch would cost more than the
+// chunks save, 16 waves take the row.
 
 struct LogprobArgs {
     const void* logits;
@@ -187,12 +188,12 @@ struct Candidates {
         if (at < kLogprobKeys) keys[at] = key;
     }
     // take(place, key) for the largest `top` of them, by the block's threads.
-    template <class Take>
+    template <int T, class Take>
     __device__ __forceinline__ void rank(int top, Take take)
     {
         if (threadIdx.x == 0) keys[count] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < count; i += 256) {
+        for (int i = threadIdx.x; i < count; i += T) {
             const u64 k = keys[i];
             int place = 0;
             for (int j = 0; j < count; j += 2) {
@@ -204,14 +205,15 @@ struct Candidates {
     }
 };
 
-template <int DT, bool TOP>
-__global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
+template <int DT, bool TOP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void token_logprobs_kernel(LogprobArgs a)
 {
     constexpr int E = DT == CK_OUT_FP32 ? 4 : 8, B = kLogprobBatch;   // logits of a load, loads of a batch
-    __shared__ LogSums sums[4];
+    constexpr int T = 64 * WAVES;
+    __shared__ LogSums sums[WAVES];
     __shared__ Candidates cand;
     __shared__ uint32_t highs[TOP ? 256 : 4];
-    __shared__ uint8_t owners[TOP ? 256 : 4];
+    __shared__ uint16_t owners[TOP ? T : 4];
     __shared__ int owning;
     __shared__ float bound;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -231,13 +233,13 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
 
     float m = kLogLow, s = 0.0f, w = 0.0f, top = -INFINITY;  // top: the largest, -inf too
     bool any = false;
-    // One batch: pieces p + 256 j + tid, n of them left.
+    // One batch: pieces p + T j + tid, n of them left.
     auto take = [&](const v4i (&v)[B], int n) {
         float x[B][E], high = -INFINITY;
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             widen_logits<DT, E>(v[j], x[j]);
-            if (256 * j + tid >= n) {
+            if (T * j + tid >= n) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[j][e] = -INFINITY;
             }
@@ -267,14 +269,14 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
     auto load = [&](v4i (&to)[B], int p) {
 #pragma unroll
         for (int j = 0; j < B; ++j)
-            if (p + 256 * j + tid < p1) to[j] = vec[p + 256 * j + tid];
+            if (p + T * j + tid < p1) to[j] = vec[p + T * j + tid];
     };
     load(v, p0);
     float given = 0.0f;
     if (tid == 0 && a.splits == 1) given = token_logit<DT>(a, row);
     any = p0 + tid < p1;
-    for (int p = p0; p < p1; p += 256 * B) {
-        load(next, p + 256 * B);
+    for (int p = p0; p < p1; p += T * B) {
+        load(next, p + T * B);
         take(v, p1 - p);
 #pragma unroll
         for (int j = 0; j < B; ++j) v[j] = next[j];
@@ -296,7 +298,14 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
         // bit by the first wave, as many bits as it takes until k reach it and no
         // more, or as the type has (of fp32 20).  (Lanes without a logit, 0, are among them only in a small chunk,
         // which has few logits: no bound then.)
-        highs[tid] = any ? order_key(top) : 0;
+        uint32_t high = any ? order_key(top) : 0;
+        if constexpr (WAVES == 16) {                         // of four lanes together
+            high = max(high, (uint32_t)__builtin_amdgcn_mov_dpp((int)high, 0xb1, 0xf, 0xf, false));
+            high = max(high, (uint32_t)__builtin_amdgcn_mov_dpp((int)high, 0x4e, 0xf, 0xf, false));
+            if (lane % 4 == 0) highs[tid / 4] = high;
+        } else {
+            highs[tid] = high;
+        }
         if (tid == 0) {
             cand.count = 0;
             owning = 0;
@@ -316,12 +325,12 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
         }
         __syncthreads();
         const float least = bound;
-        if (any && top >= least) owners[atomicAdd(&owning, 1)] = (uint8_t)tid;
+        if (any && top >= least) owners[atomicAdd(&owning, 1)] = (uint16_t)tid;
         __syncthreads();
         // The logits of the lanes that reach it.
-        const int rounds = (p1 - p0 + 255) / 256, total = owning * rounds;
-        for (int q = tid; q < total; q += 256) {
-            const int i = q / owning, p = p0 + 256 * i + owners[q - i * owning];
+        const int rounds = (p1 - p0 + T - 1) / T, total = owning * rounds;
+        for (int q = tid; q < total; q += T) {
+            const int i = q / owning, p = p0 + T * i + owners[q - i * owning];
             if (p >= p1) continue;
             float x[E];
             widen_logits<DT, E>(vec[p], x);
@@ -334,12 +343,14 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
             if (x >= least) cand.add(top_key(x, (uint32_t)few));
         }
         // Too many, or a NaN (which maxima pass over; +inf makes a sum one too).
-        const bool nan = sums[0].s != sums[0].s || sums[1].s != sums[1].s || sums[2].s != sums[2].s || sums[3].s != sums[3].s;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) nan |= sums[i].s != sums[i].s;
         __syncthreads();
         if (cand.count > kLogprobKeys || nan) {
             TopList list{0, 0};
             if (__any(few >= 0)) list.offer(few >= 0 ? top_key(logit_at<DT>(base, few), (uint32_t)few) : 0, a.top);
-            for (int p = p0 + 64 * wave; p < p1; p += 256) {
+            for (int p = p0 + 64 * wave; p < p1; p += T) {
                 float x[E];
                 if (p + lane < p1) widen_logits<DT, E>(vec[p + lane], x);
 #pragma unroll
@@ -355,8 +366,8 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
     } else {
         __syncthreads();
     }
-    const LogSums t = join_sums(lane < 4 ? sums[lane] : LogSums{0.0, 0.0, kLogLow});
-    if (a.splits > 1) {
+    const LogSums t = join_sums(lane < WAVES ? sums[lane] : LogSums{0.0, 0.0, kLogLow});
+    if (WAVES == 4 && a.splits > 1) {
         const int64_t at = row * a.splits + split;
         if (tid == 0) {
             a.sums[at] = make_double2(t.s, t.w);
@@ -364,14 +375,14 @@ __global__ __launch_bounds__(256) void token_logprobs_kernel(LogprobArgs a)
         }
         if constexpr (TOP) {
             if (tid >= cand.count && tid < a.top) a.keys[at * a.top + tid] = 0;
-            cand.rank(a.top, [&](int place, u64 key) { a.keys[at * a.top + place] = key; });
+            cand.template rank<T>(a.top, [&](int place, u64 key) { a.keys[at * a.top + place] = key; });
         }
         return;
     }
     const double logs = log(t.s);
     if (tid == 0) write_row(a, row, given, t, logs);
     if constexpr (TOP) {
-        cand.rank(a.top, [&](int place, u64 key) { write_top(a, row * a.top + place, key, t, logs); });
+        cand.template rank<T>(a.top, [&](int place, u64 key) { write_top(a, row * a.top + place, key, t, logs); });
     }
 }
 
@@ -408,33 +419,40 @@ __global__ __launch_bounds__(256) void token_logprobs_join_kernel(LogprobArgs a)
     if (tid == 0) write_row(a, row, given, t, logs);
     if (a.top == 0) return;
     __syncthreads();
-    cand.rank(a.top, [&](int place, u64 key) { write_top(a, row * a.top + place, key, t, logs); });
+    cand.rank<256>(a.top, [&](int place, u64 key) { write_top(a, row * a.top + place, key, t, logs); });
 }
 
 namespace {
 
 constexpr int64_t kLogprobTop = 64;
+constexpr int64_t kLogprobWide = 32768;  // logits of a row for one block of 16 waves
 
 struct LogprobPlan {
-    int64_t splits, bytes;
+    int64_t waves, splits, bytes;
 };
 
-// Chunks of a row: as many as give every CU two blocks, of 4096 logits at
-// least, and so few that their lists can be ranked by counting.
+// Rows of 4097 to 32768 logits, at most one a CU: 16 waves each, one launch (us
+// with five alternatives, in bf16, against chunks: 1x32000 9.6 and 10.4, 48x32000
+// 10.3 and 11.8, 200x8192 10.5 and 11.6; 1x50000 12.3 and 10.9).  Else chunks of
+// a row: as many as give every CU two blocks, of 4096 logits at least, and so
+// few that their lists can be ranked by counting.
 LogprobPlan logprob_plan(int64_t rows, int64_t vocab, int64_t top)
 {
-    LogprobPlan p{1, 0};
-    if (rows > 0) p.splits = std::min(std::min<int64_t>(2 * kNumCUs / rows, cdiv(vocab, 4096)), kLogprobKeys / std::max<int64_t>(top, 16));
+    LogprobPlan p{4, 1, 0};
+    if (rows <= kNumCUs && vocab > 4096 && vocab <= kLogprobWide) p.waves = 16;
+    else if (rows > 0) p.splits = std::min(std::min<int64_t>(2 * kNumCUs / rows, cdiv(vocab, 4096)), kLogprobKeys / std::max<int64_t>(top, 16));
     p.splits = std::max<int64_t>(p.splits, 1);
     if (p.splits > 1) p.bytes = rows * p.splits * (16 + 8 * top + 4);
     return p;
 }
 
 template <int DT>
-const void* logprob_fn(bool top)
+const void* logprob_fn(bool top, bool wide)
 {
-    return top ? reinterpret_cast<const void*>(&token_logprobs_kernel<DT, true>)
-               : reinterpret_cast<const void*>(&token_logprobs_kernel<DT, false>);
+    return wide ? top ? reinterpret_cast<const void*>(&token_logprobs_kernel<DT, true, 16>)
+                      : reinterpret_cast<const void*>(&token_logprobs_kernel<DT, false, 16>)
+           : top ? reinterpret_cast<const void*>(&token_logprobs_kernel<DT, true, 4>)
+                 : reinterpret_cast<const void*>(&token_logprobs_kernel<DT, false, 4>);
 }
 
 }  // namespace
@@ -473,15 +491,15 @@ extern "C" ck_status ck_token_logprobs(const ck_logprob_args* args, hipStream_t 
                   p.ld, p.rows, (int)p.vocab, (int)p.top, (int)plan.splits};
     a.keys = (unsigned long long*)(a.sums + p.rows * plan.splits);
     a.refs = (float*)(a.keys + p.rows * plan.splits * p.top);
-    const bool top = p.top > 0;
-    const void* const fn = p.dtype == CK_OUT_FP32   ? logprob_fn<CK_OUT_FP32>(top)
-                           : p.dtype == CK_OUT_FP16 ? logprob_fn<CK_OUT_FP16>(top)
-                                                    : logprob_fn<CK_OUT_BF16>(top);
+    const bool top = p.top > 0, wide = plan.waves == 16;
+    const void* const fn = p.dtype == CK_OUT_FP32   ? logprob_fn<CK_OUT_FP32>(top, wide)
+                           : p.dtype == CK_OUT_FP16 ? logprob_fn<CK_OUT_FP16>(top, wide)
+                                                    : logprob_fn<CK_OUT_BF16>(top, wide);
     const void* const join = p.dtype == CK_OUT_FP32   ? reinterpret_cast<const void*>(&token_logprobs_join_kernel<CK_OUT_FP32>)
                              : p.dtype == CK_OUT_FP16 ? reinterpret_cast<const void*>(&token_logprobs_join_kernel<CK_OUT_FP16>)
                                                       : reinterpret_cast<const void*>(&token_logprobs_join_kernel<CK_OUT_BF16>);
     void* kargs[] = {&a};
-    if ((s = launch(fn, (unsigned)(p.rows * plan.splits), 256, kargs, stream, "token_logprobs")) != CK_OK) return s;
+    if ((s = launch(fn, (unsigned)(p.rows * plan.splits), (unsigned)plan.waves * 64, kargs, stream, "token_logprobs")) != CK_OK) return s;
     if (plan.splits > 1 && (s = launch(join, (unsigned)p.rows, 256, kargs, stream, "token_logprobs_join")) != CK_OK) return s;
     return ok();
 }

@@ -40,6 +40,12 @@ def _workspace(n, like, what):
     return like.new_empty(n, dtype=(_torch or _load_torch()).uint8) if n else None
 
 
+def _fine(workspace, device):
+    """Whether workspace is None or a tensor as they have to be."""
+    return workspace is None or (workspace.dtype is _torch.uint8 and workspace.device == device
+                                 and workspace.is_contiguous())
+
+
 def _need_workspace(workspace, device):
     _ck._need(workspace, (_torch or _load_torch()).uint8, "workspace", device)
     if not workspace.is_contiguous():
@@ -89,7 +95,7 @@ def shared_prefix_attention(q, cache, prefix_table, prefix_lens, starts, table, 
                 and prefix_table.device == dev and (ps[1] == 1 or pwidth <= 1) and prefix_lens.dtype is i32
                 and prefix_lens.device == dev and prefix_lens.shape == (prefixes,) and prefix_lens.is_contiguous()
                 and starts.dtype is i32 and starts.device == dev and starts.shape == (prefixes + 1,)
-                and starts.is_contiguous() and out is None and workspace is None)
+                and starts.is_contiguous() and out is None and _fine(workspace, dev))
     except (AttributeError, TypeError, ValueError, IndexError):
         good = False
     if not good:
@@ -180,7 +186,7 @@ def lora_add(y, x, weight, ids, out=None, workspace=None):
         good = (y.is_cuda and tt in _code and (ys[1] == 1 or n <= 1) and type(weight) is LoraWeight
                 and weight.device == dev and x.dtype is weight.dtype and x.device == dev and rows == m and n == weight.n
                 and k == weight.k and (xs[1] == 1 or k <= 1) and ids.dtype is torch.int32 and ids.device == dev
-                and ids.shape == (m,) and ids.is_contiguous() and (out is None or out is y) and workspace is None)
+                and ids.shape == (m,) and ids.is_contiguous() and (out is None or out is y) and _fine(workspace, dev))
     except (AttributeError, TypeError, ValueError, IndexError):
         good = False
     if not good:
@@ -245,7 +251,7 @@ def token_logprobs(logits, tokens=None, top: int = 0, workspace=None):
     torch = _torch or _load_torch()
     try:
         tt, dev, (rows, vocab), ls = logits.dtype, logits.device, logits.shape, logits.stride()
-        good = logits.is_cuda and tt in _code and (ls[1] == 1 or vocab <= 1) and workspace is None and top >= 0
+        good = logits.is_cuda and tt in _code and (ls[1] == 1 or vocab <= 1) and _fine(workspace, dev) and top >= 0
         if tokens is not None:
             good = (good and tokens.dtype is torch.int64 and tokens.device == dev and tokens.shape == (rows,)
                     and tokens.is_contiguous())
@@ -256,15 +262,16 @@ def token_logprobs(logits, tokens=None, top: int = 0, workspace=None):
     if workspace is None:
         workspace = token_logprobs_workspace(logits, top)
     wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    # one allocation for the fp32 outputs: log probabilities, entropies, alternatives
-    values = logits.new_empty((2 + top) * rows, dtype=torch.float32)
+    f32 = torch.float32
+    logprob = None if tokens is None else logits.new_empty(rows, dtype=f32)
+    entropy = logits.new_empty(rows, dtype=f32)
     ids = logits.new_empty((rows, top), dtype=torch.int64)
-    at = values.data_ptr()
-    args = _LOGPROB.pack(logits.data_ptr(), 0 if tokens is None else tokens.data_ptr(), 0 if tokens is None else at,
-                         at + 4 * rows, ids.data_ptr(), at + 8 * rows, wp, wn, ls[0], rows, vocab, top, _code[tt], 0)
+    best = logits.new_empty((rows, top), dtype=f32)
+    args = _LOGPROB.pack(logits.data_ptr(), 0 if tokens is None else tokens.data_ptr(),
+                         0 if tokens is None else logprob.data_ptr(), entropy.data_ptr(), ids.data_ptr(),
+                         best.data_ptr(), wp, wn, ls[0], rows, vocab, top, _code[tt], 0)
     _decode._launch(_ck.ck_token_logprobs, dev.index, args)
-    return TokenLogprobs(None if tokens is None else values[:rows], values[rows:2 * rows], ids,
-                         values[2 * rows:].view(rows, top))
+    return TokenLogprobs(logprob, entropy, ids, best)
 
 
 def _check_logprobs(logits, tokens, top, workspace):
