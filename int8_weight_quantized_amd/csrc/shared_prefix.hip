@@ -65,6 +65,13 @@ struct PrefixWork {
     int n, rows, row0, seq0, kvh, slot;
 };
 
+// The tokens of a chunk that begins at `first`, of `len` or as many as the table
+// can name; 0 for any negative length.
+__device__ __forceinline__ int prefix_tokens(int32_t len, int64_t cap, int64_t first, int chunk)
+{
+    return (int)max<int64_t>(min<int64_t>(chunk, min<int64_t>(len, cap) - first), 0);
+}
+
 // False if there is nothing to do.
 template <int ROWS>
 __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
@@ -79,7 +86,7 @@ __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
         w.rows = min(16, a.group - w.row0);
         w.table = a.table + w.seq0 * a.table_stride;
         w.first = (int64_t)split * a.chunk;
-        w.n = (int)min<int64_t>(a.chunk, min((int64_t)a.lens[w.seq0], a.cap) - w.first);
+        w.n = prefix_tokens(a.lens[w.seq0], a.cap, w.first, a.chunk);
         w.slot = a.psplits + split;
         return w.n > 0;
     }
@@ -125,7 +132,7 @@ __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
     w.rows = __builtin_amdgcn_readfirstlane(w.rows);
     w.table = a.ptable + p * a.pt_stride;
     w.first = (int64_t)w.slot * a.pchunk;
-    w.n = (int)min<int64_t>(a.pchunk, min((int64_t)a.plens[p], a.pcap) - w.first);
+    w.n = prefix_tokens(a.plens[p], a.pcap, w.first, a.pchunk);
     return w.n > 0;
 }
 

@@ -161,6 +161,58 @@ def test_prefix_cache_without_pages_and_lens_outside(cache):
     check_prefix(q, c, pt, i32(1000, -5), starts, table, i32(-3, 1 << 30, 7))
 
 
+def test_prefix_lowest_lengths():
+    """The lowest int32 as a length is 0 for every chunk, of a prefix and of a sequence."""
+    q, c, pt, pl, starts, table, lens = prefix_inputs([3000, 3000], [0, 20, 22], [2000] * 24, 8, 2, 128, "bf16", "bf16", 16)
+    low = -(1 << 31)
+    for i in (0, 20, 23):
+        few = lens.clone()
+        few[i] = low
+        check_prefix(q[[i]], c, pt, pl, starts.clamp(0, 0), table[[i]], few[[i]])
+    check_prefix(q, c, pt, torch.tensor([low, 3000], dtype=torch.int32, device=q.device), starts, table, lens)
+    few = torch.full_like(lens, low)
+    none = ck.shared_prefix_attention(q, c, pt, torch.full_like(pl, low), starts, table, few)
+    assert (none == 0).all()
+
+
+@pytest.mark.parametrize("prefixes,sequences", [(70, 200), (300, 90), (65, 64)])
+def test_prefix_many(prefixes, sequences):
+    """More prefixes than a wave has lanes, groups of none to many sequences."""
+    g = torch.Generator().manual_seed(prefixes)
+    starts = torch.sort(torch.randint(0, sequences + 1, (prefixes + 1,), generator=g)).values.tolist()
+    prefix = torch.randint(0, 150, (prefixes,), generator=g).tolist()
+    lens = torch.randint(0, 40, (sequences,), generator=g).tolist()
+    check_prefix(*prefix_inputs(prefix, starts, lens, 12, 2, 64, "bf16", "bf16", 16))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("members", [17, 66])
+def test_prefix_long_chunks(cache, members):
+    """So many heads that a block goes through well over 1024 tokens; of an int8 cache scales that rise and fall by
+    powers of two along the way; a bad page late in such a chunk."""
+    hk, n = 256, 3000
+    q, c, pt, pl, starts, table, lens = prefix_inputs([n], [0, members], [3] * members, hk, hk, 64, "bf16", cache, 8)
+    pick = [0, 100, 255]
+    steps = [[0] * 6] if cache == "bf16" else [[0, 12, -12, 5, 20, 3], [20, 3, -20, -40, 8, 0], [-40, -41, -30, -30, -28, -10]]
+    for ups in steps:
+        if cache == "int8":
+            vs = c.v_scale.clone()
+            for i, up in enumerate(ups):
+                at = pt[0, i * 64:(i + 1) * 64].long()
+                vs[at] *= 2.0 ** up
+            now = ck.KVCache(c.k, c.v, c.k_scale, vs)
+            some = ck.KVCache(*(t[:, pick].contiguous() for t in (c.k, c.v, c.k_scale, vs)))
+        else:
+            now, some = c, ck.KVCache(c.k[:, pick].contiguous(), c.v[:, pick].contiguous())
+        out = ck.shared_prefix_attention(q, now, pt, pl, starts, table, lens)
+        want, slack = ref.shared_prefix(q[:, pick], some, pt, pl, starts, table, lens, 64 ** -0.5)
+        ref.assert_within(out[:, pick], want, slack, str(ups))
+    for where in (150, 190, 374):
+        bad = pt.clone()
+        bad[0, where] = -1
+        assert ck.shared_prefix_attention(q, c, bad, pl, starts, table, lens).isnan().all()
+
+
 def test_prefix_scores_of_minus_infinity_and_large_ones():
     """Tokens of the prefix whose score is -inf have no weight; scores that differ by hundreds; one token that
     outweighs all others, in the prefix or in the sequence."""
@@ -288,6 +340,9 @@ def check_lora(y, x, w, ids, **kw):
     (130, 300, 776, 8, 3, "fp16", "fp16"),
     (300, 700, 512, 16, 6, "bf16", "bf16"),
     (1030, 257, 136, 72, 9, "fp16", "fp32"),
+    (600, 200, 264, 256, 5, "bf16", "bf16"),
+    (513, 130, 136, 136, 70, "fp16", "fp16"),
+    (512, 64, 72, 104, 100, "bf16", "fp32"),
 ])
 def test_lora(m, n, k, rank, adapters, dtype, out):
     check_lora(*lora_inputs(m, n, k, rank, adapters, dtype, out))
@@ -439,6 +494,7 @@ def logits(rows, vocab, dtype, seed=1, spread=4.0):
 @pytest.mark.parametrize("rows,vocab,top", [
     (1, 1, 1), (3, 2, 2), (2, 7, 5), (1, 63, 63), (5, 64, 64), (2, 65, 64), (4, 255, 1), (3, 1000, 20), (1, 4096, 5), (9, 5003, 8),
     (1, 32000, 5), (2, 32001, 20), (7, 65537, 0), (1, 131072, 64), (40, 20001, 12), (300, 3001, 5), (600, 1023, 64), (1, 200000, 1),
+    (2, 4096, 64), (2, 4097, 64), (3, 32767, 64), (1, 32768, 3), (1, 32769, 3), (256, 5000, 9), (257, 5000, 9),
 ])
 def test_logprobs(rows, vocab, top, dtype):
     x, tokens = logits(rows, vocab, dtype)
@@ -568,6 +624,60 @@ def test_logprobs_far_rows():
 
 
 # -------------------------------------------------------------- all together
+
+def calls_of_three():
+    """Calls of the three operators, some of them with chunks and a second launch: (call with a workspace, its workspace)."""
+    a = prefix_inputs([1500, 90], [0, 20, 23], [400] + [60] * 23, 16, 2, 128, "bf16", "int8", 16)
+    few, many = lora_inputs(24, 2000, 1024, 64, 5, "bf16", "fp32"), lora_inputs(600, 300, 264, 16, 5, "fp16", "fp16")
+    (x, tokens), (z, told) = logits(3, 50000, "fp16"), logits(40, 5000, "bf16")
+    return [
+        (lambda ws: [ck.shared_prefix_attention(*a, workspace=ws)], ck.shared_prefix_attention_workspace(a[0], a[1], a[2], a[5])),
+        (lambda ws: [ck.lora_add(*few, workspace=ws)], ck.lora_add_workspace(few[1], few[2])),
+        (lambda ws: [ck.lora_add(*many, workspace=ws)], ck.lora_add_workspace(many[1], many[2])),
+        (lambda ws: list(ck.token_logprobs(x, tokens, 9, workspace=ws)), ck.token_logprobs_workspace(x, 9)),
+        (lambda ws: list(ck.token_logprobs(z, told, 9, workspace=ws)), ck.token_logprobs_workspace(z, 9)),
+    ]
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with workspaces of its own or of the call's, interleaved without waiting."""
+    calls = calls_of_three()
+    want = [[t.clone() for t in call(None)] for call, _ in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    own = [[None if ws is None else torch.empty_like(ws) for _, ws in calls] for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        for s, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got += [(j, call(own[s][j] if i % 2 else None)) for j, (call, _) in enumerate(calls)]
+    torch.cuda.synchronize()
+    for j, r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want[j])), j
+
+
+def test_two_graphs_with_one_workspace():
+    """Two captured graphs that use the same workspaces, replayed in turn with eager calls between."""
+    calls = calls_of_three()
+    want = [[t.clone() for t in call(ws)] for call, ws in calls]
+    graphs, got = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append([call(ws) for call, ws in calls])
+    for i in range(6):
+        for r in got[i % 2]:
+            for t in r:
+                t.zero_()
+        for _, ws in calls:
+            if ws is not None:
+                ws.fill_(255 * (i % 3 == 0))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        for r, w in zip(got[i % 2], want):
+            assert all(torch.equal(a, b) for a, b in zip(r, w)), i
+        for (call, ws), w in zip(calls, want):
+            assert all(torch.equal(a, b) for a, b in zip(call(ws), w)), i
 
 def server_step(x, qkv_w, lora_qkv, ids, pos, rope, cache, slots, pt, pl, starts, table, lens, w_out, lora_out, head, tokens):
     qkv = ck.int8_linear(x, *qkv_w)

@@ -363,3 +363,22 @@ def test_binding_logprobs(host):
     ]:
         with pytest.raises(exc):
             ck.token_logprobs(*args)
+
+
+def test_launches_go_to_the_tensors_device(host, monkeypatch):
+    """Each entry point launches once, on its tensors' device, however it came through its checks."""
+    calls = []
+    monkeypatch.setattr(ck.decode, "_launch", lambda f, index, *a: calls.append((f, index)))
+    c = ck.KVCache.empty(9, 2, 16, 128, "bf16", "cpu")
+    q, t, n = torch.zeros((3, 8, 128), dtype=torch.bfloat16), i32(3, 4), i32(3)
+    out, big = torch.empty_like(q), torch.empty(1 << 24, dtype=torch.uint8)
+    ck.shared_prefix_attention(q, c, i32(2, 4), i32(2), i32(3), t, n)
+    ck.shared_prefix_attention(q, c, i32(2, 4), i32(2), i32(3), t, n, out=out, workspace=big)
+    w = ck.LoraWeight(torch.zeros((2, 8, 64), dtype=torch.bfloat16), torch.zeros((2, 30, 8), dtype=torch.bfloat16))
+    x, y = torch.zeros((3, 64), dtype=torch.bfloat16), torch.zeros((3, 30))
+    ck.lora_add(y, x, w, n)
+    ck.lora_add(y, x, w, n, out=torch.empty_like(y), workspace=big)
+    ck.token_logprobs(y, None, 3)
+    ck.token_logprobs(y, torch.zeros(3, dtype=torch.int64), workspace=big)
+    want = [ck.ck_shared_prefix_attention] * 2 + [ck.ck_lora_add] * 2 + [ck.ck_token_logprobs] * 2
+    assert calls == [(f, None) for f in want]
