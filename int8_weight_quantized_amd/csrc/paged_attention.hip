@@ -239,8 +239,10 @@ struct AttnLane {
 // called when K has been read, before V is read and after.  FOLD: a score is
 // scaled in the step that takes the reference off, one rounding for two; V,
 // which has to be there, is read before the weights are made where there are
-// registers for it; and a wave in its products goes before one in its weights (128
-// sequences behind 65536 tokens, 64/8 heads of 128: 453 us, 421 and 408).
+// registers for it; a wave in its products goes before one in its weights; and K
+// is read some pieces ahead of its products, which the compiler, short of
+// registers, does not do by itself (128 sequences behind 65536 tokens, 64/8 heads
+// of 128: 453 us, 421, 408 and 402).
 template <int DT, bool I8, int D, int MB, int PARTS, bool FOLD, class KRead, class VReady, class VRead>
 __device__ __forceinline__ void attn_tile(const AttnLane<I8, D>& at, int off, const v4i (&qf)[MB][D / 32],
                                           const float (&sc)[MB], const float* kscale, const float* vscale, int ve,
@@ -251,21 +253,44 @@ __device__ __forceinline__ void attn_tile(const AttnLane<I8, D>& at, int off, co
     constexpr int KK = D / 32, DB = D / 16;
     using Kind = AttnKind<DT, I8, PARTS>;
     constexpr int KT = Kind::KT, VT = Kind::VT, NA = Kind::NA;
+    constexpr bool AHEAD = FOLD && MB * NA < 4;
     const int G = (threadIdx.x & 63) >> 4;
     f32x4v s[MB][2];
     if constexpr (FOLD) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int b = 0; b < MB; ++b) s[b][u] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    using Raw = std::conditional_t<I8, uint2, v4i>;
+    auto read_k = [&](int u, int kk) { return *reinterpret_cast<const Raw*>(at.k_at(u, kk) + off); };
+    auto score = [&](int u, int kk, const Raw& raw) {
+        v4i kf;
+        if constexpr (I8) kf = codes8_f16(raw);
+        else kf = raw;
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            v4i kf;
-            if constexpr (I8) kf = codes8_f16(*reinterpret_cast<const uint2*>(at.k_at(u, kk) + off));
-            else kf = *reinterpret_cast<const v4i*>(at.k_at(u, kk) + off);
+        for (int b = 0; b < MB; ++b) s[b][u] = mfma16<KT>(kf, qf[b][kk], s[b][u]);
+    };
+    if constexpr (AHEAD) {
+        constexpr int N = KK % 2 == 0 ? 4 : 2, groups = 2 * KK / N;
+        Raw raw[2][N];
 #pragma unroll
-            for (int b = 0; b < MB; ++b) s[b][u] = mfma16<KT>(kf, qf[b][kk], s[b][u]);
+        for (int g = 0; g <= groups; ++g) {
+            if (g < groups) {
+#pragma unroll
+                for (int x = 0; x < N; ++x) raw[g & 1][x] = read_k((g * N + x) / KK, (g * N + x) % KK);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (g > 0) {
+#pragma unroll
+                for (int x = 0; x < N; ++x) score(((g - 1) * N + x) / KK, ((g - 1) * N + x) % KK, raw[(g - 1) & 1][x]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) score(u, kk, read_k(u, kk));
     }
     k_read();
     if constexpr (FOLD) __builtin_amdgcn_s_setprio(0);

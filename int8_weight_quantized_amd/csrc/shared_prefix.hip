@@ -42,6 +42,7 @@ struct PrefixArgs {
 };
 
 constexpr int kPrefixParts = 2;          // 16-bit parts of a weight
+constexpr int kPrefixOwn = 512;          // a sequence's own tokens in a chunk, at most
 constexpr int kPrefixSeg = 512;          // tokens whose row offsets are made at a time
 
 // Sizes for rows of RB bytes: four waves, 64 KiB of K and V in LDS, so that two
@@ -78,8 +79,8 @@ __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
 {
     const int lane = threadIdx.x & 63;
     if ((int64_t)blockIdx.x >= a.pblocks) {                  // a sequence's own tokens
-        const int64_t id = (int64_t)blockIdx.x - a.pblocks, rest = id / a.splits, bk = rest / a.row_blocks;
-        const int split = (int)(id % a.splits), rb = (int)(rest % a.row_blocks);
+        const int64_t id = (int64_t)blockIdx.x - a.pblocks, rest = id / a.row_blocks, bk = rest % ((int64_t)a.batch * a.hk);
+        const int split = (int)(rest / ((int64_t)a.batch * a.hk)), rb = (int)(id % a.row_blocks);
         w.kvh = (int)(bk % a.hk);
         w.seq0 = (int)(bk / a.hk);
         w.row0 = 16 * rb;
@@ -95,8 +96,8 @@ __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
     const int64_t per = 8 * (int64_t)a.prows, unit = blockIdx.x / per * 8 + blockIdx.x % 8;
     int slot = (int)(blockIdx.x % per / 8);
     if (unit >= (int64_t)a.hk * a.psplits) return false;
-    w.slot = (int)(unit % a.psplits);
-    w.kvh = (int)(unit / a.psplits);
+    w.slot = (int)(unit / a.hk);
+    w.kvh = (int)(unit % a.hk);
     constexpr int most = 1 << 29;
     int p = -1;
     for (int base = 0; base < a.prefixes; base += 64) {      // whose row block it is: a sum over the prefixes before
@@ -618,7 +619,10 @@ struct PrefixPlan {
 // blocks 602; 48 behind three int8 prefixes: 512 blocks 61 us, 256 blocks 56; 24
 // behind 20000 tokens at head_dim 256: 42 and 39.)  At least 128 tokens, and where
 // groups have up to 16 rows on average 1024 at most, which the form for few rows
-// takes.  Sequences' own chunks follow the rule of paged_attention.hip.
+// takes.  Sequences' own chunks follow the rule of paged_attention.hip, but with
+// 512 tokens at most (the 48 sequences: 1024 tokens 56 us, 512 52, 256 55): they
+// run beside the prefixes' long ones.  The first chunks of all come first, as
+// they are the likeliest to have tokens.
 bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_dim, int64_t prefixes,
                  int64_t pcap, int64_t cap)
 {
@@ -645,7 +649,7 @@ bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t h
     }
     p.row_blocks = cdiv(group, 16);
     const int64_t pairs = batch * hk * p.row_blocks, tiles = std::min<int64_t>(cdiv(cap, kAttnTile), 1 << 20);
-    p.chunk = std::min<int64_t>(std::max<int64_t>(cdiv(cdiv(tiles * pairs, round), 4) * 4, 4) * kAttnTile, kAttnChunk);
+    p.chunk = std::min<int64_t>(std::max<int64_t>(cdiv(cdiv(tiles * pairs, round), 4) * 4, 4) * kAttnTile, kPrefixOwn);
     p.splits = std::max<int64_t>(1, cdiv(cap, p.chunk));
     if (pairs > limit / p.splits || pairs * p.splits + p.pblocks > limit) return false;
     p.blocks = p.pblocks + pairs * p.splits;
