@@ -212,9 +212,9 @@ struct AttnLane {
     static constexpr int KN = least(Sh::span / 16 / kstep, KK), VN = least(Sh::span / 16 / vstep, DB);
     const uint8_t *k[KN], *v[VN];
 
-    __device__ __forceinline__ AttnLane(const uint8_t* kr, const uint8_t* vr)
+    __device__ __forceinline__ AttnLane(const uint8_t* kr, const uint8_t* vr, int lane)
     {
-        const int lane = threadIdx.x & 63, G = lane >> 4, i16 = lane & 15;
+        const int G = lane >> 4, i16 = lane & 15;
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
             const int piece = 4 * i + G;                     // int8: of eight codes
@@ -616,7 +616,7 @@ __global__ __launch_bounds__(64 * (AttnShape<D * (I8 ? 1 : 2)>::waves)) void pag
         issue_k();
         issue_v();
     }
-    const AttnLane<I8, D> at(kring, vring);
+    const AttnLane<I8, D> at(kring, vring, lane);
     for (int t = wave; t < tiles; t += NW) {
         const bool more = t + NW < tiles;
         wait_vmcnt<NL>();                                    // K of this tile; V came after it

@@ -37,8 +37,9 @@ struct PrefixArgs {
     int64_t pblocks;                     // blocks of prefixes; those of sequences follow
     float scale;
     int batch, hq, hk, group, prefixes, page_shift;
-    int prows, psplits, pchunk;          // row blocks and chunks of prefixes
-    int row_blocks, splits, chunk;       // and of sequences
+    int prows, psplits, pshare;          // of prefixes: row blocks, places for chunks, blocks that share a list
+    int row_blocks, splits, share;       // and of sequences
+    int few;                             // prefixes have up to 16 rows on average
 };
 
 constexpr int kPrefixParts = 2;          // 16-bit parts of a weight
@@ -59,18 +60,43 @@ __host__ __device__ constexpr int prefix_rows(int d) { return d <= 128 ? 128 : 6
 
 // What a block works on: rows row0 .. row0 + rows - 1 of the group that begins
 // at sequence seq0 (row r: sequence seq0 + r / group, head r % group of the key
-// head), and tokens first .. first + n - 1 of the list that `table` names.
+// head), and chunks split, split + share and so on of the `len` tokens that
+// `table` names: now tokens first .. first + n - 1, whose sums go to place slot.
 struct PrefixWork {
     const int32_t* table;
+    uint32_t len, chunk;
+    int split, share, place, rows, row0, seq0, kvh;
     int64_t first;
-    int n, rows, row0, seq0, kvh, slot;
+    int n, slot;
+
+    __device__ __forceinline__ bool next()
+    {
+        first = (int64_t)split * chunk;
+        if (first >= len) return false;
+        n = (int)min<int64_t>(chunk, len - first);
+        slot = place + split;
+        split += share;
+        return true;
+    }
 };
 
-// The tokens of a chunk that begins at `first`, of `len` or as many as the table
-// can name; 0 for any negative length.
-__device__ __forceinline__ int prefix_tokens(int32_t len, int64_t cap, int64_t first, int chunk)
+// The tokens of a list, at most as many as its table can name; 0 for any
+// negative length.
+__device__ __forceinline__ uint32_t prefix_tokens(int32_t len, int64_t cap) { return (uint32_t)min<int64_t>(max(len, 0), cap); }
+
+// The length of its chunks: `share` blocks have one each, unless that would be
+// less than 128 tokens, or more than `most` for the form that takes few rows.
+__device__ __forceinline__ uint32_t prefix_chunk(uint32_t len, int share, int most)
 {
-    return (int)max<int64_t>(min<int64_t>(chunk, min<int64_t>(len, cap) - first), 0);
+    const uint32_t all = 128u * share;
+    return min((uint32_t)most, max((len + all - 1) / all, 1u) * 128);
+}
+
+// Of the chunks of a prefix that has so many sequences: 1024 tokens where all
+// their rows are few and it was planned so, else any number.
+__device__ __forceinline__ int prefix_most(const PrefixArgs& a, int members)
+{
+    return a.few && members <= 16 / a.group ? kAttnChunk : 1 << 30;
 }
 
 // False if there is nothing to do.
@@ -80,28 +106,31 @@ __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
     const int lane = threadIdx.x & 63;
     if ((int64_t)blockIdx.x >= a.pblocks) {                  // a sequence's own tokens
         const int64_t id = (int64_t)blockIdx.x - a.pblocks, rest = id / a.row_blocks, bk = rest % ((int64_t)a.batch * a.hk);
-        const int split = (int)(rest / ((int64_t)a.batch * a.hk)), rb = (int)(id % a.row_blocks);
+        const int rb = (int)(id % a.row_blocks);
+        w.split = (int)(rest / ((int64_t)a.batch * a.hk));
         w.kvh = (int)(bk % a.hk);
         w.seq0 = (int)(bk / a.hk);
         w.row0 = 16 * rb;
         w.rows = min(16, a.group - w.row0);
         w.table = a.table + w.seq0 * a.table_stride;
-        w.first = (int64_t)split * a.chunk;
-        w.n = prefix_tokens(a.lens[w.seq0], a.cap, w.first, a.chunk);
-        w.slot = a.psplits + split;
-        return w.n > 0;
+        w.len = prefix_tokens(a.lens[w.seq0], a.cap);
+        w.chunk = prefix_chunk(w.len, a.share, kPrefixOwn);
+        w.share = a.share;
+        w.place = a.psplits;
+        return w.next();
     }
     // The row blocks of a chunk and key head, which read the same rows, follow
     // each other on one XCD (blocks go to the eight in turn).
     const int64_t per = 8 * (int64_t)a.prows, unit = blockIdx.x / per * 8 + blockIdx.x % 8;
     int slot = (int)(blockIdx.x % per / 8);
-    if (unit >= (int64_t)a.hk * a.psplits) return false;
-    w.slot = (int)(unit / a.hk);
+    if (unit >= (int64_t)a.hk * a.pshare) return false;
+    w.split = (int)(unit / a.hk);
     w.kvh = (int)(unit % a.hk);
     constexpr int most = 1 << 29;
-    int p = -1;
+    int p = -1, members = 0;                                 // the prefix, and its sequences
     for (int base = 0; base < a.prefixes; base += 64) {      // whose row block it is: a sum over the prefixes before
-        int s0 = 0, blocks = 0, members = 0;
+        int s0 = 0, blocks = 0;
+        members = 0;
         if (base + lane < a.prefixes) {
             s0 = min(max(a.starts[base + lane], 0), a.batch);
             members = min(max(a.starts[base + lane + 1], s0), a.batch) - s0;
@@ -121,20 +150,24 @@ __device__ __forceinline__ bool prefix_work(const PrefixArgs& a, PrefixWork& w)
             if (at > 0) slot -= __shfl(prev, at);
             w.seq0 = __shfl(s0, at);
             w.row0 = slot * ROWS;
-            w.rows = min(ROWS, __shfl(members, at) * a.group - w.row0);
+            members = __shfl(members, at);
+            w.rows = min(ROWS, members * a.group - w.row0);
             break;
         }
         slot -= __shfl(sum, 63);
     }
     if (p < 0) return false;
+    members = __builtin_amdgcn_readfirstlane(members);
     p = __builtin_amdgcn_readfirstlane(p);
     w.seq0 = __builtin_amdgcn_readfirstlane(w.seq0);
     w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
     w.rows = __builtin_amdgcn_readfirstlane(w.rows);
     w.table = a.ptable + p * a.pt_stride;
-    w.first = (int64_t)w.slot * a.pchunk;
-    w.n = prefix_tokens(a.plens[p], a.pcap, w.first, a.pchunk);
-    return w.n > 0;
+    w.len = prefix_tokens(a.plens[p], a.pcap);
+    w.chunk = prefix_chunk(w.len, a.pshare, prefix_most(a, members));
+    w.share = a.pshare;
+    w.place = 0;
+    return w.next();
 }
 
 // The queries of 16 rows: lane 16 G + i holds elements 32 kk + 8 G + 0 .. 7 of
@@ -251,7 +284,9 @@ __device__ __forceinline__ void prefix_walk(const PrefixArgs& a, const PrefixWor
     using Sh = AttnShape<RB>;
     using Kind = AttnKind<DT, I8, kPrefixParts>;
     constexpr int NW = PrefixShape<RB>::walkers, NL = Sh::loads, DB = D / 16, NA = Kind::NA;
-    const int tid = threadIdx.x, lane = tid & 63, G = lane >> 4, i16 = lane & 15;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));                            // nothing that follows from it is kept from chunk to chunk: registers are short
+    const int lane = tid & 63, G = lane >> 4, i16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tiles = (w.n + kAttnTile - 1) / kAttnTile;
     v4i qf[1][D / 32];
@@ -299,7 +334,7 @@ __device__ __forceinline__ void prefix_walk(const PrefixArgs& a, const PrefixWor
             issue_k();
             issue_v();
         }
-        const AttnLane<I8, D> at(kring, vring);
+        const AttnLane<I8, D> at(kring, vring, lane);
         for (int t = wave; t < tiles; t += NW) {
             const bool more = t + NW < tiles;
             wait_vmcnt<NL>();                                // K of this tile; V came after it
@@ -423,7 +458,7 @@ __device__ __forceinline__ void prefix_share(const PrefixArgs& a, const PrefixWo
     int ve = -300;                                           // value scales are taken relative to 2^ve: none yet
     __syncthreads();
     issue(0);
-    const AttnLane<I8, D> at(sh.ring, sh.ring + T * RB);
+    const AttnLane<I8, D> at(sh.ring, sh.ring + T * RB, lane);
     auto tile = [&](int t, auto odd) {
         constexpr int place = decltype(odd)::value ? 2 * T * RB : 0;
         wait_vmcnt<0>();
@@ -492,15 +527,27 @@ __global__ __launch_bounds__(256, 2) void shared_prefix_kernel(PrefixArgs a)
     __shared__ PrefixShared<RB, I8> sh;
     PrefixWork w;
     if (!prefix_work<prefix_rows(D)>(a, w)) return;
-    if (threadIdx.x == 0) sh.bad_page = 0;
-    __syncthreads();
     if (a.pages == 0) {                                      // no page is inside the cache
-        for (int r = threadIdx.x; r < w.rows; r += 256) a.part_ml[prefix_part(a, w, r)] = make_float2(0.0f, NAN);
+        do {
+            for (int r = threadIdx.x; r < w.rows; r += 256) a.part_ml[prefix_part(a, w, r)] = make_float2(0.0f, NAN);
+        } while (w.next());
         return;
     }
-    if (w.rows <= 16 && w.n <= kAttnChunk) prefix_walk<DT, I8, D>(a, w, sh);
-    else if (D > 128 || w.rows <= 64) prefix_share<DT, I8, D, 1>(a, w, sh);
-    else if constexpr (D <= 128) prefix_share<DT, I8, D, 2>(a, w, sh);
+    if (threadIdx.x == 0) sh.bad_page = 0;
+    __syncthreads();
+    if (w.rows <= 16 && w.chunk <= kAttnChunk) {
+        for (;;) {
+            prefix_walk<DT, I8, D>(a, w, sh);
+            if (!w.next()) break;
+            __syncthreads();                                 // the chunk has been read
+            if (threadIdx.x == 0) sh.bad_page = 0;
+            __syncthreads();
+        }
+    } else if (D > 128 || w.rows <= 64) {
+        prefix_share<DT, I8, D, 1>(a, w, sh);
+    } else {
+        if constexpr (D <= 128) prefix_share<DT, I8, D, 2>(a, w, sh);
+    }
 }
 
 // Joins the chunks of a sequence and head, those of its prefix and its own, one
@@ -529,9 +576,10 @@ __global__ __launch_bounds__(256) void shared_prefix_join_kernel(PrefixArgs a)
         wrong |= __any(in && (s < 0 || s > a.batch || (i > 0 && s < a.starts[i - 1])));
     }
     const int p = before - 1;
-    const int64_t np = p < 0 || p >= a.prefixes ? 0 : min(max((int64_t)a.plens[p], (int64_t)0), a.pcap);
-    const int64_t no = min(max((int64_t)a.lens[b], (int64_t)0), a.cap);
-    const int shared = (int)((np + a.pchunk - 1) / a.pchunk), count = wrong ? 0 : shared + (int)((no + a.chunk - 1) / a.chunk);
+    const uint32_t np = p < 0 || p >= a.prefixes ? 0 : prefix_tokens(a.plens[p], a.pcap), no = prefix_tokens(a.lens[b], a.cap);
+    const int members = np > 0 ? a.starts[p + 1] - a.starts[p] : 0;
+    const uint32_t pchunk = prefix_chunk(np, a.pshare, prefix_most(a, members)), chunk = prefix_chunk(no, a.share, kPrefixOwn);
+    const int shared = (int)((np + pchunk - 1) / pchunk), count = wrong ? 0 : shared + (int)((no + chunk - 1) / chunk);
     const int64_t slots = a.psplits + a.splits;
     const float2* const ml = a.part_ml + bh * slots;
     const float* const part = a.part + bh * slots * D + 4 * c;
@@ -607,52 +655,65 @@ __global__ __launch_bounds__(256) void shared_prefix_join_kernel(PrefixArgs a)
 namespace {
 
 struct PrefixPlan {
-    int64_t prows, psplits, pchunk, pblocks;                 // of prefixes
-    int64_t row_blocks, splits, chunk, blocks;               // of sequences; blocks: the whole grid
+    int64_t prows, psplits, pshare, pblocks;                 // of prefixes
+    int64_t row_blocks, splits, share, blocks;               // of sequences; blocks: the whole grid
     int64_t bytes;
+    bool few;
 };
 
-// Chunks.  A prefix's are of such a length that the blocks take the least time,
-// where a round of up to two blocks a CU takes as long as its chunk, a fixed part
-// and its rows' sums, which are written and read; up to one block a CU run
+// Chunks.  The host knows how many tokens the tables can name, the kernel how
+// many there are, and a table may be far wider than any length.  So the host
+// chooses how many blocks share the tokens of a list, and they divide those that
+// there are, 128 at least each (48 sequences of 600 tokens behind prefixes of
+// 1000, in tables for 1024 tokens 29 us, for 131072 30 us, where chunks that
+// follow from the tables took 28 and 154).
+//
+// A prefix's blocks are so many that all take the least time, if the table is
+// full, where a round of up to two blocks a CU takes as long as its chunk, a fixed
+// part and its rows' sums, which are written and read; up to one block a CU run
 // half as fast again.  (128 sequences behind 65536 tokens: 512 blocks 402 us, 256
 // blocks 602; 48 behind three int8 prefixes: 512 blocks 61 us, 256 blocks 56; 24
-// behind 20000 tokens at head_dim 256: 42 and 39.)  At least 128 tokens, and where
-// groups have up to 16 rows on average 1024 at most, which the form for few rows
-// takes.  Sequences' own chunks follow the rule of paged_attention.hip, but with
-// 512 tokens at most (the 48 sequences: 1024 tokens 56 us, 512 52, 256 55): they
-// run beside the prefixes' long ones.  The first chunks of all come first, as
-// they are the likeliest to have tokens.
+// behind 20000 tokens at head_dim 256: 42 and 39.)  Where groups have up to 16
+// rows on average, those that have no more get chunks of 1024 tokens at most, which
+// the form for few rows takes, and a block goes through several.
+//
+// All sequences have two blocks a CU, and their chunks 512 tokens at most (the
+// 48 sequences: 1024 tokens 56 us, 512 52, 256 55): they run beside the prefixes'
+// long ones.  The first chunks of all come first, as they are the likeliest to
+// have tokens.
 bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_dim, int64_t prefixes,
                  int64_t pcap, int64_t cap)
 {
     const int64_t limit = 0x7fffffff, group = hq / hk, round = 2 * kNumCUs;
     if (batch * hq > limit) return false;
     p = PrefixPlan{};
+    pcap = std::min(pcap, limit);                            // no length is larger
+    cap = std::min(cap, limit);
     const int64_t used = std::min(prefixes, batch);          // prefixes with a sequence, at most
-    p.pchunk = 128;
+    p.pshare = 1;
+    p.few = batch * group <= 16 * used;
     if (used > 0 && pcap > 0 && hq > 0) {
         p.prows = cdiv(batch * group, prefix_rows((int)head_dim)) + used - 1;
-        const int64_t pairs = p.prows * hk, most = batch * group <= 16 * used ? kAttnChunk : int64_t(1) << 30;
+        const int64_t pairs = p.prows * hk;
         int64_t least = INT64_MAX;
         for (int64_t r = 1; r <= 16; r += r < 2 ? 1 : 2) {   // half a round, and whole ones
-            const int64_t s = std::max<int64_t>(1, r * kNumCUs / pairs);
-            const int64_t chunk = std::min(most, cdiv(cdiv(pcap, s), 128) * 128);
-            const int64_t n = pairs * cdiv(pcap, chunk), rest = n % round;
+            const int64_t share = std::min(std::max<int64_t>(1, r * kNumCUs / pairs), cdiv(pcap, 128));
+            const int64_t chunk = cdiv(cdiv(pcap, share), 128) * 128;
+            const int64_t n = pairs * share, rest = n % round;
             const int64_t each = chunk + 128 + 2 * prefix_rows((int)head_dim);
             const int64_t time = n / round * each + (rest > kNumCUs ? each : rest > 0 ? each * 2 / 3 : 0);
-            if (time < least) least = time, p.pchunk = chunk;
+            if (time < least) least = time, p.pshare = share;
         }
-        p.psplits = cdiv(pcap, p.pchunk);
-        if (pairs > limit / (p.psplits + 8)) return false;
-        p.pblocks = cdiv(hk * p.psplits, 8) * 8 * p.prows;
+        p.psplits = p.few ? std::max(p.pshare, cdiv(pcap, kAttnChunk)) : p.pshare;
+        if (pairs > limit / (p.pshare + 8)) return false;
+        p.pblocks = cdiv(hk * p.pshare, 8) * 8 * p.prows;
     }
     p.row_blocks = cdiv(group, 16);
-    const int64_t pairs = batch * hk * p.row_blocks, tiles = std::min<int64_t>(cdiv(cap, kAttnTile), 1 << 20);
-    p.chunk = std::min<int64_t>(std::max<int64_t>(cdiv(cdiv(tiles * pairs, round), 4) * 4, 4) * kAttnTile, kPrefixOwn);
-    p.splits = std::max<int64_t>(1, cdiv(cap, p.chunk));
-    if (pairs > limit / p.splits || pairs * p.splits + p.pblocks > limit) return false;
-    p.blocks = p.pblocks + pairs * p.splits;
+    const int64_t pairs = std::max<int64_t>(batch * hk * p.row_blocks, 1);
+    p.share = std::max<int64_t>(std::min(cdiv(round, pairs), cdiv(cap, 128)), 1);
+    p.splits = std::max(p.share, cdiv(cap, kPrefixOwn));
+    if (pairs > limit / p.share || pairs * p.share + p.pblocks > limit) return false;
+    p.blocks = p.pblocks + pairs * p.share;
     p.bytes = batch * hq * (p.psplits + p.splits) * (head_dim + 2) * 4;
     return true;
 }
@@ -748,8 +809,8 @@ extern "C" ck_status ck_shared_prefix_attention(const ck_prefix_args* args, cons
     a.page_shift = ilog2(cache->page_size); a.group = (int)(p.hq / cache->heads);
     a.part = (float*)p.workspace;
     a.part_ml = (float2*)(a.part + p.batch * p.hq * (plan.psplits + plan.splits) * d);
-    a.prows = (int)plan.prows; a.psplits = (int)plan.psplits; a.pchunk = (int)plan.pchunk; a.pblocks = plan.pblocks;
-    a.row_blocks = (int)plan.row_blocks; a.splits = (int)plan.splits; a.chunk = (int)plan.chunk;
+    a.prows = (int)plan.prows; a.psplits = (int)plan.psplits; a.pshare = (int)plan.pshare; a.pblocks = plan.pblocks; a.few = plan.few;
+    a.row_blocks = (int)plan.row_blocks; a.splits = (int)plan.splits; a.share = (int)plan.share;
     const void* fn = f16 ? (i8 ? prefix_fn<CK_DT_FP16, true>(d) : prefix_fn<CK_DT_FP16, false>(d))
                          : (i8 ? prefix_fn<CK_DT_BF16, true>(d) : prefix_fn<CK_DT_BF16, false>(d));
     const void* join = f16 ? prefix_join_fn<CK_DT_FP16>(d) : prefix_join_fn<CK_DT_BF16>(d);

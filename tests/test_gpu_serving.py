@@ -185,6 +185,37 @@ def test_prefix_many(prefixes, sequences):
     check_prefix(*prefix_inputs(prefix, starts, lens, 12, 2, 64, "bf16", "bf16", 16))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("fp16", "fp16"), ("int8", "bf16")])
+def test_prefix_blocks_with_several_chunks(d, cache, dtype):
+    """So many sequences and prefixes that a block goes through several chunks of a long one, of both kinds; a bad
+    page in one of them makes what sees it NaN and nothing else."""
+    prefix = [2500 if i in (3, 40) else 1025 if i == 63 else i % 70 for i in range(64)]
+    lens = [1700 if i in (5, 66) else 513 if i == 6 else 1 + i % 40 for i in range(70)]
+    starts = [2 + i for i in range(65)]
+    q, c, pt, pl, starts, table, lens = prefix_inputs(prefix, starts, lens, 16, 8, d, dtype, cache, 16)
+    good = check_prefix(q, c, pt, pl, starts, table, lens)
+    for where, who in ((10, 5), (75, 5), (100, 42)):         # of table, table and pt
+        bad, one = table.clone(), pt.clone()
+        (one if where == 100 else bad)[40 if where == 100 else who, where] = c.pages
+        out = ck.shared_prefix_attention(q, c, one, pl, starts, bad, lens)
+        keep = [i for i in range(70) if i != who]
+        assert out[who].isnan().all() and torch.equal(out[keep], good[keep])
+
+
+def test_prefix_wide_tables_give_the_same_bits():
+    """Tables far wider than any length, in which as many blocks share a list: the same bits."""
+    q, c, pt, pl, starts, table, lens = prefix_inputs([1000, 300], [0, 20, 30], [700 - 20 * i for i in range(33)], 8, 8, 64,
+                                                      "bf16", "bf16", 16)
+    got = []
+    for more in (2000, 3000):
+        wide = [torch.full((len(t), more), -7, dtype=torch.int32, device=q.device) for t in (pt, table)]
+        for w, t in zip(wide, (pt, table)):
+            w[:, :t.shape[1]] = t
+        got.append(check_prefix(q, c, wide[0], pl, starts, wide[1], lens))
+    assert torch.equal(*got)
+
+
 @pytest.mark.parametrize("cache", ["bf16", "int8"])
 @pytest.mark.parametrize("members", [17, 66])
 def test_prefix_long_chunks(cache, members):
