@@ -11,7 +11,7 @@
 // prompt, and the launches of small calls.  Rows are taken 64 at a time, those
 // with the same adapter together whatever their order, so an adapter is read
 // once for its rows; a row without one is copied.
-//   - Up to kLoraRows rows, a block has one adapter of one group of 64 rows and a
+//   - Up to kLoraRows rows, a block has one adapter of a group of up to 64 rows and a
 //     slice of the columns.  Where A is small every block makes v by itself, in
 //     the same launch: A comes from L2 then, once for each slice.
 //   - Otherwise a first launch makes v, with k split over blocks where there
@@ -182,14 +182,15 @@ __device__ __forceinline__ void lora_x(const LoraArgs& a, int places, int t0, in
         xo[g] = (uint32_t)(__shfl(places, min(t0 + 4 * g + ((lane >> 2) & 3), rows - 1)) * (uint32_t)a.ldx + (lane >> 4) * 32 + (lane & 3) * 8) * 2;
 }
 
-// The first launch: v of a group of rows, over one part of k.  XG: 1 for groups
-// of up to 64 rows whose adapters have a few each (four at a time), 4 for 16
-// rows in a row.
-template <int DT, int XG>
-__global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArgs a, int group, int units)
+// The first launch: v of a group of rows, over one part of k, for the rows of an
+// adapter 16 at a time, and four where there are no more (16 rows cost their
+// loads, but one pass over A; 256 rows of 4 adapters in a row, 4096 columns, rank
+// 16: 12.5 us, and 31.8 four at a time).
+template <int DT>
+__global__ __launch_bounds__(64 * kLoraWaves, 4) void lora_shrink_kernel(LoraArgs a, int group, int units)
 {
     constexpr int NW = kLoraWaves;
-    __shared__ float red[NW][4 * XG][20];                    // [wave][row][rank]
+    __shared__ float red[NW][16][20];                        // [wave][row][rank]
     const int tid = threadIdx.x, lane = tid & 63, G = lane >> 4, c = (lane >> 2) & 3;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int split = blockIdx.x % a.ksplits;
@@ -200,7 +201,8 @@ __global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArg
         int id;
         const uint64_t members = lora_members(r.left, r.ids, id);
         const int rows = __popcll(members), places = lora_places(members);
-        for (int t0 = 0; t0 < rows; t0 += 4 * XG) {
+        auto some = [&](int t0, auto size) {                 // 4 XG rows from place t0 on
+            constexpr int XG = decltype(size)::value;
             uint32_t xo[XG];
             lora_x<XG>(a, places, t0, rows, xo);
             for (int rank0 = 0; rank0 < a.rank; rank0 += 16 * share.groups) {
@@ -225,6 +227,15 @@ __global__ __launch_bounds__(64 * kLoraWaves, 2) void lora_shrink_kernel(LoraArg
                     }
                 }
                 __syncthreads();
+            }
+        };
+        for (int t0 = 0; t0 < rows;) {
+            if (rows - t0 > 4) {
+                some(t0, IntTag<4>{});
+                t0 += 16;
+            } else {
+                some(t0, IntTag<1>{});
+                t0 += 4;
             }
         }
     }
@@ -520,23 +531,24 @@ struct LoraPlan {
     int64_t group, ksplits, bytes;                           // of the first launch: rows of a block, parts of k
 };
 
+// Up to kLoraRows rows an adapter has blocks of its own: rows of 48 adapters in any
+// order (4096 x 4096, rank 16) take 35 us so at 512 rows and 125 one after the
+// other, at 1024 rows 59 and 111; but rows of one adapter, or few, in a row 14 us
+// either way at 512, and 25 to 96 or 14 at 1024.  One launch for both products where
+// A is small (16 rows; rank 16, k 8192: 8.0 us in one, 10.0 in two; k 16384: 10.0 and
+// 9.5) and rows are few (61 rows of 48 adapters 16.0 and 20.0 us; 512 rows of 4
+// adapters 45 and 33).
 LoraPlan lora_plan(int64_t m, int64_t n, int64_t k, int64_t rank)
 {
     LoraPlan p{};
     p.each = m <= kLoraRows;
     p.fused = p.each && rank <= 32 && rank * k <= 131072 && m <= 64;
     p.blocks = p.fused || rank > 128 ? 1 : rank > 64 ? 2 : 4;    // within 64 KiB
-    p.group = p.each ? 64 : 16;
+    p.group = m <= 64 ? 64 : 16;
     const int64_t units = p.each ? std::min<int64_t>(m, 16) : cdiv(m, p.group);
     p.ksplits = std::max<int64_t>(1, std::min<int64_t>(cdiv(kNumCUs, std::max<int64_t>(units, 1)), cdiv(k * std::min<int64_t>(cdiv(rank, 16), kLoraWaves), 128 * 2 * kLoraWaves)));
     if (!p.fused) p.bytes = p.ksplits * m * rank * 4;
     return p;
-}
-
-template <int DT>
-const void* lora_shrink_fn(bool each)
-{
-    return each ? reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 1>) : reinterpret_cast<const void*>(&lora_shrink_kernel<DT, 4>);
 }
 
 template <int DT, int OUT>
@@ -610,9 +622,11 @@ extern "C" ck_status ck_lora_add(const ck_lora_args* args, hipStream_t stream)
     int group = (int)plan.group, units = plan.each ? (int)std::max<int64_t>(1, std::min(std::min<int64_t>(64, p.m), p.adapters)) : 0;
     const int64_t per64 = cdiv(p.m, 64) * std::max(units, 1);
     if (!plan.fused && a.adapters > 0) {
-        void* kargs[] = {&a, &group, &units};
-        const int64_t blocks = (plan.each ? per64 : cdiv(p.m, plan.group)) * plan.ksplits;
-        const void* fn = f16 ? lora_shrink_fn<CK_DT_FP16>(plan.each) : lora_shrink_fn<CK_DT_BF16>(plan.each);
+        int few = std::min(group, units);
+        void* kargs[] = {&a, &group, &few};
+        const int64_t blocks = cdiv(p.m, plan.group) * std::max(few, 1) * plan.ksplits;
+        const void* fn = f16 ? reinterpret_cast<const void*>(&lora_shrink_kernel<CK_DT_FP16>)
+                             : reinterpret_cast<const void*>(&lora_shrink_kernel<CK_DT_BF16>);
         if ((s = launch(fn, (unsigned)blocks, 64 * kLoraWaves, kargs, stream, "lora_shrink")) != CK_OK) return s;
     }
     // Column slices, of whole rounds of a block's waves: as many blocks as give every CU two.
