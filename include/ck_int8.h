@@ -644,8 +644,10 @@ ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
  *   out[b, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b, h] . k_j - m),
  * m the largest score, over the tokens j of sequence b: those of its prefix,
  * if it has one, then its own.  Scores, exponentials and sums are fp32, the
- * products on the matrix cores with p_j in 16-bit parts (ck_paged_attention).
- * A sequence without any token gives zeros.
+ * products on the matrix cores with p_j in two 16-bit parts: they hold it to
+ * 2^-17 of itself (a bf16 or int8 cache), or to 2^-23 of itself or 2^-50 of the
+ * largest (fp16); ck_paged_attention takes more parts.  A sequence without any
+ * token gives zeros.
  *
  * q, cache, out     as in ck_paged_attention.
  * prefix_table [in] int32 [prefixes, prefix_width], rows prefix_table_stride
@@ -664,10 +666,10 @@ ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
  * A page outside [0, pages) is an error of the sequences that see it: their
  * outputs are NaN.  Queries and visible rows must be finite, the cache's k and
  * v span at most 64 GiB each, and rows that are not visible are never used.
- * workspace  [tmp] as in ck_paged_attention, of
- *                  ck_shared_prefix_attention_workspace bytes.
- * prefixes == 0 is ck_paged_attention without a window (the prefix pointers
- * may be NULL).
+ * workspace  [tmp] device memory of ck_shared_prefix_attention_workspace bytes,
+ *                  256-B aligned, used by one call at a time.  Its size grows
+ *                  with the tables' widths, the time does not.
+ * prefixes == 0: no sequence has a prefix (its pointers may be NULL).
  */
 typedef struct {
     const void* q;
