@@ -653,7 +653,8 @@ ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
  * prefix_table [in] int32 [prefixes, prefix_width], rows prefix_table_stride
  *                   apart: token j of prefix p is token j % page_size of page
  *                   prefix_table[p, j / page_size].
- * prefix_lens  [in] int32 [prefixes]: the tokens of each, any number.
+ * prefix_lens  [in] int32 [prefixes]: the tokens of each, any number up to what
+ *                   prefix_table can name, which is 2^30 at most.
  * starts       [in] int32 [prefixes + 1]: the sequences starts[p] to
  *                   starts[p + 1] - 1 begin with prefix p; those before the
  *                   first and from the last entry on have none.  The entries

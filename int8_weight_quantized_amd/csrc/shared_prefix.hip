@@ -42,7 +42,8 @@ struct PrefixArgs {
     int few;                             // prefixes have up to 16 rows on average
 };
 
-constexpr int kPrefixParts = 2;          // 16-bit parts of a weight
+constexpr int kPrefixParts = 2;          // 16-bit parts of a weight (128 sequences behind 65536 bf16 tokens: 421 us, with three 492)
+constexpr int kPrefixMost = 1 << 30;     // a prefix's tokens
 constexpr int kPrefixOwn = 512;          // a sequence's own tokens in a chunk, at most
 constexpr int kPrefixSeg = 512;          // tokens whose row offsets are made at a time
 
@@ -96,7 +97,7 @@ __device__ __forceinline__ uint32_t prefix_chunk(uint32_t len, int share, int mo
 // their rows are few and it was planned so, else any number.
 __device__ __forceinline__ int prefix_most(const PrefixArgs& a, int members)
 {
-    return a.few && members <= 16 / a.group ? kAttnChunk : 1 << 30;
+    return a.few && members <= 16 / a.group ? kAttnChunk : kPrefixMost;
 }
 
 // False if there is nothing to do.
@@ -685,10 +686,9 @@ bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t h
                  int64_t pcap, int64_t cap)
 {
     const int64_t limit = 0x7fffffff, group = hq / hk, round = 2 * kNumCUs;
-    if (batch * hq > limit) return false;
+    if (batch * hq > limit || pcap > kPrefixMost) return false;
     p = PrefixPlan{};
-    pcap = std::min(pcap, limit);                            // no length is larger
-    cap = std::min(cap, limit);
+    cap = std::min(cap, limit);                              // no length is larger
     const int64_t used = std::min(prefixes, batch);          // prefixes with a sequence, at most
     p.pshare = 1;
     p.few = batch * group <= 16 * used;
@@ -714,6 +714,7 @@ bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t h
     p.splits = std::max(p.share, cdiv(cap, kPrefixOwn));
     if (pairs > limit / p.share || pairs * p.share + p.pblocks > limit) return false;
     p.blocks = p.pblocks + pairs * p.share;
+    if ((double)batch * hq * (p.psplits + p.splits) * (head_dim + 2) > 0x1p60) return false;
     p.bytes = batch * hq * (p.psplits + p.splits) * (head_dim + 2) * 4;
     return true;
 }

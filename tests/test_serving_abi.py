@@ -91,6 +91,9 @@ def test_prefix_workspace():
                 (5, 8, 2, 128, 2, 200, -1, 16), (5, 8, 2, 128, 2, 200, 63, 12), (1 << 20, 65536, 1, 256, 1, 1 << 30, 1 << 30, 1),
                 (1 << 20, 4096, 4096, 256, 1 << 20, 1 << 25, 1 << 25, 32768)):
         assert ck.ck_shared_prefix_attention_workspace(*bad) == -1, bad
+    # a prefix of up to 2^30 tokens
+    assert ck.ck_shared_prefix_attention_workspace(5, 8, 2, 128, 2, 1 << 15, 63, 1 << 15) >= 0
+    assert ck.ck_shared_prefix_attention_workspace(5, 8, 2, 128, 2, (1 << 15) + 1, 63, 1 << 15) == -1
     # more prefixes than sequences, widths of nothing
     for fine in ((1, 8, 2, 128, 100, 3, 3, 16), (5, 8, 2, 128, 0, 0, 63, 16), (5, 8, 2, 128, 2, 0, 0, 16), (0, 8, 2, 64, 0, 0, 0, 1)):
         assert ck.ck_shared_prefix_attention_workspace(*fine) >= 0, fine
