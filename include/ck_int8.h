@@ -644,10 +644,10 @@ ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
  *   out[b, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b, h] . k_j - m),
  * m the largest score, over the tokens j of sequence b: those of its prefix,
  * if it has one, then its own.  Scores, exponentials and sums are fp32, the
- * products on the matrix cores with p_j in two 16-bit parts: they hold it to
- * 2^-17 of itself (a bf16 or int8 cache), or to 2^-23 of itself or 2^-50 of the
- * largest (fp16); ck_paged_attention takes more parts.  A sequence without any
- * token gives zeros.
+ * products on the matrix cores with p_j in 16-bit parts: three of bf16, which
+ * hold it to 2^-24 of itself (a bf16 or int8 cache), or two of fp16, 2^-23 of
+ * itself or 2^-50 of the largest (ck_paged_attention has four).  A sequence
+ * without any token gives zeros.
  *
  * q, cache, out     as in ck_paged_attention.
  * prefix_table [in] int32 [prefixes, prefix_width], rows prefix_table_stride

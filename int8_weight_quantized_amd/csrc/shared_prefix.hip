@@ -14,9 +14,10 @@
 //   - more rows: the waves split the rows, up to MB blocks of 16 each, and
 //     share tiles of K and V in LDS, one in use and one on its way, one barrier
 //     a tile.
-// A weight enters the value product in two 16-bit parts.  Of bf16 they hold it
-// to 2^-17 of itself.  The second part of fp16 is the rest that the first left,
-// 2^11 times finer, in sums of its own: 2^-23 of a weight or 2^-50 of the largest.
+// A weight enters the value product in 16-bit parts: three of bf16 (a bf16 or
+// int8 cache), which hold it to fp32's own 2^-24, or two of fp16, the second the
+// rest that the first left, 2^11 times finer, in sums of its own: 2^-23 of a
+// weight or 2^-50 of the largest.
 
 struct PrefixArgs {
     const uint16_t* q;
@@ -42,7 +43,13 @@ struct PrefixArgs {
     int few;                             // prefixes have up to 16 rows on average
 };
 
-constexpr int kPrefixParts = 2;          // 16-bit parts of a weight (128 sequences behind 65536 bf16 tokens: 421 us, with three 492)
+// 16-bit parts of a weight.  With two of bf16, 2^-17 of it, more outputs are not the
+// value nearest to the 64-bit result than of plain fp32 arithmetic, with three fewer
+// (0.25 %, 0.21 % and 0.11 % of 128 sequences behind 65536 bf16 tokens, 0.22 %, 0.11 %
+// and 0.04 % of 48 behind three int8 prefixes), in 400 and 477 us, 48 and 51 us.  Of fp16
+// two do (0.37 % of 24 behind 20000, 0.39 % with four, 1.25 % of fp32; 39 and 47 us).
+template <int DT, bool I8>
+constexpr int kPrefixParts = I8 || DT != CK_DT_FP16 ? 3 : 2;
 constexpr int kPrefixMost = 1 << 30;     // a prefix's tokens
 constexpr int kPrefixOwn = 512;          // a sequence's own tokens in a chunk, at most
 constexpr int kPrefixSeg = 512;          // tokens whose row offsets are made at a time
@@ -283,7 +290,7 @@ __device__ __forceinline__ void prefix_walk(const PrefixArgs& a, const PrefixWor
 {
     constexpr int RB = D * (I8 ? 1 : 2);
     using Sh = AttnShape<RB>;
-    using Kind = AttnKind<DT, I8, kPrefixParts>;
+    using Kind = AttnKind<DT, I8, kPrefixParts<DT, I8>>;
     constexpr int NW = PrefixShape<RB>::walkers, NL = Sh::loads, DB = D / 16, NA = Kind::NA;
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));                            // nothing that follows from it is kept from chunk to chunk: registers are short
@@ -339,7 +346,7 @@ __device__ __forceinline__ void prefix_walk(const PrefixArgs& a, const PrefixWor
         for (int t = wave; t < tiles; t += NW) {
             const bool more = t + NW < tiles;
             wait_vmcnt<NL>();                                // K of this tile; V came after it
-            attn_tile<DT, I8, D, 1, kPrefixParts, false>(
+            attn_tile<DT, I8, D, 1, kPrefixParts<DT, I8>, false>(
                 at, 0, qf, sc, &sh.kscale[I8 ? t * kAttnTile : 0], &sh.vscale[I8 ? t * kAttnTile : 0], ve,
                 w.n - t * kAttnTile, t == wave, M, L, acc,
                 [&] {
@@ -407,7 +414,7 @@ __device__ __forceinline__ void prefix_share(const PrefixArgs& a, const PrefixWo
 {
     constexpr int RB = D * (I8 ? 1 : 2), T = PrefixShape<RB>::tile;
     using Sh = AttnShape<RB>;
-    using Kind = AttnKind<DT, I8, kPrefixParts>;
+    using Kind = AttnKind<DT, I8, kPrefixParts<DT, I8>>;
     constexpr int DB = D / 16, NA = Kind::NA, LT = T * RB / 1024;    // 1 KiB loads of a tile's K
     constexpr int NL = (LT + 3) / 4;                         // and of those a wave's
     constexpr int TS = kPrefixSeg / T;                       // tiles of a segment
@@ -489,9 +496,9 @@ __device__ __forceinline__ void prefix_share(const PrefixArgs& a, const PrefixWo
         for (int u = 0; u < T / kAttnTile; ++u) {
             const int limit = w.n - t * T - u * kAttnTile, from = t % (2 * TS) * T + u * kAttnTile;
             if (limit <= 0) break;
-            attn_tile<DT, I8, D, MB, kPrefixParts, true>(at, place + u * (kAttnTile * RB), qf, sc, &sh.kscale[I8 ? from : 0],
-                                                         &sh.vscale[I8 ? from : 0], ve, limit, t + u == 0, M, L, acc,
-                                                         [] {}, [] {}, [] {});
+            attn_tile<DT, I8, D, MB, kPrefixParts<DT, I8>, true>(at, place + u * (kAttnTile * RB), qf, sc,
+                                                                 &sh.kscale[I8 ? from : 0], &sh.vscale[I8 ? from : 0], ve,
+                                                                 limit, t + u == 0, M, L, acc, [] {}, [] {}, [] {});
         }
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
     };
