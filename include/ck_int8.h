@@ -646,7 +646,7 @@ ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream);
  * if it has one, then its own.  Scores, exponentials and sums are fp32, the
  * products on the matrix cores with p_j in 16-bit parts: three of bf16, which
  * hold it to 2^-24 of itself (a bf16 or int8 cache), or two of fp16, 2^-23 of
- * itself or 2^-50 of the largest (ck_paged_attention has four).  A sequence
+ * itself or 2^-42 of the largest (ck_paged_attention has four).  A sequence
  * without any token gives zeros.
  *
  * q, cache, out     as in ck_paged_attention.
@@ -703,7 +703,7 @@ int64_t ck_shared_prefix_attention_workspace(int64_t batch, int64_t hq, int64_t 
  *   v[r] = sum_c x[i, c] a[t, r, c],  t = ids[i];
  * out[i] = y[i], bit for bit, for an id outside [0, adapters) (-1, say).
  * v and all sums are fp32; v enters the second product in 16-bit parts, which
- * hold it to 2^-24 of itself (bf16), or to 2^-22 of itself or 2^-39 of the row's
+ * hold it to 2^-24 of itself (bf16), or to 2^-22 of itself or 2^-38 of the row's
  * largest (fp16).  The a and b of an adapter that a row asks for must be finite
  * (an infinite value can give NaN in place of infinity); x and y may be anything,
  * and reach their own row only.

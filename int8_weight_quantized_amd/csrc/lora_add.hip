@@ -4,7 +4,7 @@
 // then out[i] = y[i] + (s_t v) B_t^T.  Both products run on the matrix cores
 // (16 x 16 x 32) with fp32 sums.  v stays 32 bits: it enters the second product
 // in 16-bit parts, three of bf16 (2^-24 of it), or two of fp16 after a power of
-// two that brings the row's largest to [2^13, 2^14) (2^-22 of it, or 2^-39 of the
+// two that brings the row's largest to [2^13, 2^14) (2^-22 of it, or 2^-38 of the
 // largest).
 //
 // Bound: HBM, by the adapters that a decode batch asks for or by y of a

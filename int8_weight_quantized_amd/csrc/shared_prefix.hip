@@ -17,7 +17,8 @@
 // A weight enters the value product in 16-bit parts: three of bf16 (a bf16 or
 // int8 cache), which hold it to fp32's own 2^-24, or two of fp16, the second the
 // rest that the first left, 2^11 times finer, in sums of its own: 2^-23 of a
-// weight or 2^-50 of the largest.
+// weight or 2^-42 of the largest (2^-25 of 2^11 times what is left, beside weights of
+// which the largest is 2^6 at least).
 
 struct PrefixArgs {
     const uint16_t* q;

@@ -59,3 +59,52 @@ def test_prefix_weights_to_32_bits(cache, dtype, members, hq, d, own):
     want = weight @ values / (2 + e[:, None])
     slack = 24 * ref.U32 * (weight @ values.abs()) / (2 + e[:, None])
     ref.assert_within(out.view(rows, d), want, slack, "almost nothing")
+
+
+@pytest.mark.parametrize("members", [2, 20])
+@pytest.mark.parametrize("up", [27.3, 33.3, 37.3, 39.3, 40.3])
+def test_prefix_lightest_fp16_weights(members, up):
+    """What is held of weights far below the largest in an fp16 cache: 2^-23 of a weight or 2^-42 of the largest.
+
+    One token of value 0 has weight 1, 4095 others the weight 2^-up and the value 2^15, whose sum is the output (at
+    least 2^-13 here).  Beside the weights' parts the score's offset, of at most 48, is rounded (2^-24 of it, twice with its
+    scale), the exponential is off by 2 units and the sums by 4096 + 8."""
+    dev = cuda_device()
+    n, page, d = 4096, 64, 64
+    k, v = torch.zeros((n // page, 1, page, d)), torch.full((n // page, 1, page, d), 2.0 ** 15)
+    k[0, 0, 5, 0], v[0, 0, 5] = 1, 0
+    c = ck.KVCache(k.half().to(dev), v.half().to(dev))
+    q = torch.zeros((members, 4, d), dtype=torch.float16)
+    q[:, :, 0] = up
+    x = q[0, 0, 0].double().item()
+    table = torch.zeros((members, 1), dtype=torch.int32, device=dev)
+    pages = torch.arange(n // page, dtype=torch.int32, device=dev)[None]
+    out = ck.shared_prefix_attention(q.to(dev), c, pages, i32(n), i32(0, members), table, torch.zeros_like(table[:, 0]), math.log(2.0))
+    light = 2.0 ** -x
+    want = torch.full(out.shape, (n - 1) * light * 2.0 ** 15 / (1 + (n - 1) * light), dtype=torch.float64)
+    held = (n - 1) * 2.0 ** 15 * max(2.0 ** -23 * light, 2.0 ** -42)
+    ref.assert_within(out, want, held + (2 * 48 + 2 + 4096 + 8) * ref.U32 * want, f"2^-{x}")
+
+
+# -------------------------------------------------------------------- lora_add
+
+@pytest.mark.parametrize("m", [1, 17, 70, 600])
+@pytest.mark.parametrize("rank", [8, 32, 64, 256])
+def test_lora_fp16_small_ranks_beside_a_large_one(m, rank):
+    """v of a rank far below the row's largest is held to 2^-38 of that: rank 0 has v = 1 (2^13 after the power of two
+    that the row is multiplied by, its lowest place), the others 2^-20 to 2^-36, each with a column of b of its own.
+    v itself is exact, and so are the product with b = 1 and the sum."""
+    dev = cuda_device()
+    g = torch.Generator().manual_seed(rank)
+    x, a = torch.zeros((m, 16)), torch.zeros((1, rank, 16))
+    x[:, 0], x[:, 9] = 1.0, 2.0 ** -13
+    a[0, 0, 0] = 1
+    a[0, 1:, 9] = (1 + torch.rand(rank - 1, generator=g)) * 2.0 ** (-7 - torch.arange(rank - 1) % 17).float()
+    a = a.half()
+    b = torch.eye(rank).view(1, rank, rank).half()
+    w = ck.LoraWeight(a.to(dev), b.to(dev))
+    got = ck.lora_add(torch.zeros((m, rank), device=dev), x.half().to(dev), w, torch.zeros(m, dtype=torch.int32, device=dev)).cpu().double()
+    want = a[0, :, 9].double() * 2.0 ** -13
+    want[0] = 1
+    assert ((got - want).abs() <= torch.maximum(torch.tensor(2.0 ** -38, dtype=torch.float64), 2.0 ** -22 * want)).all()
+    assert (got[:, 0] == 1).all()
