@@ -108,3 +108,30 @@ def test_lora_fp16_small_ranks_beside_a_large_one(m, rank):
     want[0] = 1
     assert ((got - want).abs() <= torch.maximum(torch.tensor(2.0 ** -38, dtype=torch.float64), 2.0 ** -22 * want)).all()
     assert (got[:, 0] == 1).all()
+
+
+# -------------------------------------------------------------- token_logprobs
+
+@pytest.mark.parametrize("top", [0, 5])
+@pytest.mark.parametrize("vocab", [3001, 20000, 60000])
+def test_logprobs_are_not_off_to_one_side(vocab, top):
+    """The mean error of 256 rows: what all terms share does not average out.
+
+    One logit is 0, the others about -log(vocab) - 1.6: the sum is about 1.2.  A change to base 2 by a factor that is r
+    too small makes every e^d too large by r |d| of it: a log probability by r sum p |d|, the entropy by about r sum p d^2.
+    With one fp32 constant for log2(e), r is 1.3e-8.  Allowed is a third of that, and what the rows' own errors leave in
+    the mean: the lane that has the largest logit adds its other terms to 1, up to 16 times, each sum off by 2^-24 at
+    most and evenly, so by 4 2^-24 / sqrt(3) as a standard deviation, a 16th of that in the mean of 256, three of those.
+    That is as much as r does to a log probability.  The entropy log S - W / S, W = sum e^d d, shows r alone: of a relative
+    error of S it takes 1 - |W| / S, here from -0.7 to -1.3 times, and r makes 2e-7 of it or more."""
+    g = torch.Generator().manual_seed(vocab)
+    x = torch.randn((256, vocab), generator=g) * 0.5 - (math.log(vocab) + 1.6)
+    x[:, 7] = 0
+    tokens = torch.full((256,), 7, dtype=torch.int64, device=cuda_device())
+    r = ck.token_logprobs(x.to(cuda_device()), tokens, top)
+    d = x.double()
+    p = torch.softmax(d, -1)
+    want, entropy = torch.log(p[:, 7]), -(p * torch.log(p)).sum(-1)
+    third, noise = 1.3e-8 / 3, 3 * 4 * ref.U32 / math.sqrt(3) / 16
+    assert abs((r.logprob.cpu().double() - want).mean()) <= third * (p * d.abs()).sum(-1).mean() + noise
+    assert abs((r.entropy.cpu().double() - entropy).mean()) <= third * (p * d * d).sum(-1).mean() + 1.3 * noise
