@@ -35,6 +35,9 @@ int ilog2(int64_t v)
     return l;
 }
 
+// Whether a launch takes so many blocks: fewer than 2^32 threads in all.
+bool grid_ok(int64_t blocks, int64_t threads) { return blocks <= 0xffffffffLL / threads; }
+
 // 16-bit rows of a [tokens, heads, head_dim] tensor that start 16 bytes apart
 // (the stride of a dimension with one element is not looked at).
 bool rows16(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t hs)

@@ -666,7 +666,7 @@ extern "C" ck_status ck_int4_pack(const uint8_t* codes, int64_t ldc, const uint1
         return fail(CK_ERR_UNSUPPORTED, "misaligned scales, w, w_scale or w_zero");
     Int4PackArgs a{codes, scales, zeros, (uint32_t*)w, w_scale, w_zero, ldc, lds, ldz, n, k, cdiv(k, 128), groups};
     const int64_t blocks = cdiv(n, 16) * a.chunks;           // 256 words a block; 16 scales a group fit
-    if (blocks > 0x7fffffffLL) return fail(CK_ERR_UNSUPPORTED, "too many blocks");
+    if (!grid_ok(blocks, 256)) return fail(CK_ERR_UNSUPPORTED, "too many blocks");
     if ((s = check_device()) != CK_OK) return s;
     void* kargs[] = {&a};
     s = launch(reinterpret_cast<const void*>(&int4_pack_kernel), (unsigned)blocks, 256, kargs, stream, "int4_pack");
@@ -701,7 +701,7 @@ extern "C" ck_status ck_int4_linear(const ck_int4_args* args, hipStream_t stream
         return fail(CK_ERR_UNSUPPORTED, "rows of x too long for 32-bit offsets");
     const Int4Plan plan = int4_plan(p.dtype, p.w_zero != nullptr, p.m, p.n, cdiv(p.k, 128), p.group);
     const int64_t bx = cdiv(cdiv(p.n, 16), plan.tiles), by = cdiv(p.m, plan.rows);
-    if (by > 65535) return fail(CK_ERR_UNSUPPORTED, "too many rows");
+    if (by > 65535 || !grid_ok(bx, 64 * plan.waves)) return fail(CK_ERR_UNSUPPORTED, "too many rows or columns");
     if ((s = check_device()) != CK_OK) return s;
     Int4Args a{(const uint16_t*)p.x, p.w, p.w_scale, p.w_zero, p.bias, p.out, p.ldx, p.ldo, p.m, p.n, p.k,
                cdiv(p.k, 128), cdiv(p.k, p.group), p.out_dtype};

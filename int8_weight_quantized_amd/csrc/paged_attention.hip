@@ -840,6 +840,7 @@ bool attn_plan(AttnPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_
     p.splits = std::max<int64_t>(1, cdiv(most, p.chunk));
     if (batch * hq > limit || pairs > limit / p.splits) return false;
     p.blocks = pairs * p.splits;
+    if (!grid_ok(p.blocks, 64 * attn_waves(row_bytes)) || (p.splits > 1 && !grid_ok(batch * hq, 256))) return false;
     p.bytes = p.splits > 1 ? batch * hq * p.splits * (head_dim + 2) * 4 : 0;
     return true;
 }
@@ -871,7 +872,7 @@ const void* attention_join_fn(int64_t d)
 }  // namespace
 
 // The layout does not tell the element type of the cache, so the size is the
-// larger of the two chunk rules'.
+// larger of the two chunk rules', of those that a launch takes.
 extern "C" int64_t ck_paged_attention_workspace(int64_t batch, int64_t hq, int64_t hk, int64_t head_dim,
                                                 int64_t table_width, int64_t page_size, int64_t window,
                                                 int64_t sinks)
@@ -881,11 +882,10 @@ extern "C" int64_t ck_paged_attention_workspace(int64_t batch, int64_t hq, int64
         !attention_sizes_ok(batch, hq, hk, table_width, page_size))
         return -1;
     const int64_t most = most_visible(table_width, page_size, window, sinks);
-    int64_t bytes = 0;
+    int64_t bytes = -1;
     for (int esz = 1; esz <= 2; ++esz) {
         AttnPlan plan;
-        if (!attn_plan(plan, batch, hq, hk, head_dim, esz * head_dim, most)) return -1;
-        bytes = std::max(bytes, plan.bytes);
+        if (attn_plan(plan, batch, hq, hk, head_dim, esz * head_dim, most)) bytes = std::max(bytes, plan.bytes);
     }
     return bytes;
 }

@@ -340,7 +340,7 @@ extern "C" ck_status ck_qk_norm_rope(const ck_qk_args* args, const ck_kv_cache* 
     const int64_t slices = std::min(heads, std::max(cdiv(heads, 8), cdiv(32 * kNumCUs * 64, lanes * p.tokens)));
     const bool many = slices < heads;
     const int64_t blocks = cdiv(p.tokens * slices, 256 / lanes);
-    if (blocks > 0x7fffffffLL) return fail(CK_ERR_UNSUPPORTED, "too many heads in all");
+    if (!grid_ok(blocks, 256)) return fail(CK_ERR_UNSUPPORTED, "too many heads in all");
     if ((s = check_device()) != CK_OK) return s;
 
     QkArgs a{};

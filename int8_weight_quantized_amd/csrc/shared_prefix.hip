@@ -722,6 +722,7 @@ bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t h
     p.splits = std::max(p.share, cdiv(cap, kPrefixOwn));
     if (pairs > limit / p.share || pairs * p.share + p.pblocks > limit) return false;
     p.blocks = p.pblocks + pairs * p.share;
+    if (!grid_ok(p.blocks, 256) || !grid_ok(cdiv(batch * hq, 4), 256)) return false;
     if ((double)batch * hq * (p.psplits + p.splits) * (head_dim + 2) > 0x1p60) return false;
     p.bytes = batch * hq * (p.psplits + p.splits) * (head_dim + 2) * 4;
     return true;

@@ -438,6 +438,7 @@ constexpr int64_t kLogprobWide = 32768;  // logits of a row for one block of 16 
 
 struct LogprobPlan {
     int64_t waves, splits, bytes;
+    bool fits;                                               // into a launch
 };
 
 // Rows of 4097 to 32768 logits, at most one a CU: 16 waves each, one launch (us
@@ -447,11 +448,12 @@ struct LogprobPlan {
 // few that their lists can be ranked by counting.
 LogprobPlan logprob_plan(int64_t rows, int64_t vocab, int64_t top)
 {
-    LogprobPlan p{4, 1, 0};
+    LogprobPlan p{4, 1, 0, false};
     if (rows <= kNumCUs && vocab > 4096 && vocab <= kLogprobWide) p.waves = 16;
     else if (rows > 0) p.splits = std::min(std::min<int64_t>(2 * kNumCUs / rows, cdiv(vocab, 4096)), kLogprobKeys / std::max<int64_t>(top, 16));
     p.splits = std::max<int64_t>(p.splits, 1);
     if (p.splits > 1) p.bytes = rows * p.splits * (16 + 8 * top + 4);
+    p.fits = grid_ok(rows, p.splits * p.waves * 64);
     return p;
 }
 
@@ -468,8 +470,9 @@ const void* logprob_fn(bool top, bool wide)
 
 extern "C" int64_t ck_token_logprobs_workspace(int64_t rows, int64_t vocab, int64_t top)
 {
-    return rows < 0 || vocab < 1 || vocab > 0x7fffffff || top < 0 || top > kLogprobTop || top > vocab ? -1
-           : logprob_plan(rows, vocab, top).bytes;
+    if (rows < 0 || vocab < 1 || vocab > 0x7fffffff || top < 0 || top > kLogprobTop || top > vocab) return -1;
+    const LogprobPlan plan = logprob_plan(rows, vocab, top);
+    return plan.fits ? plan.bytes : -1;
 }
 
 extern "C" ck_status ck_token_logprobs(const ck_logprob_args* args, hipStream_t stream)
@@ -490,10 +493,10 @@ extern "C" ck_status ck_token_logprobs(const ck_logprob_args* args, hipStream_t 
         !aligned(p.logprob, 4) || !aligned(p.entropy, 4) || !aligned(p.top_logprobs, 4))
         return fail(CK_ERR_UNSUPPORTED, "misaligned logits, tokens or outputs");
     const LogprobPlan plan = logprob_plan(p.rows, p.vocab, p.top);
+    if (!plan.fits) return fail(CK_ERR_UNSUPPORTED, "too many rows");
     if (plan.bytes > 0 && (!p.workspace || p.workspace_bytes < plan.bytes))
         return fail(CK_ERR_INVALID_ARG, "the workspace needs %lld bytes", (long long)plan.bytes);
     if (!aligned(p.workspace, 256)) return fail(CK_ERR_UNSUPPORTED, "misaligned workspace");
-    if (p.rows * plan.splits > 0x7fffffff) return fail(CK_ERR_UNSUPPORTED, "too many rows");
     ck_status s = check_device();
     if (s != CK_OK) return s;
     LogprobArgs a{p.logits, p.tokens, p.logprob, p.entropy, p.top_ids, p.top_logprobs, (double2*)p.workspace, nullptr, nullptr,
