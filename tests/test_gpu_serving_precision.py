@@ -88,6 +88,63 @@ def test_prefix_lightest_fp16_weights(members, up):
 
 # -------------------------------------------------------------------- lora_add
 
+@pytest.mark.parametrize("m", [1, 3, 17, 70, 600])
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128, 256])
+def test_lora_bf16_holds_24_bits_of_v(m, rank):
+    """Ranks that cancel: what is left are the last 8 of 22 to 23 bits of v, exactly.
+
+    Rank 2 i has v = p + c 2^-8, p of 14 or 15 bits (a product of a 7- and an 8-bit number) and c an odd number of 8, rank
+    2 i + 1 v = p and b the opposite: the output is c 2^-8.  Three parts of bf16 hold these bits, two hold 17 of them and
+    never c's last one.  Each column of b has one such pair, so all sums are whole multiples of 2^-8 below 2^24 of them,
+    which fp32 holds in any order."""
+    dev = cuda_device()
+    pairs, adapters, g = rank // 2, 3, torch.Generator().manual_seed(rank)
+    odd = lambda lo, hi, *s: torch.randint(lo // 2, hi // 2, s, generator=g) * 2.0 + 1  # noqa: E731
+    x, a = torch.zeros((m, 16)), torch.zeros((adapters, rank, 16))
+    x[:, 0], x[:, 9] = odd(64, 128, m), 2.0 ** -8
+    a[:, ::2, 0] = odd(128, 256, adapters, pairs)
+    a[:, 1::2, 0] = a[:, ::2, 0]
+    a[:, ::2, 9] = odd(128, 256, adapters, pairs)
+    b = torch.zeros((adapters, pairs, rank))
+    for i in range(pairs):
+        b[:, i, 2 * i], b[:, i, 2 * i + 1] = 1, -1
+    ids = torch.arange(m) % (adapters + 1) - 1
+    want = torch.zeros((m, pairs))
+    for i, t in enumerate(ids.tolist()):
+        if t >= 0:
+            want[i] = a[t, ::2, 9] * 2.0 ** -8
+    w = ck.LoraWeight(a.bfloat16().to(dev), b.bfloat16().to(dev))
+    got = ck.lora_add(torch.zeros((m, pairs), device=dev), x.bfloat16().to(dev), w, ids.int().to(dev))
+    assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("m", [1, 3, 17, 70, 600])
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128, 256])
+def test_lora_fp16_holds_22_bits_of_v(m, rank):
+    """As above with v = p, a product of two 11-bit numbers with 21 or 22 bits, and v = h, p's leading bits: p - h is exact.
+    (One part of fp16 holds 11 bits.)"""
+    dev = cuda_device()
+    pairs, adapters, g = rank // 2, 3, torch.Generator().manual_seed(rank)
+    odd = lambda *s: torch.randint(512, 1024, s, generator=g) * 2.0 + 1  # noqa: E731
+    x, a = torch.zeros((m, 16)), torch.zeros((adapters, rank, 16))
+    x[:, 0] = odd(1)                     # (of all rows: h goes by the product)
+    a[:, ::2, 0] = odd(adapters, pairs)
+    p = x[0, 0] * a[:, ::2, 0]
+    h = torch.floor(p / 2048)            # below 2^11, to be multiplied by 2048
+    x[:, 9], a[:, 1::2, 9] = 2048.0, h
+    b = torch.zeros((adapters, pairs, rank))
+    for i in range(pairs):
+        b[:, i, 2 * i], b[:, i, 2 * i + 1] = 1, -1
+    ids = torch.arange(m) % (adapters + 1) - 1
+    want = torch.zeros((m, pairs))
+    for i, t in enumerate(ids.tolist()):
+        if t >= 0:
+            want[i] = p[t] - h[t] * 2048
+    w = ck.LoraWeight(a.half().to(dev), b.half().to(dev))
+    got = ck.lora_add(torch.zeros((m, pairs), device=dev), x.half().to(dev), w, ids.int().to(dev))
+    assert torch.equal(got.cpu(), want)
+
+
 @pytest.mark.parametrize("m", [1, 17, 70, 600])
 @pytest.mark.parametrize("rank", [8, 32, 64, 256])
 def test_lora_fp16_small_ranks_beside_a_large_one(m, rank):
