@@ -178,8 +178,9 @@ def lora_add(y, x, weight, ids, out=None, workspace=None):
     y [m, n], what a shared projection made of x: bf16, fp16 or fp32 (one
     rounding).  x [m, k] of the adapters' type; ids int32 [m], the adapter of
     each row, in any order; -1 (or any number outside the adapters) leaves
-    the row as it is.  out: y itself to work in place.  workspace: from
-    lora_add_workspace; allocated here when None.  -> [m, n]."""
+    the row as it is.  out: y itself to work in place, but not x, whose rows
+    are read while others are written.  workspace: from lora_add_workspace;
+    allocated here when None.  -> [m, n]."""
     torch = _torch or _load_torch()
     try:
         tt, dev, (m, n), ys, (rows, k), xs = y.dtype, y.device, y.shape, y.stride(), x.shape, x.stride()
@@ -196,8 +197,11 @@ def lora_add(y, x, weight, ids, out=None, workspace=None):
     if workspace is None:
         workspace = lora_add_workspace(x, weight)
     wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    args = _LORA.pack(x.data_ptr(), weight.a_ptr, weight.b_ptr, weight.s_ptr, ids.data_ptr(), y.data_ptr(),
-                      out.data_ptr(), wp, wn, xs[0], ys[0], out.stride(0), weight.a_stride, weight.b_stride, m, n, k,
+    xp, op = x.data_ptr(), out.data_ptr()
+    if xp == op and m and n and k:
+        raise ValueError("out must not be x")
+    args = _LORA.pack(xp, weight.a_ptr, weight.b_ptr, weight.s_ptr, ids.data_ptr(), y.data_ptr(),
+                      op, wp, wn, xs[0], ys[0], out.stride(0), weight.a_stride, weight.b_stride, m, n, k,
                       weight.rank, weight.adapters, weight.code, _code[tt])
     _decode._launch(_ck.ck_lora_add, dev.index, args)
     return out

@@ -385,3 +385,15 @@ def test_launches_go_to_the_tensors_device(host, monkeypatch):
     ck.token_logprobs(y, torch.zeros(3, dtype=torch.int64), workspace=big)
     want = [ck.ck_shared_prefix_attention] * 2 + [ck.ck_lora_add] * 2 + [ck.ck_token_logprobs] * 2
     assert calls == [(f, None) for f in want]
+
+
+def test_lora_out_is_not_x(host):
+    """x is read while out is written: the same memory is refused, also where y is x; y itself as out is not."""
+    w = ck.LoraWeight(bf(4, 16, 64), bf(4, 64, 16))
+    x, y = bf(3, 64), bf(3, 64)
+    for args, kw in [((y, x), dict(out=x)), ((x, x), dict(out=x)), ((y, x), dict(out=x.view(3, 64)))]:
+        with pytest.raises(ValueError):
+            ck.lora_add(*args, w, i32(3), **kw)
+    for args, kw in [((y, x), dict(out=y)), ((x, x), dict()), ((x, x), dict(out=y))]:
+        with pytest.raises(host):
+            ck.lora_add(*args, w, i32(3), **kw)
