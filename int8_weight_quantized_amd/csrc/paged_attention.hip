@@ -13,10 +13,10 @@
 // rate.  Eight sequences of 32768 tokens, 8 key heads, both launches: bf16
 // heads of 128 194 us (5.5 TB/s; heads of 64 5.3, of 192 5.1, of 256 5.7),
 // int8 heads of 128 111 us (5.0; of 256 4.9).  48 sequences of up to 9001
-// tokens, 100000 in all, int8: 53 to 55 us (3.9 TB/s): the blocks that find
-// nothing to do leave at about 100 a us, and the last ones run alone.  A short
-// sequence is bound by latency, the chain lens -> table -> K -> V and the
-// join: one of 1000 tokens 6.6 us.
+// tokens, 100000 in all, int8: 52 to 57 us (3.9 TB/s; 43 where the Infinity Cache
+// holds them): the blocks that find nothing to do leave at about 100 a us, and the
+// last ones run alone.  A short sequence is bound by latency, the chain lens ->
+// table -> K -> V and the join: one of 1000 tokens 6.7 us.
 //
 // A block takes one sequence, one key head (up to 16 of its query heads,
 // one matrix tile) and a chunk of the visible tokens.  Its threads first
@@ -242,7 +242,7 @@ struct AttnLane {
 // registers for it; a wave in its products goes before one in its weights; and K
 // is read some pieces ahead of its products, which the compiler, short of
 // registers, does not do by itself (128 sequences behind 65536 tokens, 64/8 heads
-// of 128: 453 us, 421, 408 and 402).
+// of 128, with two parts of a weight: 453 us, 421, 408 and 402; 471 with three).
 template <int DT, bool I8, int D, int MB, int PARTS, bool FOLD, class KRead, class VReady, class VRead>
 __device__ __forceinline__ void attn_tile(const AttnLane<I8, D>& at, int off, const v4i (&qf)[MB][D / 32],
                                           const float (&sc)[MB], const float* kscale, const float* vscale, int ve,

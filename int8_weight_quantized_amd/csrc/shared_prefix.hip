@@ -674,22 +674,31 @@ struct PrefixPlan {
 // many there are, and a table may be far wider than any length.  So the host
 // chooses how many blocks share the tokens of a list, and they divide those that
 // there are, 128 at least each (48 sequences of 600 tokens behind prefixes of
-// 1000, in tables for 1024 tokens 29 us, for 131072 30 us, where chunks that
-// follow from the tables took 28 and 154).
+// 1000, in tables for 1024 tokens 30 us, for 131072 31 us, where chunks that
+// follow from the tables took 28 and 154, with two parts of a weight).
 //
 // A prefix's blocks are so many that all take the least time, if the table is
 // full, where a round of up to two blocks a CU takes as long as its chunk, a fixed
 // part and its rows' sums, which are written and read; up to one block a CU run
-// half as fast again.  (128 sequences behind 65536 tokens: 512 blocks 402 us, 256
-// blocks 602; 48 behind three int8 prefixes: 512 blocks 61 us, 256 blocks 56; 24
-// behind 20000 tokens at head_dim 256: 42 and 39.)  Where groups have up to 16
+// half as fast again.  (128 sequences behind 65536 tokens: 512 blocks 471 us, 256
+// blocks 670; 48 behind three int8 prefixes: 512 blocks 57 us, 256 blocks 51; 24
+// behind 20000 tokens at head_dim 256: 41.5 and 38.7.)  Where groups have up to 16
 // rows on average, those that have no more get chunks of 1024 tokens at most, which
 // the form for few rows takes, and a block goes through several.
 //
+// Uneven groups: the average decides, and a group's last row block may hold one
+// row, for which three of four waves stand by and the prefix is read once more.
+// (32/8 heads of 128, groups of 100, 2, 2 and 2 sequences behind 6000 tokens each 54
+// us, the first alone 47, the others alone 21, 26 or 27 each 58; 8/8 heads, one group
+// behind 20000: 128 rows 45 us, 129 rows 59, 192 rows 65.)
+//
 // All sequences have two blocks a CU, and their chunks 512 tokens at most (the
-// 48 sequences: 1024 tokens 56 us, 512 52, 256 55): they run beside the prefixes'
+// 48 sequences: 1024 and 512 tokens 51 us, 256 56): they run beside the prefixes'
 // long ones.  The first chunks of all come first, as they are the likeliest to
-// have tokens.
+// have tokens.  From 512 pairs of a sequence and a key head on each pair has one
+// block, which goes through a long sequence's chunks one after the other, whatever
+// the others' lengths: one of 60000 tokens among 127 of 100, 32/8 heads, 812 us
+// (among 31 567), where paged_attention takes 122 (61).
 bool prefix_plan(PrefixPlan& p, int64_t batch, int64_t hq, int64_t hk, int64_t head_dim, int64_t prefixes,
                  int64_t pcap, int64_t cap)
 {

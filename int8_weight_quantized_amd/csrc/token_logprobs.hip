@@ -8,7 +8,8 @@
 // S and W move to the new one by e^(m - m'), W' = (W + S (m - m')) e^(m - m').
 // So the largest logit's own term is 1 exactly, and the sums of lanes, waves
 // and chunks are joined in 64 bits: a log probability near zero keeps its
-// digits.  A masked logit has e^d = 0 and d = -inf: d is cut at -10^4 in W.
+// digits, but for the few terms of the largest's own lane, which are added to 1 in
+// fp32 (2^-24 at most for each).  A masked logit has e^d = 0 and d = -inf: d is cut at -10^4 in W.
 //
 // The alternatives, k of them, cost the pass over the logits nothing: of the
 // maxima of 256 lanes (or groups of four) the k-th is a bound that k logits reach, and those that do
